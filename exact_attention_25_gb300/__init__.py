@@ -7,7 +7,11 @@ pointers and sizes; ``forward``/``backward`` additionally allocate the outputs w
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
+import math
+from typing import NamedTuple
 
 from . import _lib
 from ._lib import FA_BF16, FA_F32, FaError, check, load
@@ -19,6 +23,9 @@ __all__ = [
     "backward_varlen", "fa_fwd_decode", "fa_decode_workspace_bytes", "fa_decode_num_splits",
     "forward_decode", "fa_checked_build", "fa_fwd_fp8", "fa_fwd_fp8_workspace_bytes",
     "forward_fp8", "fa_fwd_fp8_varlen", "fa_fwd_fp8_varlen_workspace_bytes", "forward_fp8_varlen",
+    "RopeTable", "rope_table", "fa_rope", "rope", "rope_backward", "PagedCache", "new_cache",
+    "fa_cache_append", "cache_append", "fa_cache_read", "cache_read", "fa_fwd_decode_cache",
+    "fa_decode_cache_num_splits", "forward_decode_cache",
 ]
 
 
@@ -416,4 +423,306 @@ def forward_decode(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max_s
     lse = torch.empty((H, total_q), dtype=torch.float32, device=q.device)
     fa_fwd_decode(q, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, scale,
                   causal, num_splits, ws, stream)
+    return o, lse
+
+
+# --------------------------------------------------------------------------- serving helpers
+
+def _same_device(*ts):
+    """The tensors' one CUDA device (its index); raises unless all lie on it."""
+    dev = ts[0].device
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError("tensors must lie on one device")
+    if dev.type != "cuda":
+        raise ValueError("tensors must be CUDA tensors")
+    return dev.index
+
+
+@contextlib.contextmanager
+def _switched(index, stream):
+    import torch
+
+    with torch.cuda.device(index):
+        if stream is None:
+            yield
+        else:
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _place(index, stream):
+    """Context for a call's allocations and launches: the tensors' device, and the stream the
+    call runs on (so that torch's allocator ties outputs and workspaces to it)."""
+    import torch
+
+    if stream is None and torch.cuda.current_device() == index:
+        return contextlib.nullcontext()
+    return _switched(index, stream)
+
+
+def _call(fn, index, stream, *args):
+    """One C call on the tensors' device and on ``stream`` (default: that device's current)."""
+    import torch
+
+    if torch.cuda.current_device() == index:
+        check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(index):
+            check(fn(*args, _stream(stream)))
+
+
+def _rows_strides(*ts):
+    """(row, head) element strides of [rows, heads, d] views, or None when all are contiguous."""
+    return None if all(t is None or t.is_contiguous() for t in ts) else _view_strides(*ts)
+
+
+def _view_strides(*ts):
+    vals = []
+    for t in ts:
+        if t is None:
+            vals += [0, 0]
+            continue
+        if t.dim() != 3 or t.stride(2) != 1:
+            raise ValueError("packed views need contiguous head dimensions (stride 1 in d)")
+        # a dimension of one row or head is never stepped over: any valid step will do
+        _, heads, d = t.shape
+        hs = t.stride(1) if heads > 1 else d
+        vals += [t.stride(0) if t.shape[0] > 1 else heads * hs, hs]
+    return (ctypes.c_longlong * len(vals))(*vals)
+
+
+def _int32(name, t, *shape):
+    if t.dtype != _torch_int32():
+        raise TypeError(f"{name} must be int32")
+    if not t.is_contiguous() or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be contiguous, of shape {list(shape)}")
+
+
+# --------------------------------------------------------------------------- rotary positions
+
+class RopeTable:
+    """Which angle each rotated pair of a head turns by: pair p by positions[axis[p]] *
+    inv_freq[p].  ``interleaved`` pairs are neighbours (2p, 2p + 1), else (p, pairs + p)."""
+
+    def __init__(self, d: int, inv_freq, axis, interleaved: bool = False):
+        self.d, self.interleaved = int(d), bool(interleaved)
+        self.inv_freq = tuple(float(x) for x in inv_freq)
+        self.axis = tuple(int(a) for a in axis)
+        self.pairs, self.axes = len(self.inv_freq), max(self.axis, default=-1) + 1
+        if len(self.axis) != self.pairs:
+            raise ValueError("inv_freq and axis must have one entry for each rotated pair")
+        self._freq = (ctypes.c_double * self.pairs)(*self.inv_freq)
+        self._axis = (ctypes.c_int * self.pairs)(*self.axis)
+
+
+@functools.lru_cache(maxsize=64)
+def rope_table(d: int, sections, base: float = 10000.0, per_axis: bool = False,
+               interleaved: bool = False) -> RopeTable:
+    """The table of a head of d elements whose first sum(sections) pairs turn, sections[a] of
+    them by axis a.  Frequencies run base^(-i / pairs) over all rotated pairs, or, per_axis,
+    base^(-i / sections[a]) afresh for each axis."""
+    pairs = sum(sections)
+    freq, axis = [], []
+    for a, n in enumerate(sections):
+        for i in range(n):
+            freq.append(math.pow(base, -i / n) if per_axis else math.pow(base, -len(freq) / pairs))
+            axis.append(a)
+    return RopeTable(d, freq, axis, interleaved)
+
+
+def fa_rope(q, k, q_out, k_out, positions, table: RopeTable, inverse: bool = False,
+            stream=None) -> None:
+    """C ``fa_rope``: q, q_out [total, H, d], k, k_out [total, Hkv, d] (or both None), bf16 or
+    fp32, contiguous or (row, head)-strided views; positions int32 [axes, total].  Outputs may
+    be their inputs."""
+    total, H, d = q.shape
+    ts = (q, k, q_out, k_out)
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out come together")
+    index = _same_device(q, k, q_out, k_out, positions)
+    Hkv = 0 if k is None else int(k.shape[1])
+    for t, heads in zip(ts, (H, Hkv, H, Hkv)):
+        if t is not None and (t.dtype != q.dtype or tuple(t.shape) != (total, heads, d)):
+            raise ValueError("q, k and their outputs must be [total, heads, d] of one dtype")
+    if table.d != d:
+        raise ValueError(f"the table is made for d = {table.d}")
+    if positions.dim() != 2:
+        raise ValueError("positions must be [axes, total]")
+    _int32("positions", positions, max(table.axes, int(positions.shape[0])), total)
+    _call(load().fa_rope, index, stream, _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out),
+          _ptr(positions), table._freq, table._axis, _rows_strides(*ts), total, H, Hkv, d,
+          int(positions.shape[0]), table.pairs, int(table.interleaved), int(bool(inverse)),
+          _dtype_code(q))
+
+
+def rope(q, k, positions, table: RopeTable, stream=None):
+    """Allocate and return q and k (None: only q) turned by their positions."""
+    return _rope(q, k, positions, table, False, stream)
+
+
+def rope_backward(dq, dk, positions, table: RopeTable, stream=None):
+    """The gradients of ``rope``'s inputs from those of its outputs."""
+    return _rope(dq, dk, positions, table, True, stream)
+
+
+def _rope(q, k, positions, table, inverse, stream):
+    import torch
+
+    with _place(_same_device(q), stream):
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=q.device)
+        fa_rope(q, k, q_out, k_out, positions, table, inverse, stream)
+    return q_out, k_out
+
+
+# --------------------------------------------------------------------------- the paged e4m3 cache
+
+class PagedCache(NamedTuple):
+    """The tensors of a paged cache: e4m3 codes [num_pages, Hkv, page_size, d] and one biased
+    exponent byte a row [num_pages, Hkv, page_size] (any 1-byte dtypes)."""
+    k: object
+    v: object
+    k_exp: object
+    v_exp: object
+
+
+def new_cache(num_pages: int, page_size: int, Hkv: int, d: int, device="cuda") -> PagedCache:
+    """A zeroed cache (code 0 under exponent byte 127, the value 0)."""
+    import torch
+
+    shape = (num_pages, Hkv, page_size)
+    k, v = (torch.zeros(shape + (d,), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+            for _ in range(2))
+    ke, ve = (torch.full(shape, 127, dtype=torch.uint8, device=device) for _ in range(2))
+    return PagedCache(k, v, ke, ve)
+
+
+def _cache_sizes(cache, page_table):
+    """(num_pages, Hkv, page_size, d, B, max_pages), the tensors checked against them."""
+    shape = tuple(cache.k.shape)
+    if len(shape) != 4 or tuple(cache.v.shape) != shape:
+        raise ValueError("the cache's codes must be [num_pages, Hkv, page_size, d]")
+    if tuple(cache.k_exp.shape) != shape[:3] or tuple(cache.v_exp.shape) != shape[:3]:
+        raise ValueError("the cache's exponents must be [num_pages, Hkv, page_size]")
+    for t in cache:
+        if t.element_size() != 1 or not t.is_contiguous():
+            raise ValueError("the cache's tensors must be contiguous, of 1-byte elements")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [B, max_pages]")
+    _int32("page_table", page_table, *page_table.shape)
+    return shape + tuple(page_table.shape)
+
+
+def fa_cache_append(cache: PagedCache, k, v, cu_seqlens_new, seqlens_k, page_table,
+                    max_seqlen_new: int, stream=None) -> None:
+    """C ``fa_cache_append``: quantises the new rows k, v [total_new, Hkv, d] (bf16 or fp32,
+    contiguous or strided) into the cache's pages; seqlens_k int32 [B] are the lengths after
+    the call."""
+    pages, Hkv, ps, d, B, max_pages = _cache_sizes(cache, page_table)
+    index = _same_device(*cache, k, v, cu_seqlens_new, seqlens_k, page_table)
+    _check_rows(k, v, Hkv, d)
+    _int32("cu_seqlens_new", cu_seqlens_new, B + 1)
+    _int32("seqlens_k", seqlens_k, B)
+    _call(load().fa_cache_append, index, stream, _ptr(k), _ptr(v), _rows_strides(k, v),
+          *map(_ptr, cache), _ptr(cu_seqlens_new), _ptr(seqlens_k), _ptr(page_table), B,
+          int(max_seqlen_new), int(k.shape[0]), max_pages, pages, ps, Hkv, d, _dtype_code(k))
+
+
+def _check_rows(k, v, Hkv, d):
+    if k.dim() != 3 or tuple(k.shape[1:]) != (Hkv, d) or v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must be [rows, Hkv, d] of one dtype")
+
+
+cache_append = fa_cache_append
+
+
+def fa_cache_read(cache: PagedCache, k, v, cu_seqlens_k, page_table, max_seqlen_k: int,
+                  stream=None) -> None:
+    """C ``fa_cache_read``: writes the cached rows of every sequence back to back into k, v
+    [total_k, Hkv, d] (bf16 or fp32, contiguous or strided)."""
+    pages, Hkv, ps, d, B, max_pages = _cache_sizes(cache, page_table)
+    index = _same_device(*cache, k, v, cu_seqlens_k, page_table)
+    _check_rows(k, v, Hkv, d)
+    _int32("cu_seqlens_k", cu_seqlens_k, B + 1)
+    _call(load().fa_cache_read, index, stream, *map(_ptr, cache), _ptr(k), _ptr(v),
+          _rows_strides(k, v), _ptr(cu_seqlens_k), _ptr(page_table), B, int(max_seqlen_k),
+          int(k.shape[0]), max_pages, pages, ps, Hkv, d, _dtype_code(k))
+
+
+def cache_read(cache: PagedCache, cu_seqlens_k, page_table, max_seqlen_k: int, total_k: int,
+               dtype=None, stream=None):
+    """Allocate K and V ([total_k, Hkv, d], bf16 unless dtype says otherwise) and run
+    fa_cache_read."""
+    import torch
+
+    _, Hkv, _, d = cache.k.shape
+    with _place(_same_device(cache.k), stream):
+        k, v = (torch.empty((total_k, Hkv, d), dtype=dtype or torch.bfloat16,
+                            device=cache.k.device) for _ in range(2))
+        fa_cache_read(cache, k, v, cu_seqlens_k, page_table, max_seqlen_k, stream)
+    return k, v
+
+
+def fa_decode_cache_num_splits(B: int, H: int, Hkv: int, max_seqlen_q: int,
+                               max_seqlen_k: int) -> int:
+    """C ``fa_decode_cache_num_splits``: a split count that fills this GPU."""
+    n = int(load().fa_decode_cache_num_splits(B, H, Hkv, max_seqlen_q, max_seqlen_k))
+    check(min(n, 0))
+    return n
+
+
+def fa_fwd_decode_cache(q, cache: PagedCache, o, lse, cu_seqlens_q, seqlens_k, page_table,
+                        max_seqlen_q: int, max_seqlen_k: int, scale: float, causal: bool,
+                        num_splits: int, workspace, stream=None) -> None:
+    """C ``fa_fwd_decode_cache``: q, o [total_q, H, d] bf16, lse [H, total_q] fp32 or None;
+    workspace (fa_decode_workspace_bytes) may be None for num_splits = 1."""
+    pages, Hkv, ps, d, B, max_pages = _cache_sizes(cache, page_table)
+    index = _same_device(q, *cache, o, lse, cu_seqlens_q, seqlens_k, page_table, workspace)
+    _check_decode_io(q, o, lse, d)
+    total_q, H, _ = q.shape
+    _int32("cu_seqlens_q", cu_seqlens_q, B + 1)
+    _int32("seqlens_k", seqlens_k, B)
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call(load().fa_fwd_decode_cache, index, stream, _ptr(q), *map(_ptr, cache), _ptr(o),
+          _ptr(lse), _ptr(cu_seqlens_q), _ptr(seqlens_k), _ptr(page_table), B, int(max_seqlen_q),
+          int(max_seqlen_k), total_q, max_pages, pages, ps, H, Hkv, d, float(scale),
+          int(bool(causal)), int(num_splits), _ptr(workspace), nbytes)
+
+
+def _check_decode_io(q, o, lse, d):
+    import torch
+
+    if q.dim() != 3 or q.shape[2] != d or o.shape != q.shape:
+        raise ValueError("q and o must be [total_q, H, d]")
+    if q.dtype != torch.bfloat16 or o.dtype != torch.bfloat16:
+        raise TypeError("q and o must be bfloat16")
+    if not q.is_contiguous() or not o.is_contiguous():
+        raise ValueError("q and o must be contiguous")
+    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous()
+                            or tuple(lse.shape) != (q.shape[1], q.shape[0])):
+        raise ValueError("lse must be contiguous fp32 [H, total_q]")
+
+
+def forward_decode_cache(q, cache: PagedCache, cu_seqlens_q, seqlens_k, page_table,
+                         max_seqlen_q: int, max_seqlen_k: int, scale: float | None = None,
+                         causal: bool = False, num_splits: int | None = None, stream=None):
+    """Allocate O, LSE (and the split workspace) and run fa_fwd_decode_cache."""
+    import torch
+
+    total_q, H, d = q.shape
+    if scale is None:
+        scale = d ** -0.5
+    dev = q.device
+    with _place(_same_device(q), stream):
+        if num_splits is None:
+            num_splits = fa_decode_cache_num_splits(int(page_table.shape[0]), H,
+                                                    int(cache.k.shape[1]), max_seqlen_q,
+                                                    max_seqlen_k)
+        nbytes = fa_decode_workspace_bytes(total_q, H, d, num_splits)
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+        o = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        lse = torch.empty((H, total_q), dtype=torch.float32, device=dev)
+        fa_fwd_decode_cache(q, cache, o, lse, cu_seqlens_q, seqlens_k, page_table, max_seqlen_q,
+                            max_seqlen_k, scale, causal, num_splits, ws, stream)
     return o, lse

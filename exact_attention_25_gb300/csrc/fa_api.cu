@@ -3,6 +3,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <climits>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -10,6 +11,7 @@
 
 #include "fa_common.cuh"
 #include "fa_decode.cuh"
+#include "fa_serve.cuh"
 
 namespace fa {
 cudaError_t launch_fwd_tc(int d, const CUtensorMap& tq, const CUtensorMap& tk,
@@ -30,6 +32,12 @@ cudaError_t launch_fwd_fp8_tc(const CUtensorMap& tq, const CUtensorMap& tk,
                               const CUtensorMap& tvt, const FwdParams& p, cudaStream_t st);
 cudaError_t launch_vt_transpose(const void* v, void* vt, const Layout& L, int Kpad, int* status,
                                 cudaStream_t st);
+cudaError_t launch_rope(int d, int is_f32, const RopeParams& p, int interleaved, cudaStream_t st,
+                        int num_sms);
+cudaError_t launch_cache_append(int d, int is_f32, const CacheParams& p, cudaStream_t st);
+cudaError_t launch_cache_read(int d, int is_f32, const CacheParams& p, cudaStream_t st);
+cudaError_t launch_decode_cache(int d, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const CacheDecodeParams& p, cudaStream_t st);
 
 // Device status word written by bounded waits that give up (0 = fine).
 __device__ int g_status_word;
@@ -1154,5 +1162,359 @@ extern "C" int fa_fwd_fp8_varlen(const void* q, const void* k, const void* v, vo
     if (e != cudaSuccess) return cuda_fail(e, "V transpose launch");
     e = fa::launch_fwd_fp8_tc(maps[0], maps[1], maps[2], p, st);
     if (e != cudaSuccess) return cuda_fail(e, "e4m3 forward launch");
+    return FA_OK;
+}
+
+// ---------------------------------------------------------------------------------------
+// Rotary positions (fa_rope).
+// ---------------------------------------------------------------------------------------
+namespace {
+
+// Turns per position, x / (2 pi), as a fraction of 2^64 (whole turns dropped).  The product is
+// taken in two doubles, so the fraction is good to about 2^-64 turns for |x| < 1.
+unsigned long long turn_fraction(double x)
+{
+    constexpr double kHi = 0.15915494309189535;       // 1 / (2 pi) in two doubles
+    constexpr double kLo = -9.839338337591243e-18;
+    if (x < 0) return 0ull - turn_fraction(-x);
+    const double hi = x * kHi;
+    const double lo = __builtin_fma(x, kHi, -hi) + x * kLo;
+    const double frac = hi - __builtin_floor(hi);  // exact
+    // 2^64 frac as 32 + 32 bits, then the low part (which may be negative: mod 2^64)
+    const double top = __builtin_floor(frac * 0x1p32);
+    const double rest = (frac * 0x1p32 - top) * 0x1p32 + lo * 0x1p64;
+    return (static_cast<unsigned long long>(top) << 32) +
+           static_cast<unsigned long long>(static_cast<long long>(__builtin_rint(rest)));
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// Row and head strides of packed tensors: contiguous, or `user` (n pairs) checked: positive
+// multiples of `unit` elements (16 bytes), heads not wider than their step, rows not shorter
+// than a head step.
+int packed_or_user_strides(const long long* user, int n, const int* heads, int d, int unit,
+                           long long* rs, long long* hs)
+{
+    for (int t = 0; t < n; ++t) {
+        rs[t] = static_cast<long long>(heads[t]) * d;
+        hs[t] = d;
+        if (!user || heads[t] == 0) continue;
+        rs[t] = user[2 * t];
+        hs[t] = user[2 * t + 1];
+        if (rs[t] <= 0 || hs[t] <= 0 || rs[t] % unit || hs[t] % unit)
+            return fail(FA_ERR_MISALIGNED, "strides must be positive multiples of 16 bytes");
+        if (hs[t] < d || rs[t] < hs[t])
+            return fail(FA_ERR_INVALID_ARG, "each head's d elements must fit within its head step, "
+                                            "and the head step within the row step");
+    }
+    return FA_OK;
+}
+
+long long rows_extent(long long rows, int heads, int d, long long rs, long long hs)
+{
+    const long long cut = (g_debug_flags & fa::kDebugShrinkExtents) ? rs : 0;
+    return (rows - 1) * rs + (heads - 1) * hs + d - cut;
+}
+
+}  // namespace
+
+extern "C" int fa_rope(const void* q, const void* k, void* q_out, void* k_out,
+                       const int* positions, const double* inv_freq, const int* axis,
+                       const long long* strides, int total, int H, int Hkv, int d, int axes,
+                       int pairs, int interleaved, int inverse, int dtype, void* stream)
+{
+    if (dtype != FA_BF16 && dtype != FA_F32) return fail(FA_ERR_INVALID_ARG, "dtype must be FA_BF16 or FA_F32");
+    if (total < 1 || H < 1 || Hkv < 0) return fail(FA_ERR_INVALID_ARG, "total and H must be >= 1, Hkv >= 0");
+    if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED_D, "d must be 64 or 128");
+    if (axes < 1 || axes > 8) return fail(FA_ERR_INVALID_ARG, "axes must be in [1, 8]");
+    if (pairs < 8 || pairs % 8 || 2 * pairs > d)
+        return fail(FA_ERR_INVALID_ARG, "pairs must be a multiple of 8, at most d / 2");
+    if ((interleaved != 0 && interleaved != 1) || (inverse != 0 && inverse != 1))
+        return fail(FA_ERR_INVALID_ARG, "interleaved and inverse must be 0 or 1");
+    if (!q || !q_out || (Hkv > 0 && (!k || !k_out)) || !positions || !inv_freq || !axis)
+        return fail(FA_ERR_INVALID_ARG, "q, q_out, positions, inv_freq and axis (and k, k_out where Hkv > 0) must be non-null");
+    for (int p = 0; p < pairs; ++p) {
+        if (axis[p] < 0 || axis[p] >= axes) return fail(FA_ERR_INVALID_ARG, "axis entries must be in [0, axes)");
+        if (!(inv_freq[p] >= -0x1p20 && inv_freq[p] <= 0x1p20))
+            return fail(FA_ERR_INVALID_ARG, "inv_freq entries must be finite, at most 2^20 in magnitude");
+    }
+    if (!aligned16(q) || !aligned16(q_out) || (Hkv > 0 && (!aligned16(k) || !aligned16(k_out))) ||
+        !aligned4(positions))
+        return fail(FA_ERR_MISALIGNED, "tensors must be 16-byte aligned (positions 4-byte)");
+    if (static_cast<long long>(total) * (H + static_cast<long long>(Hkv)) * d >= (1LL << 40))
+        return fail(FA_ERR_TOO_LARGE, "total*(H+Hkv)*d must be < 2^40");
+    const int es = dtype == FA_F32 ? 4 : 2;
+    const int heads[4] = {H, Hkv, H, Hkv};
+    long long rs[4], hs[4];
+    // strides come as (row, head) pairs of q, k, q_out, k_out
+    if (int rc = packed_or_user_strides(strides, 4, heads, d, 16 / es, rs, hs)) return rc;
+    if (!strides) {  // (strided views may interleave in one buffer: not checked)
+        const size_t tq = static_cast<size_t>(total) * H * d * es;
+        const size_t tk = static_cast<size_t>(total) * Hkv * d * es;
+        const Span pos{positions, static_cast<size_t>(axes) * total * 4};
+        const Span qi{q, tq}, ki{k, tk}, qo{q_out, tq}, ko{k_out, tk};
+        // each output may be its own input, and meets nothing else
+        if ((q != q_out && spans_meet(qi, qo)) || spans_meet(qo, pos) ||
+            (Hkv > 0 && ((k != k_out && spans_meet(ki, ko)) || spans_meet(qo, ki) ||
+                         spans_meet(ko, qi) || spans_meet(qo, ko) || spans_meet(ko, pos))))
+            return fail(FA_ERR_INVALID_ARG, "q_out and k_out must be their own inputs or overlap "
+                                            "neither an input nor one another");
+    }
+    DeviceInfo* di = nullptr;
+    if (int rc = device_info(&di)) return rc;
+    fa::RopeParams p{};
+    p.x[0] = q; p.x[1] = k; p.y[0] = q_out; p.y[1] = k_out;
+    for (int z = 0; z < 2; ++z) {
+        p.x_rs[z] = rs[z]; p.x_hs[z] = hs[z];
+        p.y_rs[z] = rs[2 + z]; p.y_hs[z] = hs[2 + z];
+        p.x_ext[z] = rows_extent(total, heads[z], d, rs[z], hs[z]);
+        p.y_ext[z] = rows_extent(total, heads[z], d, rs[2 + z], hs[2 + z]);
+    }
+    p.pos = positions;
+    p.pos_ext = static_cast<long long>(axes) * total;
+    p.total = total; p.H = H; p.Hkv = Hkv; p.pairs = pairs;
+    p.sign = inverse ? -1.0f : 1.0f;
+    p.status = di->status;
+    for (int i = 0; i < pairs; ++i) {
+        p.turn[i] = turn_fraction(inv_freq[i]);
+        p.axis[i] = static_cast<unsigned char>(axis[i]);
+    }
+    cudaError_t e = fa::launch_rope(d, dtype == FA_F32, p, interleaved, static_cast<cudaStream_t>(stream), di->sms);
+    if (e != cudaSuccess) return cuda_fail(e, "rope launch");
+    return FA_OK;
+}
+
+// ---------------------------------------------------------------------------------------
+// The paged e4m3 cache (fa_cache_append, fa_cache_read, fa_fwd_decode_cache).
+// ---------------------------------------------------------------------------------------
+namespace {
+
+// The cache's own arguments; *shift receives log2(page_size).
+int check_cache(const void* kc, const void* vc, const void* ke, const void* ve, const int* table,
+                int B, int max_pages, int num_pages, int page_size, int Hkv, int d, int* shift)
+{
+    if (d != 64 && d != 128) return fail(FA_ERR_UNSUPPORTED_D, "d must be 64 or 128");
+    if (B < 1 || Hkv < 1 || max_pages < 1 || num_pages < 1)
+        return fail(FA_ERR_INVALID_ARG, "B, Hkv, max_pages and num_pages must be >= 1");
+    if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)))
+        return fail(FA_ERR_INVALID_ARG, "page_size must be a power of two in [16, 1024]");
+    if (!kc || !vc || !ke || !ve || !table)
+        return fail(FA_ERR_INVALID_ARG, "the cache's tensors and page_table must be non-null");
+    if (!aligned16(kc) || !aligned16(vc) || !aligned16(ke) || !aligned16(ve) || !aligned4(table))
+        return fail(FA_ERR_MISALIGNED, "the cache's tensors must be 16-byte aligned (page_table 4-byte)");
+    if (static_cast<long long>(num_pages) * Hkv * page_size >= (1LL << 31))
+        return fail(FA_ERR_TOO_LARGE, "num_pages*Hkv*page_size must be < 2^31");
+    int s = 4;
+    while ((1 << s) < page_size) ++s;
+    *shift = s;
+    return FA_OK;
+}
+
+// What append and read share: packed rows k, v [total, Hkv, d] on one side, the cache on the other.
+int cache_rows_params(const void* k, const void* v, const long long* strides, void* kc, void* vc,
+                      void* ke, void* ve, const int* cu, const int* seqlens, const int* table,
+                      int B, int max_rows, int total, int max_pages, int num_pages, int page_size,
+                      int Hkv, int d, int dtype, fa::CacheParams* p)
+{
+    if (dtype != FA_BF16 && dtype != FA_F32) return fail(FA_ERR_INVALID_ARG, "dtype must be FA_BF16 or FA_F32");
+    int shift = 0;
+    if (int rc = check_cache(kc, vc, ke, ve, table, B, max_pages, num_pages, page_size, Hkv, d, &shift))
+        return rc;
+    if (total < 1 || max_rows < 1) return fail(FA_ERR_INVALID_ARG, "the number of rows and the longest sequence must be >= 1");
+    if (!k || !v || !cu) return fail(FA_ERR_INVALID_ARG, "k, v and cu_seqlens must be non-null");
+    if (!aligned16(k) || !aligned16(v) || !aligned4(cu))
+        return fail(FA_ERR_MISALIGNED, "k and v must be 16-byte aligned (cu_seqlens 4-byte)");
+    if (max_rows > total) max_rows = total;
+    const int heads[2] = {Hkv, Hkv};
+    long long rs[2], hs[2];
+    if (int rc = packed_or_user_strides(strides, 2, heads, d, dtype == FA_F32 ? 4 : 8, rs, hs)) return rc;
+    if (((static_cast<long long>(max_rows) + 15) / 16) * B * Hkv >= (1LL << 31))
+        return fail(FA_ERR_TOO_LARGE, "B*Hkv*ceil(max_seqlen/16) must be < 2^31");
+    *p = fa::CacheParams{};
+    p->k = k; p->v = v;
+    p->k_rs = rs[0]; p->k_hs = hs[0]; p->v_rs = rs[1]; p->v_hs = hs[1];
+    p->k_ext = rows_extent(total, Hkv, d, rs[0], hs[0]);
+    p->v_ext = rows_extent(total, Hkv, d, rs[1], hs[1]);
+    p->kc = static_cast<uint8_t*>(kc); p->vc = static_cast<uint8_t*>(vc);
+    p->ke = static_cast<uint8_t*>(ke); p->ve = static_cast<uint8_t*>(ve);
+    p->cu = cu; p->seqlens = seqlens; p->table = table;
+    p->B = B; p->Hkv = Hkv; p->total = total; p->max_new = max_rows;
+    p->max_pages = max_pages; p->num_pages = num_pages; p->page_shift = shift;
+    p->code_ext = static_cast<long long>(num_pages) * Hkv * page_size * d;
+    return FA_OK;
+}
+
+}  // namespace
+
+extern "C" int fa_cache_append(const void* k, const void* v, const long long* strides,
+                               void* k_cache, void* v_cache, void* k_exp, void* v_exp,
+                               const int* cu_seqlens_new, const int* seqlens_k,
+                               const int* page_table, int B, int max_seqlen_new, int total_new,
+                               int max_pages, int num_pages, int page_size, int Hkv, int d,
+                               int dtype, void* stream)
+{
+    fa::CacheParams p;
+    if (int rc = cache_rows_params(k, v, strides, k_cache, v_cache, k_exp, v_exp, cu_seqlens_new,
+                                   seqlens_k, page_table, B, max_seqlen_new, total_new, max_pages,
+                                   num_pages, page_size, Hkv, d, dtype, &p))
+        return rc;
+    if (!seqlens_k) return fail(FA_ERR_INVALID_ARG, "seqlens_k must be non-null");
+    if (!aligned4(seqlens_k)) return fail(FA_ERR_MISALIGNED, "seqlens_k must be 4-byte aligned");
+    DeviceInfo* di = nullptr;
+    if (int rc = device_info(&di)) return rc;
+    p.status = di->status;
+    cudaError_t e = fa::launch_cache_append(d, dtype == FA_F32, p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "cache append launch");
+    return FA_OK;
+}
+
+extern "C" int fa_cache_read(const void* k_cache, const void* v_cache, const void* k_exp,
+                             const void* v_exp, void* k, void* v, const long long* strides,
+                             const int* cu_seqlens_k, const int* page_table, int B,
+                             int max_seqlen_k, int total_k, int max_pages, int num_pages,
+                             int page_size, int Hkv, int d, int dtype, void* stream)
+{
+    fa::CacheParams p;
+    if (int rc = cache_rows_params(k, v, strides, const_cast<void*>(k_cache),
+                                   const_cast<void*>(v_cache), const_cast<void*>(k_exp),
+                                   const_cast<void*>(v_exp), cu_seqlens_k, nullptr, page_table, B,
+                                   max_seqlen_k, total_k, max_pages, num_pages, page_size, Hkv, d,
+                                   dtype, &p))
+        return rc;
+    DeviceInfo* di = nullptr;
+    if (int rc = device_info(&di)) return rc;
+    p.status = di->status;
+    cudaError_t e = fa::launch_cache_read(d, dtype == FA_F32, p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "cache read launch");
+    return FA_OK;
+}
+
+namespace {
+
+// 16-row tiles of a group's query rows that one CTA holds (1, 2 or 4).
+int cache_row_tiles(long long rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+
+// 2-D view of the cache's codes for tiles of `rows` rows of one page and head.
+int make_cache_map(CUtensorMap* m, const void* base, long long all_rows, int d, int rows)
+{
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(all_rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(d)};
+    cuuint32_t box[2] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(rows)};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(FA_ERR_LAUNCH, "cuTensorMapEncodeTiled failed with code " + std::to_string(r));
+    return FA_OK;
+}
+
+}  // namespace
+
+extern "C" int fa_decode_cache_splits_for(int B, int H, int Hkv, int max_seqlen_q,
+                                          int max_seqlen_k, int num_sms)
+{
+    if (B < 1 || H < 1 || Hkv < 1 || H % Hkv || max_seqlen_q < 1 || max_seqlen_k < 1 || num_sms < 1)
+        return fail(FA_ERR_INVALID_ARG, "sizes must be >= 1 and H a multiple of Hkv");
+    const long long rows = static_cast<long long>(max_seqlen_q) * (H / Hkv);
+    const long long rt = 16LL * cache_row_tiles(rows);
+    const long long units = static_cast<long long>(B) * Hkv * ((rows + rt - 1) / rt);
+    const int nblk = static_cast<int>((static_cast<long long>(max_seqlen_k) + 63) / 64);
+    const long long want = (4LL * num_sms + units - 1) / units;
+    const long long most = std::max(1, std::min(kDecodeMaxSplits, nblk / 2));
+    const int splits = static_cast<int>(std::min(most, std::max(1LL, want)));
+    const int per = (nblk + splits - 1) / splits;  // whole blocks to each range
+    return (nblk + per - 1) / per;
+}
+
+extern "C" int fa_decode_cache_num_splits(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_k)
+{
+    if (B < 1 || H < 1 || Hkv < 1 || H % Hkv || max_seqlen_q < 1 || max_seqlen_k < 1)
+        return fail(FA_ERR_INVALID_ARG, "sizes must be >= 1 and H a multiple of Hkv");
+    DeviceInfo* di = nullptr;
+    if (int rc = device_info(&di)) return rc;
+    return fa_decode_cache_splits_for(B, H, Hkv, max_seqlen_q, max_seqlen_k, di->sms);
+}
+
+extern "C" int fa_fwd_decode_cache(const void* q, const void* k_cache, const void* v_cache,
+                                   const void* k_exp, const void* v_exp, void* o, float* lse,
+                                   const int* cu_seqlens_q, const int* seqlens_k,
+                                   const int* page_table, int B, int max_seqlen_q,
+                                   int max_seqlen_k, int total_q, int max_pages, int num_pages,
+                                   int page_size, int H, int Hkv, int d, float scale, int causal,
+                                   int num_splits, void* workspace, size_t workspace_bytes,
+                                   void* stream)
+{
+    int shift = 0;
+    if (int rc = check_cache(k_cache, v_cache, k_exp, v_exp, page_table, B, max_pages, num_pages,
+                             page_size, Hkv, d, &shift))
+        return rc;
+    if (H < 1 || H % Hkv != 0) return fail(FA_ERR_INVALID_ARG, "H must be a multiple of Hkv");
+    if (total_q < 1 || max_seqlen_q < 1 || max_seqlen_k < 1)
+        return fail(FA_ERR_INVALID_ARG, "total_q, max_seqlen_q and max_seqlen_k must be >= 1");
+    if (causal != 0 && causal != 1) return fail(FA_ERR_INVALID_ARG, "causal must be 0 or 1");
+    if (!(scale == scale) || scale == INFINITY || scale == -INFINITY)
+        return fail(FA_ERR_INVALID_ARG, "scale must be finite");
+    if (num_splits < 1 || num_splits > kDecodeMaxSplits)
+        return fail(FA_ERR_INVALID_ARG, "num_splits must be in [1, " + std::to_string(kDecodeMaxSplits) + "]");
+    if (!q || !o || !cu_seqlens_q || !seqlens_k)
+        return fail(FA_ERR_INVALID_ARG, "q, o, cu_seqlens_q and seqlens_k must be non-null");
+    if (!aligned16(q) || !aligned16(o) || !aligned4(lse) || !aligned4(cu_seqlens_q) || !aligned4(seqlens_k))
+        return fail(FA_ERR_MISALIGNED, "q and o must be 16-byte aligned (the others 4-byte)");
+    if (static_cast<long long>(total_q) * H * d >= (1LL << 31))
+        return fail(FA_ERR_TOO_LARGE, "total_q*H*d must be < 2^31");
+    if (max_seqlen_q > total_q) max_seqlen_q = total_q;
+    // no sequence is longer than its row of the table (and block ends stay below 2^31)
+    max_seqlen_k = static_cast<int>(std::min<long long>(
+        std::min(max_seqlen_k, INT_MAX - 1024), static_cast<long long>(max_pages) * page_size));
+    const long long rows = static_cast<long long>(max_seqlen_q) * (H / Hkv);
+    const int rt = cache_row_tiles(rows);
+    const long long chunks = (rows + 16 * rt - 1) / (16 * rt);
+    if (static_cast<long long>(B) * Hkv * chunks * num_splits >= (1LL << 31) ||
+        static_cast<long long>(B) * H * max_seqlen_q >= (1LL << 31))
+        return fail(FA_ERR_TOO_LARGE, "B*Hkv*row tiles*num_splits and B*H*max_seqlen_q must be < 2^31");
+    const size_t need = fa_decode_workspace_bytes(total_q, H, d, num_splits);
+    if (need > 0) {
+        if (!workspace || workspace_bytes < need)
+            return fail(FA_ERR_WORKSPACE, "workspace must hold " + std::to_string(need) + " bytes");
+        if (!aligned16(workspace)) return fail(FA_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    }
+    DeviceInfo* di = nullptr;
+    if (int rc = device_info(&di)) return rc;
+    fa::CacheDecodeParams p{};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    if (need > 0) {
+        uint8_t* ws = static_cast<uint8_t*>(workspace);
+        p.o_part = reinterpret_cast<float*>(ws);
+        p.lse_part = reinterpret_cast<float*>(ws + decode_part_o_bytes(total_q, H, d, num_splits));
+    }
+    p.ke = static_cast<const uint8_t*>(k_exp);
+    p.ve = static_cast<const uint8_t*>(v_exp);
+    p.cu_q = cu_seqlens_q; p.seqlens = seqlens_k; p.table = page_table;
+    p.B = B; p.H = H; p.Hkv = Hkv; p.G = H / Hkv;
+    p.max_q = max_seqlen_q; p.max_k = max_seqlen_k; p.total_q = total_q;
+    p.max_pages = max_pages; p.num_pages = num_pages; p.page_shift = shift;
+    p.splits = num_splits;
+    const int nblk = static_cast<int>((static_cast<long long>(max_seqlen_k) + 63) / 64);
+    p.chunk_blocks = (nblk + num_splits - 1) / num_splits;
+    p.row_tiles = rt; p.row_chunks = static_cast<int>(chunks);
+    p.scale_log2 = scale * fa::kLog2e; p.causal = causal;
+    p.status = di->status; p.wait_limit_ns = g_wait_limit_ns; p.debug_flags = g_debug_flags;
+    const int cut = (g_debug_flags & fa::kDebugShrinkExtents) ? 1 : 0;
+    p.q_ext = (static_cast<long long>(total_q) * H - cut) * d;
+    p.stat_ext = static_cast<long long>(total_q) * H - cut;
+    p.part_ext = (static_cast<long long>(num_splits) * total_q * H - cut) * d;
+    if (int rc = get_encoder()) return rc;
+    CUtensorMap maps[2];
+    const long long all_rows = static_cast<long long>(num_pages) * Hkv * page_size;
+    const int box = page_size < 64 ? page_size : 64;
+    int rc = make_cache_map(&maps[0], k_cache, all_rows, d, box);
+    if (!rc) rc = make_cache_map(&maps[1], v_cache, all_rows, d, box);
+    if (rc) return rc;
+    cudaError_t e = fa::launch_decode_cache(d, maps[0], maps[1], p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "cache decode launch");
     return FA_OK;
 }

@@ -1,0 +1,144 @@
+// Shared definitions of the serving-side operators: rotary positions (fa_rope.cu), the paged
+// e4m3 key/value cache (fa_cache.cu) and the split-KV decode over that cache
+// (fa_decode_cache.cu).
+#pragma once
+#include "fa_common.cuh"
+
+namespace fa {
+
+// Watchdog sites of the cache decode kernel (see WaitSite; values below 64).
+enum ServeWaitSite : int {
+    kSiteCacheEmpty = 32,
+    kSiteCacheFull,
+    kSiteCacheDrain,
+};
+
+constexpr int kRopeMaxPairs = 64;
+
+// Rotary positions.  Pair p of a head turns by positions[axis[p]][token] * turn[p] / 2^64 turns.
+struct RopeParams {
+    const void* x[2];          // q, k (k null when Hkv = 0)
+    void* y[2];
+    long long x_rs[2], x_hs[2], y_rs[2], y_hs[2];  // element strides of a token and a head
+    long long x_ext[2], y_ext[2];                  // element extents (checked builds)
+    const int* pos;            // [axes, total]
+    long long pos_ext;
+    int total, H, Hkv;
+    int pairs;                 // rotated pairs of a head, a multiple of 8
+    int parts;                 // warps per token
+    float sign;                // -1 turns backwards (the gradient)
+    int* status;
+    unsigned long long turn[kRopeMaxPairs];  // turns per position, in units of 2^-64
+    unsigned char axis[kRopeMaxPairs];
+};
+
+// The paged cache: codes [num_pages, Hkv, page_size, d] (e4m3), one biased exponent a row
+// [num_pages, Hkv, page_size] (value of a code c under exponent byte x: c * 2^(x - 127)).
+// Position j of sequence b lies in page table[b][j / page_size], row j % page_size; a page
+// outside [0, num_pages) holds nothing.
+struct CacheParams {
+    const void* k;             // append: new rows [total, Hkv, d]; read: outputs of that shape
+    const void* v;
+    long long k_rs, k_hs, v_rs, v_hs;  // element strides of those rows
+    long long k_ext, v_ext;            // their element extents (checked builds)
+    uint8_t* kc;
+    uint8_t* vc;
+    uint8_t* ke;
+    uint8_t* ve;
+    const int* cu;             // [B + 1] starts of the sequences' rows in k, v
+    const int* seqlens;        // append: cached tokens of each sequence after the call
+    const int* table;          // [B, max_pages]
+    int B, Hkv, total, max_new;
+    int max_pages, num_pages, page_shift;
+    long long code_ext;        // elements of kc (checked builds); exponents: code_ext / d
+    int* status;
+};
+
+// Split-KV decode over the paged cache.
+struct CacheDecodeParams {
+    const __nv_bfloat16* q;    // [total_q, H, d]
+    __nv_bfloat16* o;
+    float* lse;                // [H, total_q] (may be null)
+    float* o_part;             // workspace: fp32 [splits, total_q, H, d]
+    float* lse_part;           // workspace: fp32 [splits, H, total_q]
+    const uint8_t* ke;
+    const uint8_t* ve;
+    const int* cu_q;           // [B + 1]
+    const int* seqlens;        // [B] keys of each sequence
+    const int* table;          // [B, max_pages]
+    int B, H, Hkv, G;          // G = H / Hkv
+    int max_q, max_k, total_q;
+    int max_pages, num_pages, page_shift;
+    int splits, chunk_blocks;  // ranges of a sequence, 64-key blocks of a range
+    int row_tiles, row_chunks; // 16-row tiles of a CTA, CTAs over a group's query rows
+    float scale_log2;
+    int causal;
+    int* status;
+    unsigned long long wait_limit_ns;
+    int debug_flags;
+    long long q_ext, stat_ext, part_ext;  // element extents (checked builds)
+};
+
+// Merge of the partial results of a decode.
+struct MergeParams {
+    __nv_bfloat16* o;          // [total_q, H, d]
+    float* lse;                // [H, total_q] (may be null)
+    const float* o_part;       // [splits, total_q, H, d]
+    const float* lse_part;     // [splits, H, total_q]
+    const int* cu_q;           // [B + 1]
+    int B, H, max_q, total_q, splits;
+    long long q_ext, stat_ext, part_ext;
+    int* status;
+};
+
+// 2^(byte - 127), the scale an exponent byte stands for; 255 is NaN.
+__device__ __forceinline__ float exp_byte_scale(uint32_t byte)
+{
+    const uint32_t bits = byte == 0 ? 0x00400000u : (byte == 255 ? 0x7fc00000u : byte << 23);
+    return __uint_as_float(bits);
+}
+
+// Two e4m3 codes (low byte first) to packed f16, exactly.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<unsigned short>(two)));
+    return r;
+}
+
+// Rows of packed sequence b, clamped to the tensor of `total` rows and to `most`.
+__device__ __forceinline__ int packed_rows(const int* cu, int b, int total, int most, int& first)
+{
+    first = min(max(cu[b], 0), total);
+    const int end = min(max(cu[b + 1], first), total);
+    return min(end - first, most);
+}
+
+// Launch as a programmatic dependent of the work before it on the stream: the grid's launch and
+// set-up overlap that work's end.  Every kernel launched so waits (griddepcontrol.wait) in all
+// of its threads before it touches global memory, so stream order is kept.
+template <class... P, class... A>
+inline cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                                    cudaStream_t st, A... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Wait for the work before this grid, then let the next grid's set-up start.
+__device__ __forceinline__ void dependent_begin()
+{
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+}  // namespace fa

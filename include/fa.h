@@ -362,6 +362,88 @@ int fa_decode_splits_for(int B, int Hkv, int max_seqlen_k, int num_sms);
 /* Library version string. */
 const char* fa_version(void);
 
+/* ---------------------------------------------------------------------------------------
+ * Serving: rotary positions, the paged e4m3 key/value cache, decoding over it.
+ * The kernels of these calls are launched as programmatic dependents, as fa_fwd_decode's are:
+ * they touch no global memory before the work before them on the stream has completed.
+ * --------------------------------------------------------------------------------------- */
+
+/* Rotary positions with several axes (time, height, width, ...), for q [total, H, d] and k
+ * [total, Hkv, d] in one call (Hkv = 0: q only, k and k_out NULL).  Pair p of a head turns by the
+ * angle positions[axis[p]][token] * inv_freq[p]:
+ *     (x1, x2) -> (x1 cos a - x2 sin a, x2 cos a + x1 sin a);
+ * pairs are (p, pairs + p), or (2p, 2p + 1) with interleaved = 1; the d - 2*pairs elements after
+ * them are copied.  inverse = 1 turns the other way: the gradient of the call (the map is
+ * orthogonal), and its undoing.
+ *   - positions: device int32 [axes, total], any values; angles are reduced exactly (64-bit
+ *     fixed-point turns), so far positions keep full accuracy.
+ *   - inv_freq (double) and axis (int): HOST arrays of `pairs` entries, read during the call.
+ *     inv_freq is finite, at most 2^20 in magnitude; axis entries are in [0, axes), axes <= 8.
+ *   - pairs: a multiple of 8, at most d / 2.
+ *   - strides: NULL for contiguous tensors, else HOST array of (row, head) element strides of q,
+ *     k, q_out, k_out, positive multiples of 16 bytes.
+ *   - q_out / k_out may be q / k themselves (in place, same strides); otherwise outputs overlap
+ *     neither an input nor one another (checked for contiguous tensors).
+ * bf16 or fp32; the rotation is computed in fp32 and rounded once. */
+int fa_rope(const void* q, const void* k, void* q_out, void* k_out, const int* positions,
+            const double* inv_freq, const int* axis, const long long* strides, int total, int H,
+            int Hkv, int d, int axes, int pairs, int interleaved, int inverse, int dtype,
+            void* stream);
+
+/* The paged cache.  k_cache, v_cache: e4m3 codes [num_pages, Hkv, page_size, d]; k_exp, v_exp:
+ * one biased exponent byte a row, [num_pages, Hkv, page_size]: code c under byte x stands for
+ * c * 2^(x - 127) (x = 255 for NaN).  page_table: device int32 [B, max_pages]; position j of
+ * sequence b is row j % page_size of page page_table[b][j / page_size].  page_size is a power of
+ * two in [16, 1024], num_pages*Hkv*page_size < 2^31.  A table entry outside [0, num_pages), and
+ * positions past max_pages * page_size, hold nothing: writes to them are dropped, they read as
+ * zero, and attention leaves their keys out.  Sequences may share pages that only get read; a
+ * page that a call writes must belong to one sequence.
+ *
+ * fa_cache_append quantises rows as they are written: k, v [total_new, Hkv, d] (dtype FA_BF16 or
+ * FA_F32; strides as fa_rope, for k and v) hold the new tokens of every sequence back to back
+ * (cu_seqlens_new, device int32 [B + 1]); seqlens_k (device int32 [B]) are the sequences'
+ * lengths after the call, so token i of sequence b goes to position
+ * seqlens_k[b] - n_b + i.  A row's scale is the least power of two 2^e with max|x| <= 448 * 2^e,
+ * e in [-110, 120] (0 for a row of zeros); codes are x / 2^e rounded to nearest, ties to even.
+ * Infinities and NaNs become the NaN code and do not count towards the maximum. */
+int fa_cache_append(const void* k, const void* v, const long long* strides, void* k_cache,
+                    void* v_cache, void* k_exp, void* v_exp, const int* cu_seqlens_new,
+                    const int* seqlens_k, const int* page_table, int B, int max_seqlen_new,
+                    int total_new, int max_pages, int num_pages, int page_size, int Hkv, int d,
+                    int dtype, void* stream);
+
+/* Reads the cache back: position i of sequence b into row cu_seqlens_k[b] + i of k, v
+ * [total_k, Hkv, d] (FA_BF16, exact for what fa_cache_append wrote, or FA_F32).  Rows that belong
+ * to no sequence are left as they are. */
+int fa_cache_read(const void* k_cache, const void* v_cache, const void* k_exp, const void* v_exp,
+                  void* k, void* v, const long long* strides, const int* cu_seqlens_k,
+                  const int* page_table, int B, int max_seqlen_k, int total_k, int max_pages,
+                  int num_pages, int page_size, int Hkv, int d, int dtype, void* stream);
+
+/* Split-KV decode over the paged cache: the attention of fa_fwd_decode (bf16 q, o [total_q, H,
+ * d], lse [H, total_q] or NULL, grouped heads, bottom-right causal mask, rows that see no key
+ * give O = 0 and lse = -inf) with the keys and values of the cache.  seqlens_k: device int32 [B],
+ * keys of each sequence (at most max_seqlen_k are used).  Any max_seqlen_q and any H / Hkv work;
+ * the kernel is made for few query rows per key/value head (up to 64 read the cache once; more
+ * read it again for every 64).  A sequence's keys are split into num_splits ranges in [1, 256]
+ * of ceil(ceil(max_seqlen_k / 64) / num_splits) blocks of 64 keys each, merged by a second
+ * kernel; fa_decode_cache_num_splits suggests a count.  workspace: as fa_fwd_decode
+ * (fa_decode_workspace_bytes(total_q, H, d, num_splits)).  Rows of o and lse that belong to no
+ * sequence are left as they are. */
+int fa_fwd_decode_cache(const void* q, const void* k_cache, const void* v_cache,
+                        const void* k_exp, const void* v_exp, void* o, float* lse,
+                        const int* cu_seqlens_q, const int* seqlens_k, const int* page_table,
+                        int B, int max_seqlen_q, int max_seqlen_k, int total_q, int max_pages,
+                        int num_pages, int page_size, int H, int Hkv, int d, float scale,
+                        int causal, int num_splits, void* workspace, size_t workspace_bytes,
+                        void* stream);
+
+/* A split count for fa_fwd_decode_cache on the current device, and the rule behind it for a
+ * device of num_sms SMs (host only).  Return it (>= 1) or a negative FA_ERR_* code. */
+int fa_decode_cache_num_splits(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_k);
+int fa_decode_cache_splits_for(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_k,
+                               int num_sms);
+
 #ifdef __cplusplus
 }
 #endif
