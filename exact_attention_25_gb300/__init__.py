@@ -25,7 +25,7 @@ __all__ = [
     "forward_fp8", "fa_fwd_fp8_varlen", "fa_fwd_fp8_varlen_workspace_bytes", "forward_fp8_varlen",
     "RopeTable", "rope_table", "fa_rope", "rope", "rope_backward", "PagedCache", "new_cache",
     "fa_cache_append", "cache_append", "fa_cache_read", "cache_read", "fa_fwd_decode_cache",
-    "fa_decode_cache_num_splits", "forward_decode_cache",
+    "fa_decode_cache_num_ctas", "fa_decode_cache_workspace_bytes", "forward_decode_cache",
 ]
 
 
@@ -664,19 +664,24 @@ def cache_read(cache: PagedCache, cu_seqlens_k, page_table, max_seqlen_k: int, t
     return k, v
 
 
-def fa_decode_cache_num_splits(B: int, H: int, Hkv: int, max_seqlen_q: int,
-                               max_seqlen_k: int) -> int:
-    """C ``fa_decode_cache_num_splits``: a split count that fills this GPU."""
-    n = int(load().fa_decode_cache_num_splits(B, H, Hkv, max_seqlen_q, max_seqlen_k))
+def fa_decode_cache_num_ctas(B: int, H: int, Hkv: int, max_seqlen_q: int,
+                             max_seqlen_k: int) -> int:
+    """C ``fa_decode_cache_num_ctas``: the number of thread blocks that fills this GPU."""
+    n = int(load().fa_decode_cache_num_ctas(B, H, Hkv, max_seqlen_q, max_seqlen_k))
     check(min(n, 0))
     return n
 
 
+def fa_decode_cache_workspace_bytes(H: int, Hkv: int, d: int, max_seqlen_q: int,
+                                    num_ctas: int) -> int:
+    return int(load().fa_decode_cache_workspace_bytes(H, Hkv, d, max_seqlen_q, num_ctas))
+
+
 def fa_fwd_decode_cache(q, cache: PagedCache, o, lse, cu_seqlens_q, seqlens_k, page_table,
                         max_seqlen_q: int, max_seqlen_k: int, scale: float, causal: bool,
-                        num_splits: int, workspace, stream=None) -> None:
+                        num_ctas: int, workspace, stream=None) -> None:
     """C ``fa_fwd_decode_cache``: q, o [total_q, H, d] bf16, lse [H, total_q] fp32 or None;
-    workspace (fa_decode_workspace_bytes) may be None for num_splits = 1."""
+    workspace (fa_decode_cache_workspace_bytes) may be None for num_ctas = 1."""
     pages, Hkv, ps, d, B, max_pages = _cache_sizes(cache, page_table)
     index = _same_device(q, *cache, o, lse, cu_seqlens_q, seqlens_k, page_table, workspace)
     _check_decode_io(q, o, lse, d)
@@ -687,7 +692,7 @@ def fa_fwd_decode_cache(q, cache: PagedCache, o, lse, cu_seqlens_q, seqlens_k, p
     _call(load().fa_fwd_decode_cache, index, stream, _ptr(q), *map(_ptr, cache), _ptr(o),
           _ptr(lse), _ptr(cu_seqlens_q), _ptr(seqlens_k), _ptr(page_table), B, int(max_seqlen_q),
           int(max_seqlen_k), total_q, max_pages, pages, ps, H, Hkv, d, float(scale),
-          int(bool(causal)), int(num_splits), _ptr(workspace), nbytes)
+          int(bool(causal)), int(num_ctas), _ptr(workspace), nbytes)
 
 
 def _check_decode_io(q, o, lse, d):
@@ -706,8 +711,8 @@ def _check_decode_io(q, o, lse, d):
 
 def forward_decode_cache(q, cache: PagedCache, cu_seqlens_q, seqlens_k, page_table,
                          max_seqlen_q: int, max_seqlen_k: int, scale: float | None = None,
-                         causal: bool = False, num_splits: int | None = None, stream=None):
-    """Allocate O, LSE (and the split workspace) and run fa_fwd_decode_cache."""
+                         causal: bool = False, num_ctas: int | None = None, stream=None):
+    """Allocate O, LSE (and the workspace) and run fa_fwd_decode_cache."""
     import torch
 
     total_q, H, d = q.shape
@@ -715,14 +720,14 @@ def forward_decode_cache(q, cache: PagedCache, cu_seqlens_q, seqlens_k, page_tab
         scale = d ** -0.5
     dev = q.device
     with _place(_same_device(q), stream):
-        if num_splits is None:
-            num_splits = fa_decode_cache_num_splits(int(page_table.shape[0]), H,
-                                                    int(cache.k.shape[1]), max_seqlen_q,
-                                                    max_seqlen_k)
-        nbytes = fa_decode_workspace_bytes(total_q, H, d, num_splits)
+        Hkv = cache.k.shape[1]
+        if num_ctas is None:
+            num_ctas = fa_decode_cache_num_ctas(page_table.shape[0], H, Hkv, max_seqlen_q,
+                                                max_seqlen_k)
+        nbytes = fa_decode_cache_workspace_bytes(H, Hkv, d, max_seqlen_q, num_ctas)
         ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
         o = torch.empty(q.shape, dtype=q.dtype, device=dev)
         lse = torch.empty((H, total_q), dtype=torch.float32, device=dev)
         fa_fwd_decode_cache(q, cache, o, lse, cu_seqlens_q, seqlens_k, page_table, max_seqlen_q,
-                            max_seqlen_k, scale, causal, num_splits, ws, stream)
+                            max_seqlen_k, scale, causal, num_ctas, ws, stream)
     return o, lse

@@ -31,7 +31,7 @@ EXPORTS = (
     "fa_checked_build", "fa_fwd_fp8", "fa_fwd_fp8_workspace_bytes", "fa_fwd_fp8_varlen",
     "fa_fwd_fp8_varlen_workspace_bytes", "fa_tile_order", "fa_order_group", "fa_decode_splits_for",
     "fa_rope", "fa_cache_append", "fa_cache_read", "fa_fwd_decode_cache",
-    "fa_decode_cache_num_splits", "fa_decode_cache_splits_for",
+    "fa_decode_cache_num_ctas", "fa_decode_cache_ctas_for", "fa_decode_cache_workspace_bytes",
 )
 
 _lock = threading.Lock()
@@ -121,10 +121,12 @@ def load(path: str | None = None):
         lib.fa_cache_append.argtypes = [vp] * 10 + [i] * 9 + [vp]
         lib.fa_cache_read.argtypes = [vp] * 9 + [i] * 9 + [vp]
         lib.fa_fwd_decode_cache.argtypes = [vp] * 10 + [i] * 10 + [f, i, i, vp, sz, vp]
-        lib.fa_decode_cache_num_splits.argtypes = [i] * 5
-        lib.fa_decode_cache_splits_for.argtypes = [i] * 6
+        lib.fa_decode_cache_num_ctas.argtypes = [i] * 5
+        lib.fa_decode_cache_ctas_for.argtypes = [i] * 6
+        lib.fa_decode_cache_workspace_bytes.argtypes = [i] * 5
+        lib.fa_decode_cache_workspace_bytes.restype = sz
         for fn in ("fa_rope", "fa_cache_append", "fa_cache_read", "fa_fwd_decode_cache",
-                   "fa_decode_cache_num_splits", "fa_decode_cache_splits_for"):
+                   "fa_decode_cache_num_ctas", "fa_decode_cache_ctas_for"):
             getattr(lib, fn).restype = ctypes.c_int
         for fn in ("fa_fwd", "fa_fwd_impl", "fa_bwd", "fa_bwd_impl", "fa_bwd_stage", "fa_device_status",
                    "fa_causal_block_counts", "fa_fwd_varlen", "fa_bwd_varlen", "fa_fwd_decode",

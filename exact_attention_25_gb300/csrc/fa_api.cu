@@ -1391,8 +1391,26 @@ extern "C" int fa_cache_read(const void* k_cache, const void* v_cache, const voi
 
 namespace {
 
-// 16-row tiles of a group's query rows that one CTA holds (1, 2 or 4).
-int cache_row_tiles(long long rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+// Query rows of a group that one CTA of the cache decode holds: one tile of 8 rows, or one, two
+// or four of 16.
+int cache_rows_cta(long long rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64; }
+
+constexpr int kCacheMaxCtas = 4096;
+
+// The most blocks a batch of these sizes can have; per_unit: places of a unit besides its blocks.
+long long cache_blocks(int B, int H, int Hkv, int max_q, int max_k, int per_unit = 0)
+{
+    const long long rows = static_cast<long long>(max_q) * (H / Hkv);
+    const int rc = cache_rows_cta(rows);
+    const long long nblk = (static_cast<long long>(max_k) + fa::kCacheBlock - 1) / fa::kCacheBlock;
+    return static_cast<long long>(B) * Hkv * ((rows + rc - 1) / rc) * (nblk + per_unit);
+}
+
+size_t cache_part_o_bytes(int H, int Hkv, int d, int max_q, int ctas)
+{
+    const int rc = cache_rows_cta(static_cast<long long>(max_q) * (H / Hkv));
+    return align256(static_cast<size_t>(2) * ctas * rc * d * 4);
+}
 
 // 2-D view of the cache's codes for tiles of `rows` rows of one page and head.
 int make_cache_map(CUtensorMap* m, const void* base, long long all_rows, int d, int rows)
@@ -1412,29 +1430,35 @@ int make_cache_map(CUtensorMap* m, const void* base, long long all_rows, int d, 
 
 }  // namespace
 
-extern "C" int fa_decode_cache_splits_for(int B, int H, int Hkv, int max_seqlen_q,
-                                          int max_seqlen_k, int num_sms)
+extern "C" int fa_decode_cache_ctas_for(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_k,
+                                        int num_sms)
 {
     if (B < 1 || H < 1 || Hkv < 1 || H % Hkv || max_seqlen_q < 1 || max_seqlen_k < 1 || num_sms < 1)
         return fail(FA_ERR_INVALID_ARG, "sizes must be >= 1 and H a multiple of Hkv");
-    const long long rows = static_cast<long long>(max_seqlen_q) * (H / Hkv);
-    const long long rt = 16LL * cache_row_tiles(rows);
-    const long long units = static_cast<long long>(B) * Hkv * ((rows + rt - 1) / rt);
-    const int nblk = static_cast<int>((static_cast<long long>(max_seqlen_k) + 63) / 64);
-    const long long want = (4LL * num_sms + units - 1) / units;
-    const long long most = std::max(1, std::min(kDecodeMaxSplits, nblk / 2));
-    const int splits = static_cast<int>(std::min(most, std::max(1LL, want)));
-    const int per = (nblk + splits - 1) / splits;  // whole blocks to each range
-    return (nblk + per - 1) / per;
+    const long long most = cache_blocks(B, H, Hkv, max_seqlen_q, max_seqlen_k);
+    // two blocks at least, so that a CTA's fixed latency is spread (one sequence of 4 K keys and 8
+    // heads: 10.5 us with 128 CTAs of two blocks, 12 with 256 of one)
+    return static_cast<int>(std::min<long long>((most + 1) / 2, std::min(2 * num_sms, kCacheMaxCtas)));
 }
 
-extern "C" int fa_decode_cache_num_splits(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_k)
+extern "C" int fa_decode_cache_num_ctas(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_k)
 {
     if (B < 1 || H < 1 || Hkv < 1 || H % Hkv || max_seqlen_q < 1 || max_seqlen_k < 1)
         return fail(FA_ERR_INVALID_ARG, "sizes must be >= 1 and H a multiple of Hkv");
     DeviceInfo* di = nullptr;
     if (int rc = device_info(&di)) return rc;
-    return fa_decode_cache_splits_for(B, H, Hkv, max_seqlen_q, max_seqlen_k, di->sms);
+    return fa_decode_cache_ctas_for(B, H, Hkv, max_seqlen_q, max_seqlen_k, di->sms);
+}
+
+extern "C" size_t fa_decode_cache_workspace_bytes(int H, int Hkv, int d, int max_seqlen_q, int num_ctas)
+{
+    if (H < 1 || Hkv < 1 || H % Hkv || (d != 64 && d != 128) || max_seqlen_q < 1 || num_ctas < 1 ||
+        num_ctas > kCacheMaxCtas)
+        return 0;
+    if (num_ctas == 1) return 0;
+    const int rc = cache_rows_cta(static_cast<long long>(max_seqlen_q) * (H / Hkv));
+    return cache_part_o_bytes(H, Hkv, d, max_seqlen_q, num_ctas) +
+           align256(static_cast<size_t>(2) * num_ctas * rc * 4) + 256;
 }
 
 extern "C" int fa_fwd_decode_cache(const void* q, const void* k_cache, const void* v_cache,
@@ -1443,7 +1467,7 @@ extern "C" int fa_fwd_decode_cache(const void* q, const void* k_cache, const voi
                                    const int* page_table, int B, int max_seqlen_q,
                                    int max_seqlen_k, int total_q, int max_pages, int num_pages,
                                    int page_size, int H, int Hkv, int d, float scale, int causal,
-                                   int num_splits, void* workspace, size_t workspace_bytes,
+                                   int num_ctas, void* workspace, size_t workspace_bytes,
                                    void* stream)
 {
     int shift = 0;
@@ -1456,8 +1480,8 @@ extern "C" int fa_fwd_decode_cache(const void* q, const void* k_cache, const voi
     if (causal != 0 && causal != 1) return fail(FA_ERR_INVALID_ARG, "causal must be 0 or 1");
     if (!(scale == scale) || scale == INFINITY || scale == -INFINITY)
         return fail(FA_ERR_INVALID_ARG, "scale must be finite");
-    if (num_splits < 1 || num_splits > kDecodeMaxSplits)
-        return fail(FA_ERR_INVALID_ARG, "num_splits must be in [1, " + std::to_string(kDecodeMaxSplits) + "]");
+    if (num_ctas < 1 || num_ctas > kCacheMaxCtas)
+        return fail(FA_ERR_INVALID_ARG, "num_ctas must be in [1, " + std::to_string(kCacheMaxCtas) + "]");
     if (!q || !o || !cu_seqlens_q || !seqlens_k)
         return fail(FA_ERR_INVALID_ARG, "q, o, cu_seqlens_q and seqlens_k must be non-null");
     if (!aligned16(q) || !aligned16(o) || !aligned4(lse) || !aligned4(cu_seqlens_q) || !aligned4(seqlens_k))
@@ -1468,13 +1492,9 @@ extern "C" int fa_fwd_decode_cache(const void* q, const void* k_cache, const voi
     // no sequence is longer than its row of the table (and block ends stay below 2^31)
     max_seqlen_k = static_cast<int>(std::min<long long>(
         std::min(max_seqlen_k, INT_MAX - 1024), static_cast<long long>(max_pages) * page_size));
-    const long long rows = static_cast<long long>(max_seqlen_q) * (H / Hkv);
-    const int rt = cache_row_tiles(rows);
-    const long long chunks = (rows + 16 * rt - 1) / (16 * rt);
-    if (static_cast<long long>(B) * Hkv * chunks * num_splits >= (1LL << 31) ||
-        static_cast<long long>(B) * H * max_seqlen_q >= (1LL << 31))
-        return fail(FA_ERR_TOO_LARGE, "B*Hkv*row tiles*num_splits and B*H*max_seqlen_q must be < 2^31");
-    const size_t need = fa_decode_workspace_bytes(total_q, H, d, num_splits);
+    if (cache_blocks(B, H, Hkv, max_seqlen_q, max_seqlen_k, fa::kUnitCost) >= (1LL << 31))
+        return fail(FA_ERR_TOO_LARGE, "the batch must have fewer than 2^31 blocks of 128 keys");
+    const size_t need = fa_decode_cache_workspace_bytes(H, Hkv, d, max_seqlen_q, num_ctas);
     if (need > 0) {
         if (!workspace || workspace_bytes < need)
             return fail(FA_ERR_WORKSPACE, "workspace must hold " + std::to_string(need) + " bytes");
@@ -1489,7 +1509,7 @@ extern "C" int fa_fwd_decode_cache(const void* q, const void* k_cache, const voi
     if (need > 0) {
         uint8_t* ws = static_cast<uint8_t*>(workspace);
         p.o_part = reinterpret_cast<float*>(ws);
-        p.lse_part = reinterpret_cast<float*>(ws + decode_part_o_bytes(total_q, H, d, num_splits));
+        p.lse_part = reinterpret_cast<float*>(ws + cache_part_o_bytes(H, Hkv, d, max_seqlen_q, num_ctas));
     }
     p.ke = static_cast<const uint8_t*>(k_exp);
     p.ve = static_cast<const uint8_t*>(v_exp);
@@ -1497,20 +1517,20 @@ extern "C" int fa_fwd_decode_cache(const void* q, const void* k_cache, const voi
     p.B = B; p.H = H; p.Hkv = Hkv; p.G = H / Hkv;
     p.max_q = max_seqlen_q; p.max_k = max_seqlen_k; p.total_q = total_q;
     p.max_pages = max_pages; p.num_pages = num_pages; p.page_shift = shift;
-    p.splits = num_splits;
-    const int nblk = static_cast<int>((static_cast<long long>(max_seqlen_k) + 63) / 64);
-    p.chunk_blocks = (nblk + num_splits - 1) / num_splits;
-    p.row_tiles = rt; p.row_chunks = static_cast<int>(chunks);
+    p.ctas = num_ctas;
+    p.rows_cta = cache_rows_cta(static_cast<long long>(max_seqlen_q) * (H / Hkv));
+    p.row_tiles = p.rows_cta <= 16 ? 1 : p.rows_cta / 16;
+    p.rows_shift = p.rows_cta == 8 ? 3 : p.rows_cta == 16 ? 4 : p.rows_cta == 32 ? 5 : 6;
     p.scale_log2 = scale * fa::kLog2e; p.causal = causal;
     p.status = di->status; p.wait_limit_ns = g_wait_limit_ns; p.debug_flags = g_debug_flags;
     const int cut = (g_debug_flags & fa::kDebugShrinkExtents) ? 1 : 0;
     p.q_ext = (static_cast<long long>(total_q) * H - cut) * d;
     p.stat_ext = static_cast<long long>(total_q) * H - cut;
-    p.part_ext = (static_cast<long long>(num_splits) * total_q * H - cut) * d;
+    p.part_ext = (2LL * num_ctas * p.rows_cta - cut) * d;
     if (int rc = get_encoder()) return rc;
     CUtensorMap maps[2];
     const long long all_rows = static_cast<long long>(num_pages) * Hkv * page_size;
-    const int box = page_size < 64 ? page_size : 64;
+    const int box = page_size < fa::kCacheBlock ? page_size : fa::kCacheBlock;
     int rc = make_cache_map(&maps[0], k_cache, all_rows, d, box);
     if (!rc) rc = make_cache_map(&maps[1], v_cache, all_rows, d, box);
     if (rc) return rc;

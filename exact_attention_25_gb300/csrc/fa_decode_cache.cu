@@ -12,37 +12,51 @@
 // Here the codes are converted between shared memory and mma.sync fragments instead, in
 // registers: 2 bytes of traffic a code, 0.18 m16n8k16 a clock.
 //
-// Layout of a CTA: warps 0-3 compute, warp 4 copies pages to a ring of 64-key blocks by TMA
+// Layout of a CTA: warps 0-3 compute, warp 4 copies pages to a ring of 128-key blocks by TMA
 // (swizzled rows, plus the rows' exponent bytes).  A group's query rows (row i * G + g: query
-// i, head g of the G that share the K/V head) form 16-row tiles; warp w works on tile
+// i, head g of the G that share the K/V head) form tiles of 8 * NR rows; warp w works on tile
 // w % row_tiles and on every (4 / row_tiles)-th 16-key step of a block, with its own online
-// softmax; the warps' results merge in shared memory at the end.  Ranges of a sequence's blocks
-// go to different CTAs and merge in fa_decode_merge_kernel.
+// softmax; the warps' results merge through shared memory at the end of a unit.  The copies run
+// ahead over unit boundaries.  Two CTAs an SM, each with an equal share of the whole batch's blocks
+// (CacheDecodeParams), found from the lengths on the device: a fixed number of ranges a sequence
+// left 30-45 % of the slots idle on ragged batches, and finer ranges cost every CTA its 4-5 us of
+// dependent loads (lengths, table, copies, output) again.
 //
+// Both products are computed transposed, with the keys (S^T = K Q^T) or the columns of V (O^T =
+// V^T P^T) as the 16 rows of the m16n8k16 product and the query rows as its 8 columns: a decode
+// step has G <= 8 query rows, which as the 16-row operand would leave half of every product
+// empty, and twice the registers.
 // Per 16-key step, thread (g = lane / 4, t = lane % 4):
-//  - S = Q K^T: the contraction index is permuted so that a thread's four elements of k-step s
-//    are d = 16 t + 4 s + {0..3} (of the 64-wide half), i.e. one word of a 16-byte chunk, and key
-//    column n holds key kperm(n) so that the chunks read together lie in different banks.
-//  - O += P V: P's accumulator layout is the A layout, V's column n of tile j is d = 16 n + j
-//    (8 n + j for d = 64), so a thread reads whole chunks of its keys' rows and pairs two keys'
-//    bytes by a byte permute.
+//  - S^T: the contraction index is permuted so that a thread's four elements of k-step s are
+//    d = 16 t + 4 s + {0..3} (of a 64-wide half), i.e. one word of a 16-byte chunk; product row m
+//    holds key kperm(m), chosen so that the chunks that are read together lie in different banks.
+//    The thread gets keys kperm(g), 8 + kperm(g) of query rows 2 t, 2 t + 1.
+//  - the weights go to the B layout by two 8 x 8 transposes (movmatrix).
+//  - O^T: product rows g and g + 8 of tile i are V's columns d = CW g + 2 i and CW g + 2 i + 1 (CW =
+//    d / 8), so a thread reads whole chunks of its keys' rows and pairs two keys' bytes by a byte
+//    permute.
 // Number ranges: Q rows are scaled by a power of two to just below 2^15 for f16 (elements down
 // to 2^-38 of the row's largest keep a value).  Two running maxima are kept.  m, of the
 // logits x (base 2), frames the sum l.  M, of x + (V's exponent), frames the weights
 // w = 2^(x + ev - M + 11) that multiply V's codes, so a V row of any size keeps its weight's
-// 11 bits and w <= 2^15 (maxima move when they grow by more than 4); f16's smallest step puts a
-// floor of 2^-36 of the largest weight under what a single key can still add.
+// 11 bits and w <= 2^15 (maxima move when they are exceeded by more than 4, so most steps need no
+// reduction over the keys' lanes, only a vote); f16's smallest step puts a floor of 2^-36 of the
+// largest weight under what a single key can still add.
 #include "fa_serve.cuh"
 #include "tc_ptx.cuh"
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 namespace fa {
 
 namespace {
 
-constexpr int kKB = 64;           // keys of a block
+constexpr int kKB = kCacheBlock;  // keys of a block
 constexpr int kComputeWarps = 4;
+constexpr int kUnits = 8;         // units described ahead
+constexpr int kMergeThreads = 128;
 constexpr float kFrame = 11.0f;   // log2 of the largest weight right after a rescale
 constexpr float kGrow = 4.0f;     // a maximum moves when it grows by more than this
 
@@ -50,13 +64,13 @@ template <int D>
 struct CacheCfg {
     static constexpr int TILE = kKB * D;               // bytes of a block's K or V codes
     static constexpr int STAGE = 2 * TILE + 2 * kKB;   // codes, then exponent bytes
-    static constexpr int STAGES = D == 128 ? 6 : 11;
+    static constexpr int STAGES = D == 128 ? 3 : 6;
     // codes need 1024-byte alignment: all tiles first, then the exponents of all stages
     static constexpr int EXP0 = STAGES * 2 * TILE;
     static constexpr int RING = STAGES * STAGE;
     static constexpr int OLD = D + 4;                  // row stride of the merge buffer, floats
-    static constexpr int MERGE = kComputeWarps * 16 * (OLD + 3) * 4;
-    static constexpr int SMEM = (RING > MERGE ? RING : MERGE) + 1024;
+    static constexpr int XCH = 8 * (OLD + 3);          // floats one warp hands over for 8 rows
+    static constexpr int SMEM = RING + 3 * XCH * 4 + 1024;
     static constexpr int THREADS = 32 * (kComputeWarps + 1);
 };
 
@@ -101,7 +115,21 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w)
     return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
-// The key of a 16-key step's column n (0..7; columns 8..15 are the same plus 8).
+// Transpose of an 8 x 8 tile of 16-bit elements held as a product's A or C tile is.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+// An exponent byte x as the float x - 127, or NaN for 255.
+__device__ __forceinline__ float exp_byte_log2(uint32_t byte)
+{
+    return byte == 255 ? NAN : __uint_as_float(0x4B000000u | byte) - (8388608.0f + 127.0f);
+}
+
+// The key of a 16-key step's product row n (0..7; rows 8..15 are the same plus 8).
 template <int D>
 __device__ __forceinline__ int kperm(int n)
 {
@@ -110,23 +138,112 @@ __device__ __forceinline__ int kperm(int n)
 
 }  // namespace
 
-// SMALL: at most 8 query rows, so the second half of every fragment row pair is empty.
-template <int D, bool SMALL>
+// One unit's part of a share.
+struct Unit {
+    int b, hk, row0;       // sequence, key/value head, first query row
+    int q0, nq, nk, nblk;  // the sequence: first token, tokens, keys, blocks
+    int in_seq;            // units of the sequence
+    int jb, J;             // this share's blocks of the unit: [jb, jb + J)
+    int flags;             // kFirst: the share's first unit
+};
+constexpr int kFirst = 1;
+
+// Sizes of sequence b: units (row sets times heads) of nblk blocks each.
+__device__ __forceinline__ void sequence_work(const CacheDecodeParams& p, int b, Unit& u)
+{
+    u.b = b;
+    u.nq = packed_rows(p.cu_q, b, p.total_q, p.max_q, u.q0);
+    u.nk = min(max(p.seqlens[b], 0), p.max_k);
+    u.nblk = max(1, (u.nk + kKB - 1) / kKB);
+    u.in_seq = ((u.nq * p.G + p.rows_cta - 1) >> p.rows_shift) * p.Hkv;
+}
+
+// The line of T places in `ctas` shares, the first T mod ctas of them one place longer.  (T is
+// below 2^31: checked on the host for the largest batch of the call's sizes.)
+struct Shares {
+    int total, per, more;
+    __device__ __forceinline__ Shares(int T, int ctas)
+        : total(T), per(static_cast<unsigned>(T) / static_cast<unsigned>(ctas)), more(T - per * ctas)
+    {
+    }
+    __device__ __forceinline__ int start(int c) const { return c * per + min(c, more); }
+    __device__ __forceinline__ int share_of(int pos) const
+    {
+        const int cut = more * (per + 1);
+        return pos < cut ? pos / (per + 1) : more + (pos - cut) / per;
+    }
+};
+
+// All lanes of a warp: the line's shares and, for the first place of share c, its sequence (u)
+// and `at`, its distance from that sequence's first place.  The search is skipped when the share
+// starts at the line's end.
+__device__ __forceinline__ Shares find_share(const CacheDecodeParams& p, int c, Unit& u, int& at)
+{
+    const int lane = threadIdx.x & 31;
+    auto work = [&](int b) {
+        if (b >= p.B) return 0;
+        Unit v;
+        sequence_work(p, b, v);
+        return v.in_seq * (v.nblk + kUnitCost);
+    };
+    const int w0 = work(lane);
+    int total = w0;
+    for (int b0 = 32; b0 < p.B; b0 += 32) total += work(b0 + lane);
+    total = __reduce_add_sync(0xffffffffu, total);
+    const Shares sh(total, p.ctas);
+    const int pos = sh.start(c);
+    if (pos >= total) return sh;
+    int run = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int w = b0 == 0 ? w0 : work(b0 + lane);
+        int sum = w;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int up = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += up;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, run + sum > pos);
+        if (past) {
+            const int src = __ffs(past) - 1;
+            at = pos - run - __shfl_sync(0xffffffffu, sum - w, src);
+            sequence_work(p, b0 + src, u);
+            break;
+        }
+        run += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    return sh;
+}
+
+// Row set and head of the sequence's unit i.
+__device__ __forceinline__ void unit_at(const CacheDecodeParams& p, int i, Unit& u)
+{
+    const int set = static_cast<unsigned>(i) / static_cast<unsigned>(p.Hkv);
+    u.row0 = set << p.rows_shift;
+    u.hk = i - set * p.Hkv;
+}
+
+// NR: 8-row query tiles of a warp.
+template <int D, int NR>
 __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
     fa_decode_cache_kernel(const __grid_constant__ CUtensorMap tm_k,
                            const __grid_constant__ CUtensorMap tm_v, const CacheDecodeParams p)
 {
     using C = CacheCfg<D>;
-    constexpr int NH = SMALL ? 1 : 2;       // rows g and g + 8 of a fragment
     constexpr int KS = D / 16;              // k-steps of S
-    constexpr int NT = D / 8;               // column tiles of O
+    constexpr int MT = D / 16;              // 16-column tiles of O
     constexpr int CH = D / 64;              // 16-byte chunks of a K row a thread reads
+    constexpr int VW = D / 32;              // words of a V row a thread reads
+    constexpr int TR = 8 * NR;              // query rows of a warp
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     __shared__ __align__(8) uint64_t bar_full[C::STAGES];
     __shared__ __align__(8) uint64_t bar_empty[C::STAGES];
+    __shared__ __align__(8) uint64_t bar_unit[kUnits];
+    __shared__ __align__(8) uint64_t bar_given[3];  // a warp's partial sums lie in xch[i] ...
+    __shared__ __align__(8) uint64_t bar_taken[3];  // ... and have been added to another's
     __shared__ int s_valid[C::STAGES];  // bit i: keys [16 i, 16 i + 16) of the block were copied
+    __shared__ Unit s_unit[kUnits];     // the copies' units, in order
     __shared__ int abort_flag;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -134,6 +251,11 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&bar_full[s], 1);
             mbar_init(&bar_empty[s], kComputeWarps);
+        }
+        for (int k = 0; k < kUnits; ++k) mbar_init(&bar_unit[k], 1);
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&bar_given[i], 1);
+            mbar_init(&bar_taken[i], 1);
         }
         abort_flag = 0;
         mbar_fence_init();
@@ -144,127 +266,159 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
     }
     __syncthreads();
     dependent_begin();
-
-    const int split = static_cast<int>(blockIdx.x) % p.splits;
-    int rest = static_cast<int>(blockIdx.x) / p.splits;
-    const int chunk = rest % p.row_chunks;
-    rest /= p.row_chunks;
-    const int b = rest / p.Hkv, hk = rest % p.Hkv;
-    int q0;
-    const int nq = packed_rows(p.cu_q, b, p.total_q, p.max_q, q0);
-    const int nk = min(max(p.seqlens[b], 0), p.max_k);
-    const int row0 = chunk * 16 * p.row_tiles;                    // first query row of the CTA
-    const int rows = min(nq * p.G - row0, 16 * p.row_tiles);
-    if (rows <= 0) return;
-    const int jb = split * p.chunk_blocks;
-    const int J = min((nk + kKB - 1) / kKB - jb, p.chunk_blocks);  // blocks of this range
-    const int shift = nk - nq;
-    // element offset of query row r's o row (also of its partial row, within a split)
-    auto out_off = [&](int r) {
-        const int i = (row0 + r) / p.G, g = (row0 + r) - i * p.G;
-        return (static_cast<long long>(q0 + i) * p.H + hk * p.G + g) * D;
-    };
-    auto stat_off = [&](int r) {
-        const int i = (row0 + r) / p.G, g = (row0 + r) - i * p.G;
-        return static_cast<long long>(hk * p.G + g) * p.total_q + q0 + i;
-    };
-    const long long part_stat = static_cast<long long>(split) * p.H * p.total_q;
-    if (J <= 0) {
-        // no key in this range: nothing for the merge, or (one range) a row without keys
-        for (int r = threadIdx.x; r < rows; r += C::THREADS) {
-            const long long so = stat_off(r);
-            if (p.splits > 1) {
-                if (in_extent(part_stat + so, 1, p.part_ext / D, p.status)) p.lse_part[part_stat + so] = -INFINITY;
-            } else if (p.lse != nullptr && in_extent(so, 1, p.stat_ext, p.status)) {
-                p.lse[so] = -INFINITY;
-            }
-        }
-        if (p.splits == 1)
-            for (int i = threadIdx.x; i < rows * (D / 8); i += C::THREADS) {
-                const long long off = out_off(i / (D / 8)) + 8 * (i % (D / 8));
-                if (in_extent(off, 8, p.q_ext, p.status))
-                    *reinterpret_cast<uint4*>(p.o + off) = make_uint4(0u, 0u, 0u, 0u);
-            }
-        return;
-    }
-
+    const int cta = static_cast<int>(blockIdx.x);
     const Watchdog wd{&abort_flag, p.status, p.wait_limit_ns};
-    float* sO = reinterpret_cast<float*>(smem);               // [4][16][OLD]
-    float* sStat = sO + kComputeWarps * 16 * C::OLD;          // [4][16][3]: M, m, l
-    int* ok_flag = &abort_flag;
 
     if (warp == kComputeWarps) {
         // ------------------------------------------------------------- copies
+        // The share's units one after another; a unit's description goes to s_unit before its
+        // page ids are read, so the compute warps fetch its queries meanwhile.  (kUnits > STAGES + 1:
+        // when a slot is written again, every warp has released a block of a later unit than the
+        // one that it held.)
+        Unit un;
+        int at = 0;
+        const Shares sh = find_share(p, cta, un, at);
+        int left = sh.start(cta + 1) - sh.start(cta);
         const int ps = 1 << p.page_shift;
         const int np = ps >= kKB ? 1 : kKB / ps;              // pages of a block
         const int rows_pp = ps >= kKB ? kKB : ps;             // rows of a copy
         const int groups_pp = rows_pp / 16;
-        int base = -1, ids = -1;                              // page ids base + lane
-        int issued = 0;
-        for (int jj = 0; jj < J; ++jj) {
-            const int s = jj % C::STAGES;
-            const int pos = (jb + jj) * kKB;
-            const int first = pos >> p.page_shift;
-            if (base < 0 || first + np > base + 32) {
-                base = first;
-                const int idx = base + lane;
-                ids = -1;
-                if (idx < p.max_pages && (static_cast<long long>(idx) << p.page_shift) < nk)
-                    ids = p.table[static_cast<long long>(b) * p.max_pages + idx];
-                if (ids >= p.num_pages) ids = -1;
-            }
-            const int id = __shfl_sync(0xffffffffu, ids, (first - base + lane) & 31);
-            const bool mine = lane < np && id >= 0;
-            const uint32_t got = __ballot_sync(0xffffffffu, mine);
-            if (!warp_wait_all(&bar_empty[s], ((jj / C::STAGES) & 1) ^ 1, wd, kSiteCacheEmpty)) break;
-            if (lane == 0) {
-                int bits = 0;
-                for (int i = 0; i < np; ++i)
-                    if (got >> i & 1) bits |= ((1 << groups_pp) - 1) << (i * groups_pp);
-                s_valid[s] = bits;
-                mbar_arrive_expect_tx(&bar_full[s],
-                                      static_cast<uint32_t>(__popc(got) * rows_pp * 2 * (D + 1)));
-            }
-            __syncwarp();
-            if (mine && !(jj == 0 && (p.debug_flags & kDebugDropFirstLoad))) {
-                const int at = lane * rows_pp;                // first key of the copy in the block
-                const long long row = ((static_cast<long long>(id) * p.Hkv + hk) << p.page_shift) +
-                                      (pos & (ps - 1));
-                uint8_t* kt = smem + s * 2 * C::TILE + at * D;
-                uint8_t* ex = smem + C::EXP0 + s * 2 * kKB + at;
-                tma_load_2d(kt, &tm_k, &bar_full[s], 0, static_cast<int>(row));
-                bulk_load(ex, p.ke + row, rows_pp, &bar_full[s]);
-                tma_load_2d(kt + C::TILE, &tm_v, &bar_full[s], 0, static_cast<int>(row));
-                bulk_load(ex + kKB, p.ve + row, rows_pp, &bar_full[s]);
-            }
-            issued = jj + 1;
+        int ui = 0, place = 0;                                // unit of the sequence, place in it
+        if (left > 0) {
+            ui = static_cast<unsigned>(at) / static_cast<unsigned>(un.nblk + kUnitCost);
+            place = at - ui * (un.nblk + kUnitCost);
         }
-        // no copy may land after the merge reuses the ring or the CTA exits
+        bool ok = true;
+        int it = 0, k = 0;                                    // blocks through the ring, units so far
+        while (ok && left > 0) {
+            unit_at(p, ui, un);
+            const int end = min(un.nblk + kUnitCost, place + left);
+            left -= end - place;
+            un.jb = max(0, place - kUnitCost);
+            un.J = max(0, end - kUnitCost) - un.jb;
+            un.flags = k == 0 ? kFirst : 0;
+            if (un.J > 0) {
+                if (lane == 0) {
+                    s_unit[k % kUnits] = un;
+                    mbar_arrive(&bar_unit[k % kUnits]);
+                }
+                // the unit's queries, ahead of the compute warps
+                const int rows = min(un.nq * p.G - un.row0, p.rows_cta);
+                for (int r = lane; r < rows; r += 32) {
+                    const int i = (un.row0 + r) / p.G, h = (un.row0 + r) - i * p.G;
+                    const __nv_bfloat16* q =
+                        p.q + (static_cast<long long>(un.q0 + i) * p.H + un.hk * p.G + h) * D;
+                    for (int c = 0; c < D; c += 64)
+                        asm volatile("prefetch.global.L1 [%0];" ::"l"(q + c));
+                }
+                ++k;
+            }
+            int base = -1, ids = -1;                          // page ids base + lane
+            for (int jj = 0; jj < un.J; ++jj, ++it) {
+                const int s = it % C::STAGES;
+                const int pos = (un.jb + jj) * kKB;
+                const int first = pos >> p.page_shift;
+                if (base < 0 || first + np > base + 32) {
+                    base = first;
+                    const int idx = base + lane;
+                    ids = -1;
+                    if (idx < p.max_pages && (static_cast<long long>(idx) << p.page_shift) < un.nk)
+                        ids = p.table[static_cast<long long>(un.b) * p.max_pages + idx];
+                    if (ids >= p.num_pages) ids = -1;
+                }
+                const int id = __shfl_sync(0xffffffffu, ids, (first - base + lane) & 31);
+                const bool mine = lane < np && id >= 0;
+                const uint32_t got = __ballot_sync(0xffffffffu, mine);
+                ok = warp_wait_all(&bar_empty[s], ((it / C::STAGES) & 1) ^ 1, wd, kSiteCacheEmpty);
+                if (!ok) break;
+                if (lane == 0) {
+                    int bits = 0;
+                    for (int i = 0; i < np; ++i)
+                        if (got >> i & 1) bits |= ((1 << groups_pp) - 1) << (i * groups_pp);
+                    s_valid[s] = bits;
+                    mbar_arrive_expect_tx(&bar_full[s],
+                                          static_cast<uint32_t>(__popc(got) * rows_pp * 2 * (D + 1)));
+                }
+                __syncwarp();
+                if (mine && !(it == 0 && (p.debug_flags & kDebugDropFirstLoad))) {
+                    const int row_in = lane * rows_pp;        // first key of the copy in the block
+                    const long long row = ((static_cast<long long>(id) * p.Hkv + un.hk) << p.page_shift) +
+                                          (pos & (ps - 1));
+                    uint8_t* kt = smem + s * 2 * C::TILE + row_in * D;
+                    uint8_t* ex = smem + C::EXP0 + s * 2 * kKB + row_in;
+                    tma_load_2d(kt, &tm_k, &bar_full[s], 0, static_cast<int>(row));
+                    bulk_load(ex, p.ke + row, rows_pp, &bar_full[s]);
+                    tma_load_2d(kt + C::TILE, &tm_v, &bar_full[s], 0, static_cast<int>(row));
+                    bulk_load(ex + kKB, p.ve + row, rows_pp, &bar_full[s]);
+                }
+            }
+            place = 0;
+            if (left > 0) {
+                if (++ui == un.in_seq) {
+                    ui = 0;
+                    do sequence_work(p, un.b + 1, un);
+                    while (un.in_seq == 0);
+                }
+            }
+        }
+        // the end of the units
+        if (ok && lane == 0) {
+            s_unit[k % kUnits].J = 0;
+            mbar_arrive(&bar_unit[k % kUnits]);
+        }
+        // no copy may land after the CTA exits (bounded waits that ignore the abort flag)
         volatile int no_abort = 0;
         const Watchdog wd_drain{&no_abort, p.status, p.wait_limit_ns};
-        for (int jj = max(0, issued - C::STAGES); jj < issued; ++jj)
-            if (!mbar_wait(&bar_full[jj % C::STAGES], (jj / C::STAGES) & 1, wd_drain, kSiteCacheDrain))
-                *ok_flag = 1;
-        __syncthreads();
-    } else {
-        // ------------------------------------------------------------- attention
-        const int g = lane >> 2, t = lane & 3;
-        const int tile = warp % p.row_tiles;
-        const int slots = kComputeWarps / p.row_tiles, slot = warp / p.row_tiles;
-        // This thread's query rows r[h] = tile * 16 + g + 8 h, their scale and last visible key.
-        uint32_t qa[KS][4];
-        float cx[NH];      // logit (base 2) per unit of the scaled product, without K's scale
-        int lim[NH];
+        for (int i = max(0, it - C::STAGES); i < it; ++i)
+            mbar_wait(&bar_full[i % C::STAGES], (i / C::STAGES) & 1, wd_drain, kSiteCacheDrain);
+        return;
+    }
+
+    // ----------------------------------------------------------------- attention
+    const int g = lane >> 2, t = lane & 3;
+    const int tile = warp % p.row_tiles;
+    const int slots = kComputeWarps / p.row_tiles, slot = warp / p.row_tiles;
+    float* xch = reinterpret_cast<float*>(smem + C::RING);  // [3][XCH]
+    const int kp = kperm<D>(g);
+    const int kc0 = kperm<D>(2 * t), kc1 = kperm<D>(2 * t + 1);
+    // which of the two keys is read first, so that a phase's rows lie in different banks
+    const int swap = D == 128 ? (g & 1) : ((g >> 1) & 1);
+    const int vr0 = swap ? kc1 : kc0, vr1 = swap ? kc0 : kc1;
+    const uint32_t sel_lo = swap ? 0x1504u : 0x5140u, sel_hi = swap ? 0x3726u : 0x7362u;
+    int it = 0;       // blocks through the ring so far
+    int rounds = 0;   // merges so far
+    for (int k = 0;; ++k) {
+        if (!warp_wait_all(&bar_unit[k % kUnits], (k / kUnits) & 1, wd, kSiteCacheFull)) return;
+        const Unit& un = s_unit[k % kUnits];
+        if (un.J == 0) return;
+        const int rows = min(un.nq * p.G - un.row0, p.rows_cta);
+        // element offset of query row r's o row, and its lse
+        auto out_off = [&](int r) {
+            const int i = (un.row0 + r) / p.G, h = (un.row0 + r) - i * p.G;
+            return (static_cast<long long>(un.q0 + i) * p.H + un.hk * p.G + h) * D;
+        };
+        auto stat_off = [&](int r) {
+            const int i = (un.row0 + r) / p.G, h = (un.row0 + r) - i * p.G;
+            return static_cast<long long>(un.hk * p.G + h) * p.total_q + un.q0 + i;
+        };
+        // last key that query row r of the tile sees (-1: none, or no such row)
+        auto limit = [&](int r) {
+            r += tile * TR;
+            if (r >= rows) return -1;
+            return p.causal ? min(un.nk - 1, (un.row0 + r) / p.G + un.nk - un.nq) : un.nk - 1;
+        };
+        uint32_t qb[NR][KS][2];    // query row 8 n + g, the thread's elements
+        float cx[NR][2];           // rows 8 n + 2 t + e: logit (base 2) per unit of the product
+        int lim[NR][2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int r = tile * 16 + g + 8 * h;
-            const bool on = (h < NH) && r < rows;
+        for (int n = 0; n < NR; ++n) {
+            const int r = tile * TR + 8 * n + g;
             float f[CH][16];
             float mx = 0.0f;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
-                if (on) {
+                if (r < rows) {
                     const long long off = out_off(r) + 64 * c + 16 * t;
                     if (in_extent(off, 16, p.q_ext, p.status)) {
                         w[0] = reinterpret_cast<const uint4*>(p.q + off)[0];
@@ -288,400 +442,489 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
             // 2^a brings the row's largest magnitude to [2^14, 2^15)
             const int a = min(14 + 127 - static_cast<int>(__float_as_uint(mx) >> 23), 126);
             const float up = __uint_as_float(static_cast<uint32_t>(127 + a) << 23);
-            const float down = __uint_as_float(static_cast<uint32_t>(127 - a) << 23);
+            const float down = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - a) << 23);
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    qa[4 * c + s][h] = pack_f16x2(f[c][4 * s] * up, f[c][4 * s + 1] * up);
-                    qa[4 * c + s][2 + h] = pack_f16x2(f[c][4 * s + 2] * up, f[c][4 * s + 3] * up);
-                }
-            if (h < NH) {
-                cx[h] = p.scale_log2 * down;
-                lim[h] = -1;
-                if (on) lim[h] = p.causal ? min(nk - 1, (row0 + r) / p.G + shift) : nk - 1;
+                for (int s = 0; s < 4; ++s)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        qb[n][4 * c + s][i] =
+                            pack_f16x2(f[c][4 * s + 2 * i] * up, f[c][4 * s + 2 * i + 1] * up);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                cx[n][e] = __shfl_sync(0xffffffffu, down, 4 * (2 * t + e));
+                lim[n][e] = limit(8 * n + 2 * t + e);
             }
         }
         // keys past `most` are seen by no row of the tile; up to `least` by every row of it
-        int most = -1, least = nk - 1;
-        {
-            const int r_first = row0 + tile * 16, r_last = row0 + min(tile * 16 + 16, rows) - 1;
-            if (tile * 16 < rows) {
-                most = p.causal ? min(nk - 1, r_last / p.G + shift) : nk - 1;
-                if (p.causal) least = min(least, r_first / p.G + shift);
-            }
+        int most = -1, least = un.nk - 1;
+        if (tile * TR < rows) {
+            most = limit(min(TR, rows - tile * TR) - 1);
+            least = limit(0);
         }
-        float o[NT][4];
+        float o[NR][MT][4];
+        float M[NR][2], m[NR][2], l[NR][2];
 #pragma unroll
-        for (int j = 0; j < NT; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-        float M[NH], m[NH], l[NH];
+        for (int n = 0; n < NR; ++n) {
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
-            M[h] = m[h] = -INFINITY;
-            l[h] = 0.0f;
+            for (int i = 0; i < MT; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.0f;
+            M[n][0] = M[n][1] = m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.0f;
         }
-        const int kp = kperm<D>(g);
-        const int kc0 = D == 128 ? t : 2 * t, kc1 = D == 128 ? t + 4 : 2 * t + 1;  // columns 2t, 2t+1
-        // which of the two keys is read first, so that a phase's rows lie in different banks
-        const int swap = D == 128 ? (g & 1) : ((g >> 1) & 1);
-        const int vr0 = swap ? kc1 : kc0, vr1 = swap ? kc0 : kc1;
-        const uint32_t sel_lo = swap ? 0x1504u : 0x5140u, sel_hi = swap ? 0x3726u : 0x7362u;
 
-        bool ok = true;
-        for (int jj = 0; jj < J; ++jj) {
-            const int s = jj % C::STAGES;
-            if (!warp_wait_all(&bar_full[s], (jj / C::STAGES) & 1, wd, kSiteCacheFull)) {
-                ok = false;
-                break;
-            }
-            const int valid = s_valid[s];
-            const uint8_t* kt = smem + s * 2 * C::TILE;
+        // U 16-key steps of block `block` at once, gi and gi + gap.  MASKED: the step's keys may lie past
+        // the end or be hidden from some rows.
+        auto step = [&](auto masked_c, auto u_c, const uint8_t* kt, const uint8_t* ex, int block, int gi,
+                        int gap) {
+            constexpr bool MASKED = decltype(masked_c)::value;
+            constexpr int U = decltype(u_c)::value;
             const uint8_t* vt = kt + C::TILE;
-            const uint8_t* ex = smem + C::EXP0 + s * 2 * kKB;
-            for (int gi = slot; gi < 4; gi += slots) {
-                const int kbase = (jb + jj) * kKB + gi * 16;
-                if (!(valid >> gi & 1) || kbase > most) continue;
-                // ---- S
-                float sc[2][CH][4];
+            // ---- S^T
+            float sc[U][NR][4];
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
-                    const int row = gi * 16 + nt * 8 + kp;
+            for (int u = 0; u < U; ++u) {
+                float part[CH][NR][4];
 #pragma unroll
-                    for (int c = 0; c < CH; ++c) {
+                for (int c = 0; c < CH; ++c) {
+                    uint32_t w[2][4];
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int row = (gi + u * gap) * 16 + hf * 8 + kp;
                         const int phys = D == 128 ? ((t + 4 * c) ^ (row & 7)) : (t ^ ((row >> 1) & 3));
-                        const uint4 w = *reinterpret_cast<const uint4*>(kt + row * D + 16 * phys);
-                        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                        float* a = sc[nt][c];
-                        a[0] = a[1] = a[2] = a[3] = 0.0f;
+                        const uint4 x = *reinterpret_cast<const uint4*>(kt + row * D + 16 * phys);
+                        w[hf][0] = x.x; w[hf][1] = x.y; w[hf][2] = x.z; w[hf][3] = x.w;
+                    }
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma16816(a, qa[4 * c + k], e4m3x2_to_f16x2(u[k]), e4m3x2_to_f16x2(u[k] >> 16));
+                    for (int n = 0; n < NR; ++n)
+                        part[c][n][0] = part[c][n][1] = part[c][n][2] = part[c][n][3] = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t a[4] = {e4m3x2_to_f16x2(w[0][k]), e4m3x2_to_f16x2(w[1][k]),
+                                               e4m3x2_to_f16x2(w[0][k] >> 16), e4m3x2_to_f16x2(w[1][k] >> 16)};
+#pragma unroll
+                        for (int n = 0; n < NR; ++n)
+                            mma16816(part[c][n], a, qb[n][4 * c + k][0], qb[n][4 * c + k][1]);
                     }
                 }
-                // ---- V's words, loaded early
-                uint32_t va[2][2][D / 32];  // [key half][first, second row][word]
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sc[u][n][i] = CH == 2 ? part[0][n][i] + part[CH - 1][n][i] : part[0][n][i];
+            }
+            // ---- logits x, and x plus V's exponent
+            float x[U][NR][4], tv[U][NR][4];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int key = (gi + u * gap) * 16 + hf * 8 + kp;
+                    const float ks = exp_byte_scale(ex[key]);
+                    const float ev = exp_byte_log2(ex[kKB + key]);
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float v = sc[u][n][2 * hf + e] * (cx[n][e] * ks);
+                            float w = v + ev;
+                            if (MASKED && block * kKB + key > lim[n][e]) v = w = -INFINITY;
+                            x[u][n][2 * hf + e] = v;
+                            tv[u][n][2 * hf + e] = w;
+                        }
+                }
+            bool need = false;
+            float xm[NR][2], tm[NR][2];
+#pragma unroll
+            for (int n = 0; n < NR; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    xm[n][e] = fmaxf(x[0][n][e], x[0][n][2 + e]);
+                    tm[n][e] = fmaxf(tv[0][n][e], tv[0][n][2 + e]);
+                    if constexpr (U == 2) {
+                        xm[n][e] = fmax3(xm[n][e], x[U - 1][n][e], x[U - 1][n][2 + e]);
+                        tm[n][e] = fmax3(tm[n][e], tv[U - 1][n][e], tv[U - 1][n][2 + e]);
+                    }
+                    need = need || xm[n][e] > m[n][e] + kGrow || tm[n][e] > M[n][e] + kGrow;
+                }
+            if (__any_sync(0xffffffffu, need)) {
+#pragma unroll
+                for (int n = 0; n < NR; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        // m frames this thread's own sum; M is the row's, shared by its lanes
+                        if (xm[n][e] > m[n][e] + kGrow) {
+                            l[n][e] *= ex2(m[n][e] - xm[n][e]);
+                            m[n][e] = xm[n][e];
+                        }
+                        float r = tm[n][e];
+                        r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 4));
+                        r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 8));
+                        r = fmaxf(r, __shfl_xor_sync(0xffffffffu, r, 16));
+                        if (r > M[n][e] + kGrow) {
+                            const float alpha = ex2(M[n][e] - r);
+                            M[n][e] = r;
+#pragma unroll
+                            for (int i = 0; i < MT; ++i) {
+                                o[n][i][e] *= alpha;
+                                o[n][i][2 + e] *= alpha;
+                            }
+                        }
+                    }
+            }
+            uint32_t pb[U][NR][2];
+#pragma unroll
+            for (int n = 0; n < NR; ++n) {
+                float nm[2], nM[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    nm[e] = m[n][e] == -INFINITY ? 0.0f : m[n][e];
+                    nM[e] = (M[n][e] == -INFINITY ? 0.0f : M[n][e]) - kFrame;
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) l[n][e] += ex2(x[u][n][2 * hf + e] - nm[e]);
+                        pb[u][n][hf] = transpose8x8(pack_f16x2(ex2(tv[u][n][2 * hf] - nM[0]),
+                                                               ex2(tv[u][n][2 * hf + 1] - nM[1])));
+                    }
+            }
+            // ---- V's words
+            uint32_t va[U][2][2][VW];  // [step][key half][first, second row][word]
+#pragma unroll
+            for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
                     for (int f = 0; f < 2; ++f) {
-                        const int row = gi * 16 + hf * 8 + (f ? vr1 : vr0);
+                        const int row = (gi + u * gap) * 16 + hf * 8 + (f ? vr1 : vr0);
                         if constexpr (D == 128) {
-                            const uint4 w = *reinterpret_cast<const uint4*>(vt + row * D + 16 * (g ^ (row & 7)));
-                            va[hf][f][0] = w.x; va[hf][f][1] = w.y; va[hf][f][2] = w.z; va[hf][f][3] = w.w;
+                            const uint4 x = *reinterpret_cast<const uint4*>(vt + row * D + 16 * (g ^ (row & 7)));
+                            va[u][hf][f][0] = x.x; va[u][hf][f][1] = x.y;
+                            va[u][hf][f][2] = x.z; va[u][hf][f][3] = x.w;
                         } else {
-                            const uint2 w = *reinterpret_cast<const uint2*>(
+                            const uint2 x = *reinterpret_cast<const uint2*>(
                                 vt + row * D + 16 * ((g >> 1) ^ ((row >> 1) & 3)) + 8 * (g & 1));
-                            va[hf][f][0] = w.x; va[hf][f][1] = w.y;
+                            va[u][hf][f][0] = x.x; va[u][hf][f][1] = x.y;
                         }
                     }
-                // ---- softmax weights
-                const bool masked = kbase + 15 > least;
-                float x[NH][4], tv[NH][4];  // logits; logits plus V's exponent
+            if constexpr (MASKED) {
+                // Rows past the sequence's end hold whatever the page held: zero them.  NaN codes
+                // of rows that only some queries see must not reach the others (0 * NaN): they are
+                // taken out of the product, and the rows that do see them get NaN by a product of
+                // indicators.
+                const int kbase = block * kKB + gi * 16;
+                bool bad = false;
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int key = gi * 16 + nt * 8 + (e ? kc1 : kc0);
-                        const float ks = exp_byte_scale(ex[key]);
-                        const uint32_t vb = ex[kKB + key];
-                        const float ev = vb == 255 ? NAN : static_cast<float>(static_cast<int>(vb) - 127);
+                    for (int f = 0; f < 2; ++f) {
+                        const int key = kbase + hf * 8 + (f ? vr1 : vr0);
 #pragma unroll
-                        for (int h = 0; h < NH; ++h) {
-                            float sum = sc[nt][0][2 * h + e];
-                            if constexpr (CH == 2) sum += sc[nt][1][2 * h + e];
-                            float v = sum * (cx[h] * ks);
-                            float w = v + ev;
-                            if (masked && (jb + jj) * kKB + key > lim[h]) v = w = -INFINITY;
-                            x[h][2 * nt + e] = v;
-                            tv[h][2 * nt + e] = w;
+                        for (int i = 0; i < VW; ++i) {
+                            if (key >= un.nk) va[0][hf][f][i] = 0u;
+                            bad = bad || nan_bytes(va[0][hf][f][i]);
                         }
                     }
-                float xm[NH], tm[NH];
-                bool need = false;
+                if (__any_sync(0xffffffffu, bad)) {
 #pragma unroll
-                for (int h = 0; h < NH; ++h) {
-                    xm[h] = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
-                    tm[h] = fmaxf(fmaxf(tv[h][0], tv[h][1]), fmaxf(tv[h][2], tv[h][3]));
-                    tm[h] = fmaxf(tm[h], __shfl_xor_sync(0xffffffffu, tm[h], 1));
-                    tm[h] = fmaxf(tm[h], __shfl_xor_sync(0xffffffffu, tm[h], 2));
-                    need = need || xm[h] > m[h] + kGrow || tm[h] > M[h] + kGrow;
-                }
-                if (__any_sync(0xffffffffu, need)) {
+                    for (int i = 0; i < VW; ++i) {
+                        uint32_t z[2][2];
 #pragma unroll
-                    for (int h = 0; h < NH; ++h) {
-                        if (xm[h] > m[h] + kGrow) {
-                            l[h] *= ex2(m[h] - xm[h]);
-                            m[h] = xm[h];
-                        }
-                        if (tm[h] > M[h] + kGrow) {
-                            const float alpha = ex2(M[h] - tm[h]);
-                            M[h] = tm[h];
+                        for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-                            for (int j = 0; j < NT; ++j) {
-                                o[j][2 * h] *= alpha;
-                                o[j][2 * h + 1] *= alpha;
-                            }
-                        }
-                    }
-                }
-                uint32_t pa[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-                for (int h = 0; h < NH; ++h) {
-                    const float nm = m[h] == -INFINITY ? 0.0f : m[h];
-                    const float nM = (M[h] == -INFINITY ? 0.0f : M[h]) - kFrame;
-                    float w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        l[h] += ex2(x[h][e] - nm);
-                        w[e] = ex2(tv[h][e] - nM);
-                    }
-                    pa[h] = pack_f16x2(w[0], w[1]);
-                    pa[2 + h] = pack_f16x2(w[2], w[3]);
-                }
-                if (masked) {
-                    // Rows past the sequence's end hold whatever the page held: zero them.  NaN
-                    // codes of rows that only some queries see must not reach the others (0 *
-                    // NaN): they are taken out of the product, and the rows that do see them get
-                    // NaN by a product of indicators.
-                    bool bad = false;
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                        for (int f = 0; f < 2; ++f) {
-                            const int key = kbase + hf * 8 + (f ? vr1 : vr0);
-#pragma unroll
-                            for (int i = 0; i < D / 32; ++i) {
-                                if (key >= nk) va[hf][f][i] = 0u;
-                                bad = bad || nan_bytes(va[hf][f][i]);
-                            }
-                        }
-                    if (__any_sync(0xffffffffu, bad)) {
-                        uint32_t ia[4] = {0u, 0u, 0u, 0u};
-#pragma unroll
-                        for (int h = 0; h < NH; ++h)
-#pragma unroll
-                            for (int nt = 0; nt < 2; ++nt) {
-                                const int k0 = kbase + nt * 8;
-                                ia[2 * nt + h] = pack_f16x2(k0 + kc0 <= lim[h] ? 1.0f : 0.0f,
-                                                            k0 + kc1 <= lim[h] ? 1.0f : 0.0f);
+                            for (int f = 0; f < 2; ++f) {
+                                const uint32_t nb = nan_bytes(va[0][hf][f][i]) >> 7;
+                                z[hf][f] = nb * 0x38u;  // the code of 1.0 where NaN
+                                va[0][hf][f][i] &= ~(nb * 0xffu);
                             }
 #pragma unroll
-                        for (int i = 0; i < D / 32; ++i) {
-                            uint32_t n[2][2];
+                        for (int c = 0; c < 2; ++c) {
+                            const uint32_t lo = __byte_perm(z[0][0], z[0][1], c ? sel_hi : sel_lo);
+                            const uint32_t hi = __byte_perm(z[1][0], z[1][1], c ? sel_hi : sel_lo);
+                            const uint32_t a[4] = {e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16),
+                                                   e4m3x2_to_f16x2(hi), e4m3x2_to_f16x2(hi >> 16)};
 #pragma unroll
-                            for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-                                for (int f = 0; f < 2; ++f) {
-                                    const uint32_t nb = nan_bytes(va[hf][f][i]);
-                                    n[hf][f] = (nb >> 7) * 0x38u;  // the code of 1.0 where NaN
-                                    va[hf][f][i] &= ~((nb >> 7) * 0xffu);
-                                }
-                            uint32_t b2[2][2];
-#pragma unroll
-                            for (int hf = 0; hf < 2; ++hf) {
-                                b2[hf][0] = __byte_perm(n[hf][0], n[hf][1], sel_lo);
-                                b2[hf][1] = __byte_perm(n[hf][0], n[hf][1], sel_hi);
-                            }
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) {
+                            for (int n = 0; n < NR; ++n) {
+                                const int rl = limit(8 * n + g) - kbase;  // B's column is row 8 n + g
                                 float cnt[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                                const int sh = c & 1 ? 16 : 0;
-                                mma16816(cnt, ia, e4m3x2_to_f16x2(b2[0][c >> 1] >> sh),
-                                         e4m3x2_to_f16x2(b2[1][c >> 1] >> sh));
+                                mma16816(cnt, a,
+                                         pack_f16x2(kc0 <= rl ? 1.0f : 0.0f, kc1 <= rl ? 1.0f : 0.0f),
+                                         pack_f16x2(8 + kc0 <= rl ? 1.0f : 0.0f, 8 + kc1 <= rl ? 1.0f : 0.0f));
 #pragma unroll
                                 for (int e = 0; e < 4; ++e)
-                                    if (cnt[e] > 0.0f) o[4 * i + c][e] = NAN;
+                                    if (cnt[e] > 0.0f) o[n][2 * i + c][e] = NAN;
                             }
                         }
-                    }
-                }
-                // ---- O += P V
-#pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
-                    uint32_t b2[2][2];
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        b2[hf][0] = __byte_perm(va[hf][0][i], va[hf][1][i], sel_lo);
-                        b2[hf][1] = __byte_perm(va[hf][0][i], va[hf][1][i], sel_hi);
-                    }
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int sh = c & 1 ? 16 : 0;
-                        mma16816(o[4 * i + c], pa, e4m3x2_to_f16x2(b2[0][c >> 1] >> sh),
-                                 e4m3x2_to_f16x2(b2[1][c >> 1] >> sh));
                     }
                 }
             }
+            // ---- O^T += V^T P^T
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < VW; ++i)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const uint32_t lo = __byte_perm(va[u][0][0][i], va[u][0][1][i], c ? sel_hi : sel_lo);
+                        const uint32_t hi = __byte_perm(va[u][1][0][i], va[u][1][1][i], c ? sel_hi : sel_lo);
+                        const uint32_t a[4] = {e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16),
+                                               e4m3x2_to_f16x2(hi), e4m3x2_to_f16x2(hi >> 16)};
+#pragma unroll
+                        for (int n = 0; n < NR; ++n) mma16816(o[n][2 * i + c], a, pb[u][n][0], pb[u][n][1]);
+                    }
+        };
+
+        const int j1 = un.jb + un.J;
+        for (int j = un.jb; j < j1; ++j, ++it) {
+            const int s = it % C::STAGES;
+            if (!warp_wait_all(&bar_full[s], (it / C::STAGES) & 1, wd, kSiteCacheFull)) return;
+            const int valid = s_valid[s];
+            const uint8_t* kt = smem + s * 2 * C::TILE;
+            const uint8_t* ex = smem + C::EXP0 + s * 2 * kKB;
+            // steps in the clear go U at a time
+            constexpr int U = NR == 1 ? 2 : 1;
+            if (most >= 0)  // (else there is no query row in this warp's tile)
+                for (int gi = slot; gi < kKB / 16; gi += U * slots) {
+                    const int last = gi + (U - 1) * slots;
+                    if ((valid >> gi & 1) && (valid >> last & 1) && j * kKB + last * 16 + 15 <= least) {
+                        step(std::false_type{}, std::integral_constant<int, U>{}, kt, ex, j, gi, slots);
+                    } else {
+                        for (int i = gi; i <= last; i += slots)
+                            if ((valid >> i & 1) && j * kKB + i * 16 <= most)
+                                step(std::true_type{}, std::integral_constant<int, 1>{}, kt, ex, j, i, slots);
+                    }
+                }
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_empty[s]);
         }
-        if (!ok) *ok_flag = 1;
-        // every copy has landed and every warp is past the ring: it becomes the merge buffer
-        __syncthreads();
+        // ---- merge of the warps of a tile into its slot 0: slots 2, 3 into 0, 1, then 1 into 0
+        // (two slots: one round; a chain of three hand-overs to slot 0 took 700 clocks longer).
+        // Threads of the same lane hold the same elements.
 #pragma unroll
-        for (int h = 0; h < NH; ++h) {
-            // the quad's sums in one frame
-            float mm = fmaxf(m[h], __shfl_xor_sync(0xffffffffu, m[h], 1));
-            mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, 2));
-            float ll = l[h] * (m[h] == -INFINITY ? (l[h] == 0.0f ? 0.0f : 1.0f) : ex2(m[h] - mm));
-            ll += __shfl_xor_sync(0xffffffffu, ll, 1);
-            ll += __shfl_xor_sync(0xffffffffu, ll, 2);
-            const int r = warp * 16 + g + 8 * h;
-            if (t == 0) {
-                sStat[3 * r] = M[h];
-                sStat[3 * r + 1] = mm;
-                sStat[3 * r + 2] = ll;
+        for (int n = 0; n < NR; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                // the row's sums of its eight lanes in one frame
+                float mm = m[n][e];
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, d));
+                float ll = l[n][e] * (m[n][e] == -INFINITY ? 1.0f : ex2(m[n][e] - mm));
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2) ll += __shfl_xor_sync(0xffffffffu, ll, d);
+                m[n][e] = mm;
+                l[n][e] = ll;
             }
-            float* dst = sO + r * C::OLD + (D / 4) * t;  // columns [D / 4 * t, D / 4 * (t + 1))
+            auto give = [&](int i) {
+                if (!warp_wait_all(&bar_taken[i], (rounds & 1) ^ 1, wd, kSiteCacheMerge)) return false;
+                float* x = xch + i * C::XCH;
 #pragma unroll
-            for (int e = 0; e < 2; ++e)
+                for (int e = 0; e < 2; ++e) {
+                    float* row = x + (2 * t + e) * C::OLD;
 #pragma unroll
-                for (int j = 0; j < NT; j += 4)
-                    *reinterpret_cast<float4*>(dst + e * NT + j) =
-                        make_float4(o[j][2 * h + e], o[j + 1][2 * h + e], o[j + 2][2 * h + e], o[j + 3][2 * h + e]);
-        }
-    }
-    __syncthreads();
-    if (*static_cast<volatile int*>(ok_flag)) return;  // a wait gave up: nothing is written
-    // ------------------------------------------------------------- merge of the warps, stores
-    const int slots = kComputeWarps / p.row_tiles;
-    for (int i = threadIdx.x; i < rows * (D / 4); i += C::THREADS) {
-        const int r = i / (D / 4), c4 = i % (D / 4);
-        const int tile = r / 16, rr = r % 16;
-        float mm = -INFINITY, MM = -INFINITY;
-        for (int k = 0; k < slots; ++k) {
-            const float* st = sStat + 3 * ((tile + k * p.row_tiles) * 16 + rr);
-            MM = fmaxf(MM, st[0]);
-            mm = fmaxf(mm, st[1]);
-        }
-        float l = 0.0f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int k = 0; k < slots; ++k) {
-            const int wr = (tile + k * p.row_tiles) * 16 + rr;
-            const float* st = sStat + 3 * wr;
-            const float wl = st[1] == -INFINITY ? 1.0f : ex2(st[1] - mm);
-            const float wo = st[0] == -INFINITY ? 1.0f : ex2(st[0] - MM);
-            const float4 v = *reinterpret_cast<const float4*>(sO + wr * C::OLD + 4 * c4);
-            l = fmaf(wl, st[2], l);
-            acc.x = fmaf(wo, v.x, acc.x);
-            acc.y = fmaf(wo, v.y, acc.y);
-            acc.z = fmaf(wo, v.z, acc.z);
-            acc.w = fmaf(wo, v.w, acc.w);
-        }
-        // O = acc 2^(MM - frame) / (l 2^mm); a row that saw no key has l = 0.  The power is
-        // applied in halves: each is representable where the whole may not be.
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-        const float half = (MM == -INFINITY || mm == -INFINITY) ? 1.0f : ex2(0.5f * (MM - kFrame - mm));
-        const float f0 = inv * half;
-        acc = make_float4(acc.x * f0 * half, acc.y * f0 * half, acc.z * f0 * half, acc.w * f0 * half);
-        const float lse = l == 0.0f ? -INFINITY : (mm + log2f(l)) * kLn2;
-        const long long off = out_off(r) + 4 * c4, so = stat_off(r);
-        if (p.splits == 1) {
-            if (in_extent(off, 4, p.q_ext, p.status))
-                *reinterpret_cast<uint2*>(p.o + off) =
-                    make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-            if (c4 == 0 && p.lse != nullptr && in_extent(so, 1, p.stat_ext, p.status)) p.lse[so] = lse;
-        } else {
-            const long long po = static_cast<long long>(split) * p.total_q * p.H * D + off;
-            if (in_extent(po, 4, p.part_ext, p.status)) *reinterpret_cast<float4*>(p.o_part + po) = acc;
-            if (c4 == 0 && in_extent(part_stat + so, 1, p.part_ext / D, p.status))
-                p.lse_part[part_stat + so] = lse;
+                    for (int i = 0; i < MT; i += 2)
+                        *reinterpret_cast<float4*>(row + 2 * MT * g + 2 * i) =
+                            make_float4(o[n][i][e], o[n][i][2 + e], o[n][i + 1][e], o[n][i + 1][2 + e]);
+                    if (g == 0) {
+                        float* st = x + 8 * C::OLD + 3 * (2 * t + e);
+                        st[0] = M[n][e];
+                        st[1] = m[n][e];
+                        st[2] = l[n][e];
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar_given[i]);
+                return true;
+            };
+            auto take = [&](int i) {
+                if (!warp_wait_all(&bar_given[i], rounds & 1, wd, kSiteCacheMerge)) return false;
+                const float* x = xch + i * C::XCH;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float* st = x + 8 * C::OLD + 3 * (2 * t + e);
+                    const float M2 = fmaxf(M[n][e], st[0]), m2 = fmaxf(m[n][e], st[1]);
+                    const float fa = M[n][e] == -INFINITY ? 1.0f : ex2(M[n][e] - M2);
+                    const float fb = st[0] == -INFINITY ? 1.0f : ex2(st[0] - M2);
+                    l[n][e] = l[n][e] * (m[n][e] == -INFINITY ? 1.0f : ex2(m[n][e] - m2)) +
+                              st[2] * (st[1] == -INFINITY ? 1.0f : ex2(st[1] - m2));
+                    M[n][e] = M2;
+                    m[n][e] = m2;
+                    const float* row = x + (2 * t + e) * C::OLD;
+#pragma unroll
+                    for (int i = 0; i < MT; i += 2) {
+                        const float4 v = *reinterpret_cast<const float4*>(row + 2 * MT * g + 2 * i);
+                        o[n][i][e] = o[n][i][e] * fa + v.x * fb;
+                        o[n][i][2 + e] = o[n][i][2 + e] * fa + v.y * fb;
+                        o[n][i + 1][e] = o[n][i + 1][e] * fa + v.z * fb;
+                        o[n][i + 1][2 + e] = o[n][i + 1][2 + e] * fa + v.w * fb;
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar_taken[i]);
+                return true;
+            };
+            if (slots > 1) {
+                if (2 * slot >= slots) {
+                    if (!give(warp & 1)) return;
+                } else {
+                    if (!take(warp & 1)) return;
+                    if (slots == 4 && (slot == 1 ? !give(2) : !take(2))) return;
+                }
+                ++rounds;
+            }
+            if (slot != 0) continue;
+            // ---- O = o 2^(M - frame) / (l 2^m); a row that saw no key has l = 0.  The power is
+            // applied in halves: each is representable where the whole may not be.
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = tile * TR + 8 * n + 2 * t + e;
+                if (r >= rows) continue;
+                const float inv = l[n][e] == 0.0f ? 0.0f : 1.0f / l[n][e];
+                const float half = (M[n][e] == -INFINITY || m[n][e] == -INFINITY)
+                                       ? 1.0f : ex2(0.5f * (M[n][e] - kFrame - m[n][e]));
+                const float lse = l[n][e] == 0.0f ? -INFINITY : (m[n][e] + log2f(l[n][e])) * kLn2;
+                const float f0 = inv * half;
+                float v[2 * MT];
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    v[2 * i] = o[n][i][e] * f0 * half;
+                    v[2 * i + 1] = o[n][i][2 + e] * f0 * half;
+                }
+                if (un.J == un.nblk) {
+                    const long long off = out_off(r) + 2 * MT * g, so = stat_off(r);
+                    if (in_extent(off, 2 * MT, p.q_ext, p.status)) {
+#pragma unroll
+                        for (int i = 0; i < 2 * MT; i += 8)
+                            *reinterpret_cast<uint4*>(p.o + off + i) =
+                                make_uint4(pack_bf16x2(v[i], v[i + 1]), pack_bf16x2(v[i + 2], v[i + 3]),
+                                           pack_bf16x2(v[i + 4], v[i + 5]), pack_bf16x2(v[i + 6], v[i + 7]));
+                    }
+                    if (g == 0 && p.lse != nullptr && in_extent(so, 1, p.stat_ext, p.status)) p.lse[so] = lse;
+                } else {
+                    const long long pr = static_cast<long long>(2 * cta + (un.flags & kFirst ? 0 : 1)) * p.rows_cta + r;
+                    const long long off = pr * D + 2 * MT * g;
+                    if (in_extent(off, 2 * MT, p.part_ext, p.status)) {
+#pragma unroll
+                        for (int i = 0; i < 2 * MT; i += 4)
+                            *reinterpret_cast<float4*>(p.o_part + off + i) =
+                                make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                    }
+                    if (g == 0 && in_extent(pr, 1, p.part_ext / D, p.status)) p.lse_part[pr] = lse;
+                }
+            }
         }
     }
 }
 
-// Merge of the ranges of every (query, head) row, one warp each:
+// Merge of the parts of every unit that several shares cut: CTA c takes the unit that the border
+// between shares c and c + 1 cuts, if that is the unit's first cut; a warp takes a query row:
 //     O = sum_s e^{lse_s} O_s / sum_s e^{lse_s},   lse = log sum_s e^{lse_s}.
-// Only ranges that saw a key (lse_s > -inf) are read; a row without any gets O = 0, lse = -inf.
-// Rows that belong to no sequence are left as they are.
+// Only parts that saw a key (lse_s > -inf) are read; a row without any gets O = 0, lse = -inf.
+// It is always launched behind the attention kernel of its call, whose CTAs let it start only after
+// their own wait: so the lengths, which that wait has made visible, are read before this kernel's.
 template <int D>
-__global__ void __launch_bounds__(256) fa_decode_merge_kernel(const MergeParams p)
+__global__ void __launch_bounds__(kMergeThreads) fa_decode_cache_merge_kernel(const CacheDecodeParams p)
 {
     constexpr int EPL = D / 32;
-    constexpr int BATCH = 4;  // ranges whose rows are in flight together
-    dependent_begin();
+    constexpr int BATCH = 4;  // parts whose rows are in flight together
     const int lane = threadIdx.x & 31;
-    const int w = static_cast<int>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    const int h = w % p.H;
-    const int i = w / p.H % p.max_q, b = w / p.H / p.max_q;
-    if (b >= p.B) return;
-    int q0;
-    const int nq = packed_rows(p.cu_q, b, p.total_q, p.max_q, q0);
-    if (i >= nq) return;
-    const long long stat = static_cast<long long>(h) * p.total_q + q0 + i;
-    const long long row = (static_cast<long long>(q0 + i) * p.H + h) * D + EPL * lane;
-    const long long stat_step = static_cast<long long>(p.H) * p.total_q;
-    float mx = -INFINITY, sum = 0.0f, acc[EPL];
+    const int c0 = static_cast<int>(blockIdx.x);
+    Unit u;
+    int at = 0;
+    // the first place of share c0 + 1
+    const Shares sh = find_share(p, c0 + 1, u, at);
+    const int border = sh.start(c0 + 1);
+    const bool cut = border < sh.total;
+    const int ui = cut ? at / (u.nblk + kUnitCost) : 0;
+    const int j = cut ? at - ui * (u.nblk + kUnitCost) : 0;
+    const int start = border - j + kUnitCost;  // the place of the unit's first block
+    // not cut here (no border between two of the unit's blocks), or cut before (share c0 starts
+    // inside them): every CTA waits all the same, so that this grid ends after the attention
+    if (!cut || j <= kUnitCost || sh.start(c0) > start) {
+        dependent_begin();
+        return;
+    }
+    unit_at(p, ui, u);
+    const int c1 = sh.share_of(start + u.nblk - 1);  // the last share in it
+    const int rows = min(u.nq * p.G - u.row0, p.rows_cta);
+    const int parts = c1 - c0 + 1;
+    // share c0's part is its last unit, which is also its first if the share starts in its places
+    const int lead = sh.start(c0) >= start - kUnitCost ? 0 : 1;
+    dependent_begin();
+    const int r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);
+    if (r < rows) {
+        float mx = -INFINITY, sum = 0.0f, acc[EPL];
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) acc[e] = 0.0f;
-    for (int s0 = 0; s0 < p.splits; s0 += 32) {
-        float ls = -INFINITY;
-        if (s0 + lane < p.splits && in_extent((s0 + lane) * stat_step + stat, 1, p.part_ext / D, p.status))
-            ls = p.lse_part[(s0 + lane) * stat_step + stat];
-        float bm = ls;
-        uint32_t live = __ballot_sync(0xffffffffu, !(ls == -INFINITY));  // NaN counts
+        for (int e = 0; e < EPL; ++e) acc[e] = 0.0f;
+        auto row_of = [&](int k) {
+            return static_cast<long long>(2 * (c0 + k) + (k == 0 ? lead : 0)) * p.rows_cta + r;
+        };
+        for (int s0 = 0; s0 < parts; s0 += 32) {
+            float ls = -INFINITY;
+            if (s0 + lane < parts && in_extent(row_of(s0 + lane), 1, p.part_ext / D, p.status))
+                ls = p.lse_part[row_of(s0 + lane)];
+            float bm = ls;
+            uint32_t live = __ballot_sync(0xffffffffu, !(ls == -INFINITY));  // NaN counts
 #pragma unroll
-        for (int d = 16; d; d >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, d));
-        if (!live) continue;
-        const float nm = fmaxf(mx, bm);
-        const float keep = mx == -INFINITY ? 0.0f : expf(mx - nm);
-        sum *= keep;
+            for (int d = 16; d; d >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, d));
+            if (!live) continue;
+            const float nm = fmaxf(mx, bm);
+            const float keep = mx == -INFINITY ? 0.0f : expf(mx - nm);
+            sum *= keep;
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) acc[e] *= keep;
-        mx = nm;
-        const float wt = ls == -INFINITY ? 0.0f : expf(ls - nm);
-        while (live) {
-            float v[BATCH][EPL], ws[BATCH];
+            for (int e = 0; e < EPL; ++e) acc[e] *= keep;
+            mx = nm;
+            const float wt = ls == -INFINITY ? 0.0f : expf(ls - nm);
+            while (live) {
+                float v[BATCH][EPL], ws[BATCH];
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                ws[k] = 0.0f;
+                for (int k = 0; k < BATCH; ++k) {
+                    ws[k] = 0.0f;
 #pragma unroll
-                for (int e = 0; e < EPL; ++e) v[k][e] = 0.0f;
-                if (live) {
-                    const int s = __ffs(live) - 1;
-                    live &= live - 1;
-                    ws[k] = __shfl_sync(0xffffffffu, wt, s);
-                    const long long po = (s0 + s) * stat_step * D + row;
-                    if (in_extent(po, EPL, p.part_ext, p.status)) {
-                        if constexpr (EPL == 4) {
-                            const float4 x = *reinterpret_cast<const float4*>(p.o_part + po);
-                            v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
-                        } else {
-                            const float2 x = *reinterpret_cast<const float2*>(p.o_part + po);
-                            v[k][0] = x.x; v[k][1] = x.y;
+                    for (int e = 0; e < EPL; ++e) v[k][e] = 0.0f;
+                    if (live) {
+                        const int s = __ffs(live) - 1;
+                        live &= live - 1;
+                        ws[k] = __shfl_sync(0xffffffffu, wt, s);
+                        const long long po = row_of(s0 + s) * D + EPL * lane;
+                        if (in_extent(po, EPL, p.part_ext, p.status)) {
+                            if constexpr (EPL == 4) {
+                                const float4 x = *reinterpret_cast<const float4*>(p.o_part + po);
+                                v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+                            } else {
+                                const float2 x = *reinterpret_cast<const float2*>(p.o_part + po);
+                                v[k][0] = x.x; v[k][1] = x.y;
+                            }
                         }
                     }
                 }
-            }
 #pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                sum += ws[k];
+                for (int k = 0; k < BATCH; ++k) {
+                    sum += ws[k];
 #pragma unroll
-                for (int e = 0; e < EPL; ++e) acc[e] = fmaf(ws[k], v[k][e], acc[e]);
+                    for (int e = 0; e < EPL; ++e) acc[e] = fmaf(ws[k], v[k][e], acc[e]);
+                }
             }
         }
+        const int i = (u.row0 + r) / p.G, h = u.hk * p.G + (u.row0 + r) - i * p.G;
+        const long long row = (static_cast<long long>(u.q0 + i) * p.H + h) * D + EPL * lane;
+        const long long stat = static_cast<long long>(h) * p.total_q + u.q0 + i;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if (in_extent(row, EPL, p.q_ext, p.status)) {
+            if constexpr (EPL == 4)
+                *reinterpret_cast<uint2*>(p.o + row) = make_uint2(
+                    pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
+            else
+                *reinterpret_cast<uint32_t*>(p.o + row) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
+        }
+        if (lane == 0 && p.lse != nullptr && in_extent(stat, 1, p.stat_ext, p.status))
+            p.lse[stat] = sum == 0.0f ? -INFINITY : mx + logf(sum);
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    if (in_extent(row, EPL, p.q_ext, p.status)) {
-        if constexpr (EPL == 4)
-            *reinterpret_cast<uint2*>(p.o + row) =
-                make_uint2(pack_bf16x2(acc[0] * inv, acc[1] * inv), pack_bf16x2(acc[2] * inv, acc[3] * inv));
-        else
-            *reinterpret_cast<uint32_t*>(p.o + row) = pack_bf16x2(acc[0] * inv, acc[1] * inv);
-    }
-    if (lane == 0 && p.lse != nullptr && in_extent(stat, 1, p.stat_ext, p.status))
-        p.lse[stat] = sum == 0.0f ? -INFINITY : mx + logf(sum);
 }
 
-cudaError_t launch_decode_merge(int d, const MergeParams& p, cudaStream_t st)
-{
-    const long long rows = static_cast<long long>(p.B) * p.max_q * p.H;
-    const dim3 grid(static_cast<unsigned>((rows + 7) / 8));
-    if (d == 64) return launch_dependent(fa_decode_merge_kernel<64>, grid, dim3(256), 0, st, p);
-    return launch_dependent(fa_decode_merge_kernel<128>, grid, dim3(256), 0, st, p);
-}
-
-template <int D, bool SMALL>
+template <int D, int NR>
 static cudaError_t launch_decode_cache_impl(const CUtensorMap& tk, const CUtensorMap& tv,
                                             const CacheDecodeParams& p, cudaStream_t st)
 {
@@ -690,34 +933,27 @@ static cudaError_t launch_decode_cache_impl(const CUtensorMap& tk, const CUtenso
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 64 && !attr_set[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(fa_decode_cache_kernel<D, SMALL>,
+        cudaError_t e = cudaFuncSetAttribute(fa_decode_cache_kernel<D, NR>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
         if (e != cudaSuccess) return e;
         attr_set[dev] = true;
     }
-    const dim3 grid(static_cast<unsigned>(p.B * p.Hkv * p.row_chunks * p.splits));
-    return launch_dependent(fa_decode_cache_kernel<D, SMALL>, grid, dim3(C::THREADS), C::SMEM, st,
-                            tk, tv, p);
+    cudaError_t e = launch_dependent(fa_decode_cache_kernel<D, NR>, dim3(p.ctas), dim3(C::THREADS),
+                                     C::SMEM, st, tk, tv, p);
+    if (e != cudaSuccess || p.ctas == 1) return e;
+    return launch_dependent(fa_decode_cache_merge_kernel<D>, dim3(p.ctas - 1, p.rows_cta / (kMergeThreads / 32)), dim3(kMergeThreads), 0,
+                            st, p);
 }
 
 cudaError_t launch_decode_cache(int d, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const CacheDecodeParams& p, cudaStream_t st)
 {
-    const bool small = static_cast<long long>(p.max_q) * p.G <= 8;
-    cudaError_t e;
+    const bool small = p.rows_cta == 8;
     if (d == 64)
-        e = small ? launch_decode_cache_impl<64, true>(tk, tv, p, st)
-                  : launch_decode_cache_impl<64, false>(tk, tv, p, st);
-    else
-        e = small ? launch_decode_cache_impl<128, true>(tk, tv, p, st)
-                  : launch_decode_cache_impl<128, false>(tk, tv, p, st);
-    if (e != cudaSuccess || p.splits == 1) return e;
-    MergeParams m{};
-    m.o = p.o; m.lse = p.lse; m.o_part = p.o_part; m.lse_part = p.lse_part;
-    m.cu_q = p.cu_q; m.B = p.B; m.H = p.H; m.max_q = p.max_q; m.total_q = p.total_q;
-    m.splits = p.splits; m.q_ext = p.q_ext; m.stat_ext = p.stat_ext; m.part_ext = p.part_ext;
-    m.status = p.status;
-    return launch_decode_merge(d, m, st);
+        return small ? launch_decode_cache_impl<64, 1>(tk, tv, p, st)
+                     : launch_decode_cache_impl<64, 2>(tk, tv, p, st);
+    return small ? launch_decode_cache_impl<128, 1>(tk, tv, p, st)
+                 : launch_decode_cache_impl<128, 2>(tk, tv, p, st);
 }
 
 }  // namespace fa

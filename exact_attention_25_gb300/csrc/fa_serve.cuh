@@ -11,6 +11,7 @@ enum ServeWaitSite : int {
     kSiteCacheEmpty = 32,
     kSiteCacheFull,
     kSiteCacheDrain,
+    kSiteCacheMerge,
 };
 
 constexpr int kRopeMaxPairs = 64;
@@ -54,13 +55,22 @@ struct CacheParams {
     int* status;
 };
 
-// Split-KV decode over the paged cache.
+constexpr int kCacheBlock = 128;  // keys of a block of the cache decode
+
+// What a unit (below) costs besides its blocks (queries, merge of the warps, output), in blocks.
+constexpr int kUnitCost = 2;
+
+// Split-KV decode over the paged cache.  The work is a line of units: for every sequence, for
+// every `rows_cta` query rows of a group and every key/value head, kUnitCost places and one place
+// for each 128-key block of the sequence (at least one).  The CTAs take equal shares of that line
+// (to a place), however ragged the lengths are.  A unit whose blocks lie in one share is finished
+// by its CTA; one that several shares cut is written in parts, and merged by the next kernel.
 struct CacheDecodeParams {
     const __nv_bfloat16* q;    // [total_q, H, d]
     __nv_bfloat16* o;
     float* lse;                // [H, total_q] (may be null)
-    float* o_part;             // workspace: fp32 [splits, total_q, H, d]
-    float* lse_part;           // workspace: fp32 [splits, H, total_q]
+    float* o_part;             // workspace: fp32 [2 * ctas, rows_cta, d]; a share's first unit is
+    float* lse_part;           // its part 2 c, its last (if another) 2 c + 1; [2 * ctas, rows_cta]
     const uint8_t* ke;
     const uint8_t* ve;
     const int* cu_q;           // [B + 1]
@@ -69,26 +79,15 @@ struct CacheDecodeParams {
     int B, H, Hkv, G;          // G = H / Hkv
     int max_q, max_k, total_q;
     int max_pages, num_pages, page_shift;
-    int splits, chunk_blocks;  // ranges of a sequence, 64-key blocks of a range
-    int row_tiles, row_chunks; // 16-row tiles of a CTA, CTAs over a group's query rows
+    int ctas;
+    int row_tiles;             // row tiles of a CTA
+    int rows_cta, rows_shift;  // query rows of a CTA, and their log2
     float scale_log2;
     int causal;
     int* status;
     unsigned long long wait_limit_ns;
     int debug_flags;
     long long q_ext, stat_ext, part_ext;  // element extents (checked builds)
-};
-
-// Merge of the partial results of a decode.
-struct MergeParams {
-    __nv_bfloat16* o;          // [total_q, H, d]
-    float* lse;                // [H, total_q] (may be null)
-    const float* o_part;       // [splits, total_q, H, d]
-    const float* lse_part;     // [splits, H, total_q]
-    const int* cu_q;           // [B + 1]
-    int B, H, max_q, total_q, splits;
-    long long q_ext, stat_ext, part_ext;
-    int* status;
 };
 
 // 2^(byte - 127), the scale an exponent byte stands for; 255 is NaN.

@@ -425,24 +425,28 @@ int fa_cache_read(const void* k_cache, const void* v_cache, const void* k_exp, c
  * give O = 0 and lse = -inf) with the keys and values of the cache.  seqlens_k: device int32 [B],
  * keys of each sequence (at most max_seqlen_k are used).  Any max_seqlen_q and any H / Hkv work;
  * the kernel is made for few query rows per key/value head (up to 64 read the cache once; more
- * read it again for every 64).  A sequence's keys are split into num_splits ranges in [1, 256]
- * of ceil(ceil(max_seqlen_k / 64) / num_splits) blocks of 64 keys each, merged by a second
- * kernel; fa_decode_cache_num_splits suggests a count.  workspace: as fa_fwd_decode
- * (fa_decode_workspace_bytes(total_q, H, d, num_splits)).  Rows of o and lse that belong to no
- * sequence are left as they are. */
+ * read it again for every 64).  The batch's blocks of 128 keys are shared out evenly over num_ctas
+ * thread blocks, in [1, 4096], whatever the sequences' lengths are, and what several of them
+ * computed of one sequence and head is merged by a second kernel; fa_decode_cache_num_ctas gives
+ * the count that fills the device.  workspace: fa_decode_cache_workspace_bytes(H, Hkv, d,
+ * max_seqlen_q, num_ctas) bytes, overwritten (0 for num_ctas = 1, when it may be NULL).  Rows of o
+ * and lse that belong to no sequence are left as they are. */
 int fa_fwd_decode_cache(const void* q, const void* k_cache, const void* v_cache,
                         const void* k_exp, const void* v_exp, void* o, float* lse,
                         const int* cu_seqlens_q, const int* seqlens_k, const int* page_table,
                         int B, int max_seqlen_q, int max_seqlen_k, int total_q, int max_pages,
                         int num_pages, int page_size, int H, int Hkv, int d, float scale,
-                        int causal, int num_splits, void* workspace, size_t workspace_bytes,
+                        int causal, int num_ctas, void* workspace, size_t workspace_bytes,
                         void* stream);
 
-/* A split count for fa_fwd_decode_cache on the current device, and the rule behind it for a
- * device of num_sms SMs (host only).  Return it (>= 1) or a negative FA_ERR_* code. */
-int fa_decode_cache_num_splits(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_k);
-int fa_decode_cache_splits_for(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_k,
-                               int num_sms);
+size_t fa_decode_cache_workspace_bytes(int H, int Hkv, int d, int max_seqlen_q, int num_ctas);
+
+/* The number of thread blocks that fills the current device (two for each SM, at most one for
+ * every two blocks of keys), and the rule behind it for a device of num_sms SMs (host only).  Return it
+ * (>= 1) or a negative FA_ERR_* code. */
+int fa_decode_cache_num_ctas(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_k);
+int fa_decode_cache_ctas_for(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_k,
+                             int num_sms);
 
 #ifdef __cplusplus
 }

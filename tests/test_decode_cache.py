@@ -1,6 +1,6 @@
 """Split-KV decode over the paged e4m3 cache (fa_fwd_decode_cache) against attention in 64 bits on
 the cached values: head layouts, head sizes, page sizes, lengths from zero on, masks that leave
-rows empty, split counts; what lies behind a sequence's end and in missing pages; NaN codes that
+rows empty, thread block counts; what lies behind a sequence's end and in missing pages; NaN codes that
 only some queries see; rows far apart in size; padded batches, streams, graphs, determinism;
 refusals."""
 import ctypes
@@ -63,7 +63,7 @@ def reference(q, codes, exps, table, lens_q, lens_k, H, page, scale, causal, tok
     return ref
 
 
-def run_case(lens_q, lens_k, H, Hkv, d, page, causal, splits, seed, scale=None, spread=2):
+def run_case(lens_q, lens_k, H, Hkv, d, page, causal, ctas, seed, scale=None, spread=2):
     table, pool = table_for(lens_k, page, 1, seed)
     codes, exps = random_cache(pool, Hkv, page, d, seed, spread)
     q = torch.randn(sum(lens_q), H, d, generator=torch.Generator().manual_seed(seed)).bfloat16()
@@ -71,7 +71,7 @@ def run_case(lens_q, lens_k, H, Hkv, d, page, causal, splits, seed, scale=None, 
     got = fa.forward_decode_cache(
         q.cuda(), to_cache(codes, exps), cu(lens_q).cuda(),
         torch.tensor(lens_k, dtype=torch.int32).cuda(), table.cuda(), max(lens_q),
-        max(max(lens_k), 1), scale, causal, splits)
+        max(max(lens_k), 1), scale, causal, ctas)
     fa.fa_device_status()
     ref = reference(q, codes, exps, table, lens_q, lens_k, H, page, scale, causal)
     return _check(got, ref)
@@ -99,14 +99,14 @@ CASES = {
 
 
 @gpu
-@pytest.mark.parametrize("splits", [None, 1, 2, 3, 7])
+@pytest.mark.parametrize("ctas", [None, 1, 2, 3, 7, 29])
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("case", list(CASES))
-def test_decode_cache_against_64_bits(case, d, causal, splits):
+def test_decode_cache_against_64_bits(case, d, causal, ctas):
     lens_q, lens_k, H, Hkv, page = CASES[case]
-    worst = run_case(lens_q, lens_k, H, Hkv, d, page, causal, splits, seed=7 * len(case) + d)
-    print(case, d, causal, splits, worst)
+    worst = run_case(lens_q, lens_k, H, Hkv, d, page, causal, ctas, seed=7 * len(case) + d)
+    print(case, d, causal, ctas, worst)
 
 
 @gpu
@@ -138,9 +138,9 @@ def test_rows_of_very_different_size(d):
 
 
 @gpu
-@pytest.mark.parametrize("splits", [1, 3])
+@pytest.mark.parametrize("ctas", [1, 3])
 @pytest.mark.parametrize("d", [64, 128])
-def test_a_peaked_row_keeps_its_long_tail(d, splits):
+def test_a_peaked_row_keeps_its_long_tail(d, ctas):
     """One key far above the rest in weight and thousands of light ones: what the light ones add
     in the columns where the heavy one is zero is kept (weights are not flushed)."""
     H, Hkv, page, nk = 1, 1, 64, 4096
@@ -157,7 +157,7 @@ def test_a_peaked_row_keeps_its_long_tail(d, splits):
     q[0, 0, 0] = 8.0                         # logits +8 and -8: a weight of e^-16 each
     got = fa.forward_decode_cache(q.cuda(), to_cache(codes, exps), cu([1]).cuda(),
                                   torch.tensor([nk], dtype=torch.int32).cuda(), table.cuda(), 1,
-                                  nk, 1.0, False, splits)
+                                  nk, 1.0, False, ctas)
     ref = reference(q, codes, exps, table, [1], [nk], H, page, 1.0, False)
     assert ref[0][0, 0, 1] > 1e-4
     _check(got, ref)
@@ -179,16 +179,16 @@ def poisoned(case_seed, lens_q, lens_k, H, Hkv, d, page):
 
 
 @gpu
-@pytest.mark.parametrize("splits", [1, 2])
+@pytest.mark.parametrize("ctas", [1, 2])
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("page", [16, 64, 128])
-def test_what_lies_behind_the_end_is_not_seen(page, d, causal, splits):
+def test_what_lies_behind_the_end_is_not_seen(page, d, causal, ctas):
     lens_q, lens_k, H, Hkv = [1, 3, 2], [70, 129, 1], 4, 2
     table, codes, exps, q = poisoned(6, lens_q, lens_k, H, Hkv, d, page)
     got = fa.forward_decode_cache(q.cuda(), to_cache(codes, exps), cu(lens_q).cuda(),
                                   torch.tensor(lens_k, dtype=torch.int32).cuda(), table.cuda(), 3,
-                                  129, 0.1, causal, splits)
+                                  129, 0.1, causal, ctas)
     fa.fa_device_status()
     _check(got, reference(q, codes, exps, table, lens_q, lens_k, H, page, 0.1, causal))
 
@@ -238,8 +238,8 @@ def test_nan_of_a_late_key_reaches_only_the_queries_that_see_it(d, what):
 
 
 @gpu
-@pytest.mark.parametrize("splits", [1, 3])
-def test_missing_pages_are_left_out(splits):
+@pytest.mark.parametrize("ctas", [1, 3])
+def test_missing_pages_are_left_out(ctas):
     """Table entries outside the pool: their keys take no part, whatever the mask."""
     H, Hkv, d, page, nk = 4, 1, 128, 16, 200
     table, pool = table_for([nk], page, 0, 4)
@@ -250,7 +250,7 @@ def test_missing_pages_are_left_out(splits):
         holes[0, i] = bad
     got = fa.forward_decode_cache(q.cuda(), to_cache(codes, exps), cu([1]).cuda(),
                                   torch.tensor([nk], dtype=torch.int32).cuda(), holes.cuda(), 1,
-                                  nk, 0.1, False, splits)
+                                  nk, 0.1, False, ctas)
     fa.fa_device_status()
     keep = np.array([j for j in range(nk) if j // page not in (0, 5, 6, 12)])
     for h in range(H):
@@ -261,8 +261,8 @@ def test_missing_pages_are_left_out(splits):
 
 
 @gpu
-@pytest.mark.parametrize("splits", [1, 4])
-def test_padded_batches_guards_and_repeats(splits):
+@pytest.mark.parametrize("ctas", [1, 4])
+def test_padded_batches_guards_and_repeats(ctas):
     """Tokens before the first and behind the last sequence stay as they are, nothing outside the
     outputs and the workspace is written, and a second call gives the same bits."""
     lens_q, lens_k, H, Hkv, d, page = [2, 0, 1], [130, 9, 64], 6, 2, 64, 32
@@ -280,11 +280,11 @@ def test_padded_batches_guards_and_repeats(splits):
         lse, lw = guarded_empty((H, T), torch.float32)
         o.fill_(3.0)
         lse.fill_(4.0)
-        nbytes = fa.fa_decode_workspace_bytes(T, H, d, splits)
+        nbytes = fa.fa_decode_cache_workspace_bytes(H, Hkv, d, 2, ctas)
         ws, ww = guarded_empty((max(nbytes, 16),), torch.uint8)
         ws.fill_(0xFF)  # NaNs
         fa.fa_fwd_decode_cache(q.cuda(), cache, o, lse, starts, n, table.cuda(), 2, 130, 0.1, True,
-                               splits, ws if nbytes else None)
+                               ctas, ws if nbytes else None)
         fa.fa_device_status()
         for w in (ow, lw, ww):
             w()
@@ -311,7 +311,7 @@ def test_malformed_lengths_stay_inside():
                          ([6, 6, 0, 100], [-2 ** 31, 33, 64])):
         o, ow = guarded_empty((6, H, d), torch.bfloat16)
         lse, lw = guarded_empty((H, 6), torch.float32)
-        ws = torch.empty(fa.fa_decode_workspace_bytes(6, H, d, 3), dtype=torch.uint8).cuda()
+        ws = torch.empty(fa.fa_decode_cache_workspace_bytes(H, Hkv, d, 6, 3), dtype=torch.uint8).cuda()
         fa.fa_fwd_decode_cache(q, cache, o, lse, torch.tensor(starts, dtype=torch.int32).cuda(),
                                torch.tensor(lens, dtype=torch.int32).cuda(), table, 6, 1000, 0.1,
                                True, 3, ws)
@@ -336,7 +336,7 @@ def test_decode_cache_streams_and_graphs():
         mine = fa.PagedCache(*(t.clone() for t in cache))
         q, k, v = (torch.randn(B, h, d).bfloat16().cuda() for h in (H, Hkv, Hkv))
         o, lse = torch.empty_like(q), torch.empty(H, B, device="cuda")
-        ws = torch.empty(fa.fa_decode_workspace_bytes(B, H, d, 2), dtype=torch.uint8).cuda()
+        ws = torch.empty(fa.fa_decode_cache_workspace_bytes(H, Hkv, d, 1, 2), dtype=torch.uint8).cuda()
 
         def step():
             n.add_(1)
@@ -405,36 +405,37 @@ def lib():
 @pytest.mark.parametrize("kw, code", [
     (dict(d=96), -2), (dict(B=0), -1), (dict(Hkv=0), -1), (dict(H=3), -1), (dict(H=0), -1),
     (dict(total=0), -1), (dict(mq=0), -1), (dict(mk=0), -1), (dict(causal=2), -1),
-    (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1), (dict(splits=0), -1),
-    (dict(splits=257), -1), (dict(page=24), -1), (dict(pages=0), -1), (dict(max_pages=0), -1),
+    (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1), (dict(ctas=0), -1),
+    (dict(ctas=4097), -1), (dict(page=24), -1), (dict(pages=0), -1), (dict(max_pages=0), -1),
     (dict(q=0), -1), (dict(o=0), -1), (dict(kc=0), -1), (dict(ke=0), -1), (dict(cu=0), -1),
     (dict(n=0), -1), (dict(table=0), -1), (dict(q=0x10008), -3), (dict(vc=0x40008), -3),
     (dict(lse=0x80002), -3), (dict(n=0x92001), -3), (dict(ws=0), -4), (dict(wsb=64), -4),
     (dict(ws=0xA0004), -3), (dict(pages=1 << 26, page=32), -7),
-    (dict(total=1 << 25, H=4, mq=1), -7), (dict(B=1 << 24, mq=64, total=64), -7),
+    (dict(total=1 << 25, H=4, mq=1), -7),
+    (dict(B=1 << 28, mq=64, total=64, mk=1 << 20, max_pages=1 << 16), -7),
 ])
 def test_decode_cache_refuses(lib, kw, code):
     a = dict(q=0x10000, kc=0x30000, vc=0x40000, ke=0x50000, ve=0x60000, o=0x70000, lse=0x80000,
              cu=0x91000, n=0x92000, table=0x93000, B=1, mq=1, mk=100, total=1, max_pages=8, pages=8,
-             page=16, H=4, Hkv=2, d=64, scale=0.1, causal=0, splits=2, ws=0xA0000, wsb=1 << 20)
+             page=16, H=4, Hkv=2, d=64, scale=0.1, causal=0, ctas=2, ws=0xA0000, wsb=1 << 20)
     a.update(kw)
     vp = ctypes.c_void_p
     rc = lib.fa_fwd_decode_cache(
         vp(a["q"]), vp(a["kc"]), vp(a["vc"]), vp(a["ke"]), vp(a["ve"]), vp(a["o"]), vp(a["lse"]),
         vp(a["cu"]), vp(a["n"]), vp(a["table"]), a["B"], a["mq"], a["mk"], a["total"],
         a["max_pages"], a["pages"], a["page"], a["H"], a["Hkv"], a["d"], ctypes.c_float(a["scale"]),
-        a["causal"], a["splits"], vp(a["ws"]), a["wsb"], None)
+        a["causal"], a["ctas"], vp(a["ws"]), a["wsb"], None)
     assert rc == code
 
 
-def test_split_rule(lib):
-    f = lib.fa_decode_cache_splits_for
-    assert f(1, 32, 8, 1, 64, 152) == 1                     # one block: one range
-    for args in [(1, 32, 8, 1, 4096), (8, 32, 8, 1, 32768), (64, 64, 8, 1, 3000), (3, 12, 4, 40, 999),
-                 (1, 128, 1, 8, 200000), (300, 8, 8, 1, 100)]:
-        n = f(*args, 152)
-        nblk = -(-args[4] // 64)
-        assert 1 <= n <= min(256, max(1, nblk // 2))
-        per = -(-nblk // n)
-        assert (n - 1) * per < nblk                         # no range is always empty
+def test_thread_block_rule(lib):
+    f, w = lib.fa_decode_cache_ctas_for, lib.fa_decode_cache_workspace_bytes
+    assert f(1, 8, 8, 1, 1, 152) == 4                       # one for every two blocks of keys
+    assert f(1, 32, 8, 1, 4096, 152) == 8 * 32 / 2
+    assert f(8, 32, 8, 1, 32768, 152) == 304
+    assert f(1, 64, 1, 3, 100, 152) == 2                    # 192 query rows: three sets of 64
     assert f(0, 8, 8, 1, 1, 152) == -1 and f(1, 9, 8, 1, 1, 152) == -1 and f(1, 8, 8, 1, 1, 0) == -1
+    assert w(8, 2, 64, 1, 1) == 0 and w(8, 2, 96, 1, 2) == 0 and w(8, 2, 64, 1, 4097) == 0
+    for mq, rows in ((1, 8), (3, 16), (5, 32), (9, 64), (100, 64)):   # of 4 heads a group
+        n = w(8, 2, 64, mq, 10)
+        assert 20 * rows * 65 * 4 <= n <= 20 * rows * 65 * 4 + 3 * 256
