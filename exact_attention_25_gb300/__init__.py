@@ -26,6 +26,8 @@ __all__ = [
     "RopeTable", "rope_table", "fa_rope", "rope", "rope_backward", "PagedCache", "new_cache",
     "fa_cache_append", "cache_append", "fa_cache_read", "cache_read", "fa_fwd_decode_cache",
     "fa_decode_cache_num_ctas", "fa_decode_cache_workspace_bytes", "forward_decode_cache",
+    "fa_fwd_decode_shared", "fa_decode_shared_num_ctas", "fa_decode_shared_workspace_bytes",
+    "forward_decode_shared",
 ]
 
 
@@ -730,4 +732,72 @@ def forward_decode_cache(q, cache: PagedCache, cu_seqlens_q, seqlens_k, page_tab
         lse = torch.empty((H, total_q), dtype=torch.float32, device=dev)
         fa_fwd_decode_cache(q, cache, o, lse, cu_seqlens_q, seqlens_k, page_table, max_seqlen_q,
                             max_seqlen_k, scale, causal, num_ctas, ws, stream)
+    return o, lse
+
+
+# --------------------------------------------------------------------------- shared prefixes
+
+def fa_decode_shared_num_ctas() -> int:
+    """C ``fa_decode_shared_num_ctas``: the number of thread blocks that fills this GPU."""
+    n = int(load().fa_decode_shared_num_ctas())
+    check(min(n, 0))
+    return n
+
+
+def fa_decode_shared_workspace_bytes(total_q: int, H: int, d: int, num_ctas: int) -> int:
+    return int(load().fa_decode_shared_workspace_bytes(total_q, H, d, num_ctas))
+
+
+def fa_fwd_decode_shared(q, k_prefix, v_prefix, k, v, o, lse, cu_seqlens_q, cu_seqlens_k,
+                         cu_groups, cu_seqlens_p, max_seqlen_q: int, max_seqlen_k: int,
+                         max_group_q: int, max_seqlen_p: int, scale: float, causal: bool,
+                         num_ctas: int, workspace, stream=None) -> None:
+    """C ``fa_fwd_decode_shared``: q, o [total_q, H, d]; k_prefix, v_prefix [total_p, Hkv, d];
+    k, v [total_k, Hkv, d] (bf16); lse [H, total_q] fp32 or None; cu_seqlens_q, cu_seqlens_k
+    int32 [B + 1]; cu_groups (first sequence of each group), cu_seqlens_p int32 [groups + 1]."""
+    import torch
+
+    index = _same_device(q, k_prefix, v_prefix, k, v, o, lse, cu_seqlens_q, cu_seqlens_k,
+                         cu_groups, cu_seqlens_p, workspace)
+    total_q, H, d = q.shape
+    _check_decode_io(q, o, lse, d)
+    Hkv = int(k.shape[1])
+    for a, b in ((k, v), (k_prefix, v_prefix)):
+        _check_rows(a, b, Hkv, d)
+        if a.dtype != torch.bfloat16 or not a.is_contiguous() or not b.is_contiguous():
+            raise ValueError("keys and values must be contiguous bfloat16")
+    B, groups = cu_seqlens_q.numel() - 1, cu_groups.numel() - 1
+    _int32("cu_seqlens_q", cu_seqlens_q, B + 1)
+    _int32("cu_seqlens_k", cu_seqlens_k, B + 1)
+    _int32("cu_groups", cu_groups, groups + 1)
+    _int32("cu_seqlens_p", cu_seqlens_p, groups + 1)
+    _call(load().fa_fwd_decode_shared, index, stream, _ptr(q), _ptr(k_prefix), _ptr(v_prefix),
+          _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
+          _ptr(cu_groups), _ptr(cu_seqlens_p), B, groups, int(max_seqlen_q), int(max_seqlen_k),
+          int(max_group_q), int(max_seqlen_p), total_q, int(k.shape[0]), int(k_prefix.shape[0]), H,
+          Hkv, d, float(scale), int(bool(causal)), int(num_ctas), _ptr(workspace),
+          workspace.numel() * workspace.element_size())
+
+
+def forward_decode_shared(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seqlens_k, cu_groups,
+                          cu_seqlens_p, max_seqlen_q: int, max_seqlen_k: int, max_group_q: int,
+                          max_seqlen_p: int, scale: float | None = None, causal: bool = False,
+                          num_ctas: int | None = None, stream=None):
+    """Allocate O, LSE and the workspace and run fa_fwd_decode_shared."""
+    import torch
+
+    total_q, H, d = q.shape
+    if scale is None:
+        scale = d ** -0.5
+    dev = q.device
+    with _place(_same_device(q), stream):
+        if num_ctas is None:
+            num_ctas = fa_decode_shared_num_ctas()
+        ws = torch.empty(fa_decode_shared_workspace_bytes(total_q, H, d, num_ctas),
+                         dtype=torch.uint8, device=dev)
+        o = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        lse = torch.empty((H, total_q), dtype=torch.float32, device=dev)
+        fa_fwd_decode_shared(q, k_prefix, v_prefix, k, v, o, lse, cu_seqlens_q, cu_seqlens_k,
+                             cu_groups, cu_seqlens_p, max_seqlen_q, max_seqlen_k, max_group_q,
+                             max_seqlen_p, scale, causal, num_ctas, ws, stream)
     return o, lse

@@ -32,6 +32,7 @@ EXPORTS = (
     "fa_fwd_fp8_varlen_workspace_bytes", "fa_tile_order", "fa_order_group", "fa_decode_splits_for",
     "fa_rope", "fa_cache_append", "fa_cache_read", "fa_fwd_decode_cache",
     "fa_decode_cache_num_ctas", "fa_decode_cache_ctas_for", "fa_decode_cache_workspace_bytes",
+    "fa_fwd_decode_shared", "fa_decode_shared_workspace_bytes", "fa_decode_shared_num_ctas",
 )
 
 _lock = threading.Lock()
@@ -125,7 +126,11 @@ def load(path: str | None = None):
         lib.fa_decode_cache_ctas_for.argtypes = [i] * 6
         lib.fa_decode_cache_workspace_bytes.argtypes = [i] * 5
         lib.fa_decode_cache_workspace_bytes.restype = sz
-        for fn in ("fa_rope", "fa_cache_append", "fa_cache_read", "fa_fwd_decode_cache",
+        lib.fa_fwd_decode_shared.argtypes = [vp] * 11 + [i] * 12 + [f, i, i, vp, sz, vp]
+        lib.fa_decode_shared_workspace_bytes.argtypes = [i] * 4
+        lib.fa_decode_shared_workspace_bytes.restype = sz
+        lib.fa_decode_shared_num_ctas.argtypes = []
+        for fn in ("fa_fwd_decode_shared", "fa_decode_shared_num_ctas", "fa_rope", "fa_cache_append", "fa_cache_read", "fa_fwd_decode_cache",
                    "fa_decode_cache_num_ctas", "fa_decode_cache_ctas_for"):
             getattr(lib, fn).restype = ctypes.c_int
         for fn in ("fa_fwd", "fa_fwd_impl", "fa_bwd", "fa_bwd_impl", "fa_bwd_stage", "fa_device_status",

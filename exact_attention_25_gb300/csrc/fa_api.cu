@@ -38,6 +38,8 @@ cudaError_t launch_cache_append(int d, int is_f32, const CacheParams& p, cudaStr
 cudaError_t launch_cache_read(int d, int is_f32, const CacheParams& p, cudaStream_t st);
 cudaError_t launch_decode_cache(int d, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const CacheDecodeParams& p, cudaStream_t st);
+cudaError_t launch_decode_shared(int d, const CUtensorMap* maps, const SharedDecodeParams& p,
+                                 cudaStream_t st);
 
 // Device status word written by bounded waits that give up (0 = fine).
 __device__ int g_status_word;
@@ -844,6 +846,23 @@ namespace {
 
 constexpr int kDecodeMaxSplits = 256;
 
+// Q of the decode kernels: (d, H, total_q) with a box of (64 columns, G heads, `tokens` tokens),
+// so one copy brings the rows of a tile, in (token, head) order; K, V are mapped as fa_fwd_varlen's.
+int make_decode_q_map(CUtensorMap* m, const void* q, int H, int total_q, int d, int G, int tokens)
+{
+    const cuuint64_t dd = static_cast<cuuint64_t>(d);
+    cuuint64_t dims[3] = {dd, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(total_q)};
+    cuuint64_t strides[2] = {dd * 2, static_cast<cuuint64_t>(H) * dd * 2};
+    cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(tokens)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides,
+                          box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS)
+        return fail(FA_ERR_LAUNCH, "cuTensorMapEncodeTiled failed with code " + std::to_string(r));
+    return FA_OK;
+}
+
 size_t decode_part_o_bytes(int total_q, int H, int d, int splits)
 {
     return align256(static_cast<size_t>(splits) * total_q * H * d * 4);
@@ -939,22 +958,8 @@ extern "C" int fa_fwd_decode(const void* q, const void* k, const void* v, void* 
     p.L = packed_layout(cu_seqlens_q, cu_seqlens_k, B, max_seqlen_q, max_seqlen_k, total_q,
                         total_k, H, Hkv, d, st);
     if ((rc = get_encoder())) return rc;
-    // Q: (d, H, total_q) with a box of (64 columns, G heads, max_seqlen_q tokens), so one copy
-    // brings the G x nq query rows of a CTA; K, V as fa_fwd_varlen.
     CUtensorMap maps[4];
-    {
-        const cuuint64_t dd = static_cast<cuuint64_t>(d);
-        cuuint64_t dims[3] = {dd, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(total_q)};
-        cuuint64_t strides[2] = {dd * 2, static_cast<cuuint64_t>(H) * dd * 2};
-        cuuint32_t box[3] = {64, static_cast<cuuint32_t>(G), static_cast<cuuint32_t>(max_seqlen_q)};
-        cuuint32_t estr[3] = {1, 1, 1};
-        CUresult r = g_encode(&maps[0], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q),
-                              dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-        if (r != CUDA_SUCCESS)
-            return fail(FA_ERR_LAUNCH, "cuTensorMapEncodeTiled failed with code " + std::to_string(r));
-    }
+    if ((rc = make_decode_q_map(&maps[0], q, H, total_q, d, G, max_seqlen_q))) return rc;
     if ((rc = make_map(&maps[1], k, Hkv, total_k, d, 128, true, st.rs[kK], st.hs[kK])) ||
         (rc = make_map(&maps[2], v, Hkv, total_k, d, 128, true, st.rs[kV], st.hs[kV])))
         return rc;
@@ -1536,5 +1541,107 @@ extern "C" int fa_fwd_decode_cache(const void* q, const void* k_cache, const voi
     if (rc) return rc;
     cudaError_t e = fa::launch_decode_cache(d, maps[0], maps[1], p, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "cache decode launch");
+    return FA_OK;
+}
+
+// ---------------------------------------------------------------------------------------
+// Decode with shared prefixes (fa_fwd_decode_shared).
+// ---------------------------------------------------------------------------------------
+namespace {
+
+constexpr int kSharedMaxCtas = 1024;
+
+size_t shared_rows(int total_q, int H, int ctas) { return static_cast<size_t>(2) * total_q * H + 256 * static_cast<size_t>(ctas); }
+
+}  // namespace
+
+extern "C" size_t fa_decode_shared_workspace_bytes(int total_q, int H, int d, int num_ctas)
+{
+    if (total_q < 1 || H < 1 || (d != 64 && d != 128) || num_ctas < 1 || num_ctas > kSharedMaxCtas) return 0;
+    const size_t rows = shared_rows(total_q, H, num_ctas);
+    return align256(rows * d * 4) + align256(rows * 4);
+}
+
+extern "C" int fa_decode_shared_num_ctas(void)
+{
+    DeviceInfo* di = nullptr;
+    if (int rc = device_info(&di)) return rc;
+    return std::min(di->sms, kSharedMaxCtas);
+}
+
+extern "C" int fa_fwd_decode_shared(const void* q, const void* k_prefix, const void* v_prefix,
+                                    const void* k, const void* v, void* o, float* lse,
+                                    const int* cu_seqlens_q, const int* cu_seqlens_k,
+                                    const int* cu_groups, const int* cu_seqlens_p, int B,
+                                    int num_groups, int max_seqlen_q, int max_seqlen_k,
+                                    int max_group_q, int max_seqlen_p, int total_q, int total_k,
+                                    int total_p, int H, int Hkv, int d, float scale, int causal,
+                                    int num_ctas, void* workspace, size_t workspace_bytes,
+                                    void* stream)
+{
+    if (int rc = check_varlen(cu_seqlens_q, cu_seqlens_k, B, &max_seqlen_q, &max_seqlen_k, total_q,
+                              total_k, H, Hkv, d, scale, causal))
+        return rc;
+    if (num_groups < 1 || total_p < 1 || max_group_q < 1 || max_seqlen_p < 1)
+        return fail(FA_ERR_INVALID_ARG, "num_groups, total_p, max_group_q and max_seqlen_p must be >= 1");
+    const int G = H / Hkv;
+    if (G > 128) return fail(FA_ERR_INVALID_ARG, "H / Hkv must be <= 128");
+    if (num_ctas < 1 || num_ctas > kSharedMaxCtas)
+        return fail(FA_ERR_INVALID_ARG, "num_ctas must be in [1, " + std::to_string(kSharedMaxCtas) + "]");
+    if (!q || !k_prefix || !v_prefix || !k || !v || !o || !cu_groups || !cu_seqlens_p)
+        return fail(FA_ERR_INVALID_ARG, "q, k_prefix, v_prefix, k, v, o, cu_groups and cu_seqlens_p must be non-null");
+    if (!aligned16(q) || !aligned16(k_prefix) || !aligned16(v_prefix) || !aligned16(k) || !aligned16(v) ||
+        !aligned16(o) || !aligned4(lse) || !aligned4(cu_groups) || !aligned4(cu_seqlens_p))
+        return fail(FA_ERR_MISALIGNED, "tensors must be 16-byte aligned (lse and the integers 4-byte)");
+    if (static_cast<long long>(total_p) * Hkv * d >= (1LL << 31))
+        return fail(FA_ERR_TOO_LARGE, "total_p*Hkv*d must be < 2^31");
+    max_group_q = std::min(max_group_q, total_q);
+    max_seqlen_p = std::min(max_seqlen_p, total_p);
+    const int tok = std::min(128 / G, total_q);
+    const long long places =
+        static_cast<long long>(num_groups) * Hkv * ((max_group_q + tok - 1) / tok) * ((max_seqlen_p + 127) / 128 + fa::kUnitCost) +
+        static_cast<long long>(B) * Hkv * ((max_seqlen_q + tok - 1) / tok) * ((max_seqlen_k + 127) / 128 + fa::kUnitCost);
+    if (places >= (1LL << 31) || static_cast<long long>(B) * H * max_seqlen_q >= (1LL << 31) ||
+        static_cast<long long>(B) + num_groups >= (1LL << 31) - 64)
+        return fail(FA_ERR_TOO_LARGE, "the batch must have fewer than 2^31 blocks of 128 keys, and B*H*max_seqlen_q < 2^31");
+    const size_t need = fa_decode_shared_workspace_bytes(total_q, H, d, num_ctas);
+    if (!workspace || workspace_bytes < need)
+        return fail(FA_ERR_WORKSPACE, "workspace must hold " + std::to_string(need) + " bytes");
+    if (!aligned16(workspace)) return fail(FA_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    DeviceInfo* di = nullptr;
+    if (int rc = device_info(&di)) return rc;
+    fa::SharedDecodeParams p{};
+    p.o = static_cast<__nv_bfloat16*>(o);
+    p.lse = lse;
+    const size_t rows = shared_rows(total_q, H, num_ctas);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.o_part = reinterpret_cast<float*>(ws);
+    p.lse_part = reinterpret_cast<float*>(ws + align256(rows * d * 4));
+    p.part_row0 = 2LL * total_q * H;
+    p.v = static_cast<const __nv_bfloat16*>(v);
+    p.cu_q = cu_seqlens_q; p.cu_k = cu_seqlens_k; p.cu_g = cu_groups; p.cu_p = cu_seqlens_p;
+    p.B = B; p.groups = num_groups; p.H = H; p.Hkv = Hkv; p.G = G;
+    p.max_q = max_seqlen_q; p.max_k = max_seqlen_k; p.max_group_q = max_group_q; p.max_p = max_seqlen_p;
+    p.total_q = total_q; p.total_k = total_k; p.total_p = total_p;
+    p.tile_tokens = tok;
+    p.ctas = num_ctas;
+    p.scale_log2 = scale * fa::kLog2e; p.causal = causal;
+    p.status = di->status; p.wait_limit_ns = g_wait_limit_ns; p.debug_flags = g_debug_flags;
+    const int cut = (g_debug_flags & fa::kDebugShrinkExtents) ? 1 : 0;
+    p.q_ext = (static_cast<long long>(total_q) * H - cut) * d;
+    p.stat_ext = static_cast<long long>(total_q) * H - cut;
+    p.v_ext = (static_cast<long long>(total_k) * Hkv - cut) * d;
+    p.part_ext = static_cast<long long>(rows) - cut;
+    if (int rc = get_encoder()) return rc;
+    CUtensorMap maps[5];
+    int rc = make_decode_q_map(&maps[0], q, H, total_q, d, G, tok);
+    const long long krs = static_cast<long long>(Hkv) * d;
+    if (!rc) rc = make_map(&maps[1], k_prefix, Hkv, total_p, d, 128, true, krs, d);
+    if (!rc) rc = make_map(&maps[2], v_prefix, Hkv, total_p, d, 128, true, krs, d);
+    if (!rc) rc = make_map(&maps[3], k, Hkv, total_k, d, 128, true, krs, d);
+    if (!rc) rc = make_map(&maps[4], v, Hkv, total_k, d, 128, true, krs, d);
+    if (rc) return rc;
+    cudaError_t e = fa::launch_decode_shared(d, maps, p, static_cast<cudaStream_t>(stream));
+    if (e != cudaSuccess) return cuda_fail(e, "shared decode launch");
     return FA_OK;
 }

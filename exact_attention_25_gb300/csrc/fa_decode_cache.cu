@@ -158,22 +158,6 @@ __device__ __forceinline__ void sequence_work(const CacheDecodeParams& p, int b,
     u.in_seq = ((u.nq * p.G + p.rows_cta - 1) >> p.rows_shift) * p.Hkv;
 }
 
-// The line of T places in `ctas` shares, the first T mod ctas of them one place longer.  (T is
-// below 2^31: checked on the host for the largest batch of the call's sizes.)
-struct Shares {
-    int total, per, more;
-    __device__ __forceinline__ Shares(int T, int ctas)
-        : total(T), per(static_cast<unsigned>(T) / static_cast<unsigned>(ctas)), more(T - per * ctas)
-    {
-    }
-    __device__ __forceinline__ int start(int c) const { return c * per + min(c, more); }
-    __device__ __forceinline__ int share_of(int pos) const
-    {
-        const int cut = more * (per + 1);
-        return pos < cut ? pos / (per + 1) : more + (pos - cut) / per;
-    }
-};
-
 // All lanes of a warp: the line's shares and, for the first place of share c, its sequence (u)
 // and `at`, its distance from that sequence's first place.  The search is skipped when the share
 // starts at the line's end.

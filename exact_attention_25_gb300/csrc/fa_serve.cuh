@@ -1,17 +1,26 @@
 // Shared definitions of the serving-side operators: rotary positions (fa_rope.cu), the paged
-// e4m3 key/value cache (fa_cache.cu) and the split-KV decode over that cache
-// (fa_decode_cache.cu).
+// e4m3 key/value cache (fa_cache.cu), the split-KV decode over that cache (fa_decode_cache.cu)
+// and the decode with shared prefixes (fa_decode_shared.cu).
 #pragma once
 #include "fa_common.cuh"
 
 namespace fa {
 
-// Watchdog sites of the cache decode kernel (see WaitSite; values below 64).
+// Watchdog sites of the serving kernels (see WaitSite; values below 64).
 enum ServeWaitSite : int {
     kSiteCacheEmpty = 32,
     kSiteCacheFull,
     kSiteCacheDrain,
     kSiteCacheMerge,
+    kSiteSharedEmpty,
+    kSiteSharedUnit,
+    kSiteSharedQ,
+    kSiteSharedK,
+    kSiteSharedV,
+    kSiteSharedS,
+    kSiteSharedP,
+    kSiteSharedO,
+    kSiteSharedDrain,
 };
 
 constexpr int kRopeMaxPairs = 64;
@@ -88,6 +97,52 @@ struct CacheDecodeParams {
     unsigned long long wait_limit_ns;
     int debug_flags;
     long long q_ext, stat_ext, part_ext;  // element extents (checked builds)
+};
+
+// Decode with shared prefixes: the same kind of line, over the groups' prefixes and then the
+// sequences' own keys, in units of one tile of query rows (tile_tokens tokens times the G heads of
+// a group, at most 128) and one key/value head.
+struct SharedDecodeParams {
+    __nv_bfloat16* o;          // [total_q, H, d]
+    float* lse;                // [H, total_q] (may be null)
+    // workspace rows of d fp32 values and their LSE: [2][total_q][H] for units that one share
+    // holds whole (prefix, own keys), then from row part_row0 on 128 rows for each of the parts
+    // 2 c (first unit of share c) and 2 c + 1 (last)
+    float* o_part;
+    float* lse_part;
+    long long part_row0;
+    const __nv_bfloat16* v;    // [total_k, Hkv, d] (read for infinities and NaNs only)
+    const int* cu_q;           // [B + 1]
+    const int* cu_k;           // [B + 1]
+    const int* cu_g;           // [groups + 1] first sequence of each group
+    const int* cu_p;           // [groups + 1] first row of each group's prefix
+    int B, groups, H, Hkv, G;
+    int max_q, max_k, max_group_q, max_p;
+    int total_q, total_k, total_p;
+    int tile_tokens;
+    int ctas;
+    float scale_log2;
+    int causal;
+    int* status;
+    unsigned long long wait_limit_ns;
+    int debug_flags;
+    long long q_ext, stat_ext, v_ext, part_ext;  // extents (checked builds): elements, workspace rows
+};
+
+// The line of T places in `ctas` shares, the first T mod ctas of them one place longer.  (T is
+// below 2^31: checked on the host for the largest batch of the call's sizes.)
+struct Shares {
+    int total, per, more;
+    __device__ __forceinline__ Shares(int T, int ctas)
+        : total(T), per(static_cast<unsigned>(T) / static_cast<unsigned>(ctas)), more(T - per * ctas)
+    {
+    }
+    __device__ __forceinline__ int start(int c) const { return c * per + min(c, more); }
+    __device__ __forceinline__ int share_of(int pos) const
+    {
+        const int cut = more * (per + 1);
+        return pos < cut ? pos / (per + 1) : more + (pos - cut) / per;
+    }
 };
 
 // 2^(byte - 127), the scale an exponent byte stands for; 255 is NaN.

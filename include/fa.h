@@ -448,6 +448,32 @@ int fa_decode_cache_num_ctas(int B, int H, int Hkv, int max_seqlen_q, int max_se
 int fa_decode_cache_ctas_for(int B, int H, int Hkv, int max_seqlen_q, int max_seqlen_k,
                              int num_sms);
 
+/* Decoding for batches whose sequences share long prefixes: the packed forward of fa_fwd_decode
+ * (bf16 q, o [total_q, H, d], lse [H, total_q] or NULL, grouped heads with H / Hkv <= 128) where
+ * every query sees the whole prefix of its group and, under one softmax, its sequence's own keys
+ * (those bottom-right causal among themselves when causal = 1).
+ *   - k, v [total_k, Hkv, d]: the sequences' own keys, cu_seqlens_q / cu_seqlens_k as
+ *     fa_fwd_varlen; sequences may have none.
+ *   - k_prefix, v_prefix [total_p, Hkv, d]: the prefixes back to back, cu_seqlens_p (device int32
+ *     [num_groups + 1]); group g has the sequences [cu_groups[g], cu_groups[g + 1]) (device int32
+ *     [num_groups + 1], rising).  A sequence in no group sees only its own keys.
+ *   - max_group_q: the most queries of a group; max_seqlen_p: the longest prefix.
+ * A prefix is read once for every 128 / (H / Hkv) tokens of its group, instead of once a sequence.
+ * The batch's blocks of 128 keys are shared out evenly over num_ctas thread blocks (in [1, 1024];
+ * fa_decode_shared_num_ctas: one for each SM), and a second kernel merges each query's parts.
+ * workspace: fa_decode_shared_workspace_bytes(total_q, H, d, num_ctas) bytes, overwritten.  A query
+ * that sees no key gets O = 0, lse = -inf; rows that belong to no sequence are left as they are;
+ * what lies in k and v behind the sequences may be anything.  bf16 only, forward only. */
+int fa_fwd_decode_shared(const void* q, const void* k_prefix, const void* v_prefix, const void* k,
+                         const void* v, void* o, float* lse, const int* cu_seqlens_q,
+                         const int* cu_seqlens_k, const int* cu_groups, const int* cu_seqlens_p,
+                         int B, int num_groups, int max_seqlen_q, int max_seqlen_k,
+                         int max_group_q, int max_seqlen_p, int total_q, int total_k, int total_p,
+                         int H, int Hkv, int d, float scale, int causal, int num_ctas,
+                         void* workspace, size_t workspace_bytes, void* stream);
+size_t fa_decode_shared_workspace_bytes(int total_q, int H, int d, int num_ctas);
+int fa_decode_shared_num_ctas(void);
+
 #ifdef __cplusplus
 }
 #endif

@@ -56,9 +56,9 @@ def values(codes: np.ndarray, exps: np.ndarray) -> np.ndarray:
     return CODES[codes] * np.exp2(exps.astype(np.float64) - 127.0)[..., None]
 
 
-def attention_rows(q, k, v, scale, causal, shift, v_scale=None):
+def attention_rows(q, k, v, scale, causal, shift, v_scale=None, always=0):
     """One (sequence, head): q [nq, d], k, v [nk, d] fp64.  Query i sees key j iff j <= i + shift
-    (every key without the mask).  Returns o, lse, and for the error bound sum_j p_j |v_j|, the
+    (every key without the mask), and the first `always` keys whatever the mask.  Returns o, lse, and for the error bound sum_j p_j |v_j|, the
     largest scale * sum |q| |k| of each row and (v_scale: the power of two of each V row) the
     floor 2^-36 * max_j (p_j 2^ev_j) * sum_j |v_j| / 2^ev_j, else 0.  A row that sees no key: o = 0,
     lse = -inf."""
@@ -67,7 +67,7 @@ def attention_rows(q, k, v, scale, causal, shift, v_scale=None):
     o, pv = np.zeros((nq, d)), np.zeros((nq, d))
     lse, mag, low = np.full(nq, -np.inf), np.zeros(nq), np.zeros((nq, d))
     for i in range(nq):
-        n = nk if not causal else max(0, min(nk, i + shift + 1))
+        n = nk if not causal else max(always, min(nk, i + shift + 1))
         if n == 0:
             continue
         with np.errstate(invalid="ignore", over="ignore"):
