@@ -429,22 +429,38 @@ def forward_decode(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max_s
 
 
 # --------------------------------------------------------------------------- serving helpers
+# These calls are made once for every token of a decode, so their host side is kept short: plain
+# ints for pointers and streams, one check of each property, one device lookup.
 
-def _same_device(*ts):
-    """The tensors' one CUDA device (its index); raises unless all lie on it."""
-    dev = ts[0].device
+@functools.lru_cache(maxsize=None)
+def _torch():
+    import torch
+
+    return torch
+
+
+@functools.lru_cache(maxsize=None)
+def _raw_stream_of():
+    """device index -> cudaStream_t of torch's current stream there."""
+    torch = _torch()
+    fast = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return fast or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _device(*ts) -> int:
+    """The index of the tensors' one CUDA device; raises unless all lie on it."""
+    index = ts[0].get_device()
     for t in ts:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != index:
             raise ValueError("tensors must lie on one device")
-    if dev.type != "cuda":
+    if index < 0 or not ts[0].is_cuda:
         raise ValueError("tensors must be CUDA tensors")
-    return dev.index
+    return index
 
 
 @contextlib.contextmanager
 def _switched(index, stream):
-    import torch
-
+    torch = _torch()
     with torch.cuda.device(index):
         if stream is None:
             yield
@@ -454,51 +470,65 @@ def _switched(index, stream):
 
 
 def _place(index, stream):
-    """Context for a call's allocations and launches: the tensors' device, and the stream the
-    call runs on (so that torch's allocator ties outputs and workspaces to it)."""
-    import torch
-
-    if stream is None and torch.cuda.current_device() == index:
-        return contextlib.nullcontext()
+    """Context for a call that allocates: the tensors' device, and the stream the call runs on (so
+    that torch's allocator ties outputs and workspaces to it).  None where both are current."""
+    if stream is None and _torch().cuda.current_device() == index:
+        return None
     return _switched(index, stream)
 
 
 def _call(fn, index, stream, *args):
     """One C call on the tensors' device and on ``stream`` (default: that device's current)."""
-    import torch
-
+    raw = _raw_stream_of()(index) if stream is None else stream.cuda_stream
+    torch = _torch()
     if torch.cuda.current_device() == index:
-        check(fn(*args, _stream(stream)))
+        rc = fn(*args, raw)
     else:
         with torch.cuda.device(index):
-            check(fn(*args, _stream(stream)))
+            rc = fn(*args, raw)
+    if rc:
+        check(rc)
 
 
-def _rows_strides(*ts):
-    """(row, head) element strides of [rows, heads, d] views, or None when all are contiguous."""
-    return None if all(t is None or t.is_contiguous() for t in ts) else _view_strides(*ts)
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _view_strides(*ts):
+    """(row, head) element strides of [rows, heads, d] views, or None when all are contiguous."""
+    for t in ts:
+        if t is not None and not t.is_contiguous():
+            break
+    else:
+        return None
     vals = []
     for t in ts:
         if t is None:
             vals += [0, 0]
             continue
-        if t.dim() != 3 or t.stride(2) != 1:
+        if t.stride(2) != 1:
             raise ValueError("packed views need contiguous head dimensions (stride 1 in d)")
         # a dimension of one row or head is never stepped over: any valid step will do
-        _, heads, d = t.shape
+        rows, heads, d = t.shape
         hs = t.stride(1) if heads > 1 else d
-        vals += [t.stride(0) if t.shape[0] > 1 else heads * hs, hs]
+        vals += [t.stride(0) if rows > 1 else heads * hs, hs]
     return (ctypes.c_longlong * len(vals))(*vals)
 
 
 def _int32(name, t, *shape):
-    if t.dtype != _torch_int32():
+    if t.dtype != _torch().int32:
         raise TypeError(f"{name} must be int32")
-    if not t.is_contiguous() or tuple(t.shape) != shape:
+    if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous, of shape {list(shape)}")
+
+
+def _dtype_of(t) -> int:
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return FA_BF16
+    if t.dtype == torch.float32:
+        return FA_F32
+    raise TypeError(f"unsupported dtype {t.dtype}; use bfloat16 or float32")
 
 
 # --------------------------------------------------------------------------- rotary positions
@@ -538,24 +568,35 @@ def fa_rope(q, k, q_out, k_out, positions, table: RopeTable, inverse: bool = Fal
     """C ``fa_rope``: q, q_out [total, H, d], k, k_out [total, Hkv, d] (or both None), bf16 or
     fp32, contiguous or (row, head)-strided views; positions int32 [axes, total].  Outputs may
     be their inputs."""
-    total, H, d = q.shape
-    ts = (q, k, q_out, k_out)
+    index = _rope_check(q, k, positions, table)
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out come together")
-    index = _same_device(q, k, q_out, k_out, positions)
-    Hkv = 0 if k is None else int(k.shape[1])
-    for t, heads in zip(ts, (H, Hkv, H, Hkv)):
-        if t is not None and (t.dtype != q.dtype or tuple(t.shape) != (total, heads, d)):
-            raise ValueError("q, k and their outputs must be [total, heads, d] of one dtype")
+    if q_out.shape != q.shape or q_out.dtype != q.dtype or (
+            k is not None and (k_out.shape != k.shape or k_out.dtype != q.dtype)):
+        raise ValueError("outputs must have their inputs' shape and dtype")
+    _device(q, q_out, k_out)
+    _rope_call(index, q, k, q_out, k_out, positions, table, inverse, stream)
+
+
+def _rope_check(q, k, positions, table):
+    total, _, d = q.shape
     if table.d != d:
         raise ValueError(f"the table is made for d = {table.d}")
+    if k is not None and (k.dtype != q.dtype or k.dim() != 3 or k.shape[0] != total
+                          or k.shape[2] != d):
+        raise ValueError("q and k must be [total, heads, d] of one dtype")
     if positions.dim() != 2:
         raise ValueError("positions must be [axes, total]")
-    _int32("positions", positions, max(table.axes, int(positions.shape[0])), total)
-    _call(load().fa_rope, index, stream, _ptr(q), _ptr(k), _ptr(q_out), _ptr(k_out),
-          _ptr(positions), table._freq, table._axis, _rows_strides(*ts), total, H, Hkv, d,
-          int(positions.shape[0]), table.pairs, int(table.interleaved), int(bool(inverse)),
-          _dtype_code(q))
+    _int32("positions", positions, max(table.axes, positions.shape[0]), total)
+    return _device(q, k, positions)
+
+
+def _rope_call(index, q, k, q_out, k_out, positions, table, inverse, stream):
+    total, H, d = q.shape
+    _call(load().fa_rope, index, stream, q.data_ptr(), _at(k), q_out.data_ptr(), _at(k_out),
+          positions.data_ptr(), table._freq, table._axis, _view_strides(q, k, q_out, k_out), total,
+          H, 0 if k is None else k.shape[1], d, positions.shape[0], table.pairs,
+          int(table.interleaved), 1 if inverse else 0, _dtype_of(q))
 
 
 def rope(q, k, positions, table: RopeTable, stream=None):
@@ -569,12 +610,15 @@ def rope_backward(dq, dk, positions, table: RopeTable, stream=None):
 
 
 def _rope(q, k, positions, table, inverse, stream):
-    import torch
-
-    with _place(_same_device(q), stream):
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=q.device)
-        fa_rope(q, k, q_out, k_out, positions, table, inverse, stream)
+    index = _rope_check(q, k, positions, table)
+    place = _place(index, stream)
+    if place is not None:
+        with place:
+            return _rope(q, k, positions, table, inverse, None)
+    torch = _torch()
+    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
+    _rope_call(index, q, k, q_out, k_out, positions, table, inverse, None)
     return q_out, k_out
 
 
@@ -602,18 +646,22 @@ def new_cache(num_pages: int, page_size: int, Hkv: int, d: int, device="cuda") -
 
 def _cache_sizes(cache, page_table):
     """(num_pages, Hkv, page_size, d, B, max_pages), the tensors checked against them."""
-    shape = tuple(cache.k.shape)
-    if len(shape) != 4 or tuple(cache.v.shape) != shape:
+    k, v, ke, ve = cache
+    shape = k.shape
+    if len(shape) != 4 or v.shape != shape:
         raise ValueError("the cache's codes must be [num_pages, Hkv, page_size, d]")
-    if tuple(cache.k_exp.shape) != shape[:3] or tuple(cache.v_exp.shape) != shape[:3]:
+    if ke.shape != shape[:3] or ve.shape != shape[:3]:
         raise ValueError("the cache's exponents must be [num_pages, Hkv, page_size]")
     for t in cache:
         if t.element_size() != 1 or not t.is_contiguous():
             raise ValueError("the cache's tensors must be contiguous, of 1-byte elements")
     if page_table.dim() != 2:
         raise ValueError("page_table must be [B, max_pages]")
-    _int32("page_table", page_table, *page_table.shape)
-    return shape + tuple(page_table.shape)
+    if page_table.dtype != _torch().int32:
+        raise TypeError("page_table must be int32")
+    if not page_table.is_contiguous():
+        raise ValueError("page_table must be contiguous")
+    return (*shape, *page_table.shape)
 
 
 def fa_cache_append(cache: PagedCache, k, v, cu_seqlens_new, seqlens_k, page_table,
@@ -622,17 +670,20 @@ def fa_cache_append(cache: PagedCache, k, v, cu_seqlens_new, seqlens_k, page_tab
     contiguous or strided) into the cache's pages; seqlens_k int32 [B] are the lengths after
     the call."""
     pages, Hkv, ps, d, B, max_pages = _cache_sizes(cache, page_table)
-    index = _same_device(*cache, k, v, cu_seqlens_new, seqlens_k, page_table)
     _check_rows(k, v, Hkv, d)
     _int32("cu_seqlens_new", cu_seqlens_new, B + 1)
     _int32("seqlens_k", seqlens_k, B)
-    _call(load().fa_cache_append, index, stream, _ptr(k), _ptr(v), _rows_strides(k, v),
-          *map(_ptr, cache), _ptr(cu_seqlens_new), _ptr(seqlens_k), _ptr(page_table), B,
-          int(max_seqlen_new), int(k.shape[0]), max_pages, pages, ps, Hkv, d, _dtype_code(k))
+    kc, vc, ke, ve = cache
+    index = _device(k, v, kc, vc, ke, ve, cu_seqlens_new, seqlens_k, page_table)
+    _call(load().fa_cache_append, index, stream, k.data_ptr(), v.data_ptr(), _view_strides(k, v),
+          kc.data_ptr(), vc.data_ptr(), ke.data_ptr(), ve.data_ptr(), cu_seqlens_new.data_ptr(),
+          seqlens_k.data_ptr(), page_table.data_ptr(), B, int(max_seqlen_new), k.shape[0],
+          max_pages, pages, ps, Hkv, d, _dtype_of(k))
 
 
 def _check_rows(k, v, Hkv, d):
-    if k.dim() != 3 or tuple(k.shape[1:]) != (Hkv, d) or v.shape != k.shape or v.dtype != k.dtype:
+    shape = k.shape
+    if len(shape) != 3 or shape[1] != Hkv or shape[2] != d or v.shape != shape or v.dtype != k.dtype:
         raise ValueError("k and v must be [rows, Hkv, d] of one dtype")
 
 
@@ -644,25 +695,30 @@ def fa_cache_read(cache: PagedCache, k, v, cu_seqlens_k, page_table, max_seqlen_
     """C ``fa_cache_read``: writes the cached rows of every sequence back to back into k, v
     [total_k, Hkv, d] (bf16 or fp32, contiguous or strided)."""
     pages, Hkv, ps, d, B, max_pages = _cache_sizes(cache, page_table)
-    index = _same_device(*cache, k, v, cu_seqlens_k, page_table)
     _check_rows(k, v, Hkv, d)
     _int32("cu_seqlens_k", cu_seqlens_k, B + 1)
-    _call(load().fa_cache_read, index, stream, *map(_ptr, cache), _ptr(k), _ptr(v),
-          _rows_strides(k, v), _ptr(cu_seqlens_k), _ptr(page_table), B, int(max_seqlen_k),
-          int(k.shape[0]), max_pages, pages, ps, Hkv, d, _dtype_code(k))
+    kc, vc, ke, ve = cache
+    index = _device(k, v, kc, vc, ke, ve, cu_seqlens_k, page_table)
+    _call(load().fa_cache_read, index, stream, kc.data_ptr(), vc.data_ptr(), ke.data_ptr(),
+          ve.data_ptr(), k.data_ptr(), v.data_ptr(), _view_strides(k, v), cu_seqlens_k.data_ptr(),
+          page_table.data_ptr(), B, int(max_seqlen_k), k.shape[0], max_pages, pages, ps, Hkv, d,
+          _dtype_of(k))
 
 
 def cache_read(cache: PagedCache, cu_seqlens_k, page_table, max_seqlen_k: int, total_k: int,
                dtype=None, stream=None):
     """Allocate K and V ([total_k, Hkv, d], bf16 unless dtype says otherwise) and run
     fa_cache_read."""
-    import torch
-
+    place = _place(_device(cache.k), stream)
+    if place is not None:
+        with place:
+            return cache_read(cache, cu_seqlens_k, page_table, max_seqlen_k, total_k, dtype)
+    torch = _torch()
     _, Hkv, _, d = cache.k.shape
-    with _place(_same_device(cache.k), stream):
-        k, v = (torch.empty((total_k, Hkv, d), dtype=dtype or torch.bfloat16,
-                            device=cache.k.device) for _ in range(2))
-        fa_cache_read(cache, k, v, cu_seqlens_k, page_table, max_seqlen_k, stream)
+    dev, dtype = cache.k.device, dtype or torch.bfloat16
+    k = torch.empty((total_k, Hkv, d), dtype=dtype, device=dev)
+    v = torch.empty((total_k, Hkv, d), dtype=dtype, device=dev)
+    fa_cache_read(cache, k, v, cu_seqlens_k, page_table, max_seqlen_k)
     return k, v
 
 
@@ -685,53 +741,64 @@ def fa_fwd_decode_cache(q, cache: PagedCache, o, lse, cu_seqlens_q, seqlens_k, p
     """C ``fa_fwd_decode_cache``: q, o [total_q, H, d] bf16, lse [H, total_q] fp32 or None;
     workspace (fa_decode_cache_workspace_bytes) may be None for num_ctas = 1."""
     pages, Hkv, ps, d, B, max_pages = _cache_sizes(cache, page_table)
-    index = _same_device(q, *cache, o, lse, cu_seqlens_q, seqlens_k, page_table, workspace)
     _check_decode_io(q, o, lse, d)
-    total_q, H, _ = q.shape
     _int32("cu_seqlens_q", cu_seqlens_q, B + 1)
     _int32("seqlens_k", seqlens_k, B)
+    kc, vc, ke, ve = cache
+    index = _device(q, kc, vc, ke, ve, o, lse, cu_seqlens_q, seqlens_k, page_table, workspace)
+    total_q, H, _ = q.shape
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _call(load().fa_fwd_decode_cache, index, stream, _ptr(q), *map(_ptr, cache), _ptr(o),
-          _ptr(lse), _ptr(cu_seqlens_q), _ptr(seqlens_k), _ptr(page_table), B, int(max_seqlen_q),
-          int(max_seqlen_k), total_q, max_pages, pages, ps, H, Hkv, d, float(scale),
-          int(bool(causal)), int(num_ctas), _ptr(workspace), nbytes)
+    _call(load().fa_fwd_decode_cache, index, stream, q.data_ptr(), kc.data_ptr(), vc.data_ptr(),
+          ke.data_ptr(), ve.data_ptr(), o.data_ptr(), _at(lse), cu_seqlens_q.data_ptr(),
+          seqlens_k.data_ptr(), page_table.data_ptr(), B, int(max_seqlen_q), int(max_seqlen_k),
+          total_q, max_pages, pages, ps, H, Hkv, d, float(scale), 1 if causal else 0,
+          int(num_ctas), _at(workspace), nbytes)
 
 
 def _check_decode_io(q, o, lse, d):
-    import torch
-
-    if q.dim() != 3 or q.shape[2] != d or o.shape != q.shape:
+    torch = _torch()
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != d or o.shape != shape:
         raise ValueError("q and o must be [total_q, H, d]")
     if q.dtype != torch.bfloat16 or o.dtype != torch.bfloat16:
         raise TypeError("q and o must be bfloat16")
     if not q.is_contiguous() or not o.is_contiguous():
         raise ValueError("q and o must be contiguous")
     if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous()
-                            or tuple(lse.shape) != (q.shape[1], q.shape[0])):
+                            or lse.shape != (shape[1], shape[0])):
         raise ValueError("lse must be contiguous fp32 [H, total_q]")
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_cache_plan(index, B, H, Hkv, d, max_q, max_k):
+    """(thread blocks, workspace bytes) for these sizes on device `index` (the current one)."""
+    n = fa_decode_cache_num_ctas(B, H, Hkv, max_q, max_k)
+    return n, fa_decode_cache_workspace_bytes(H, Hkv, d, max_q, n)
 
 
 def forward_decode_cache(q, cache: PagedCache, cu_seqlens_q, seqlens_k, page_table,
                          max_seqlen_q: int, max_seqlen_k: int, scale: float | None = None,
                          causal: bool = False, num_ctas: int | None = None, stream=None):
     """Allocate O, LSE (and the workspace) and run fa_fwd_decode_cache."""
-    import torch
-
+    index = _device(q)
+    place = _place(index, stream)
+    if place is not None:
+        with place:
+            return forward_decode_cache(q, cache, cu_seqlens_q, seqlens_k, page_table,
+                                        max_seqlen_q, max_seqlen_k, scale, causal, num_ctas)
+    torch = _torch()
     total_q, H, d = q.shape
-    if scale is None:
-        scale = d ** -0.5
-    dev = q.device
-    with _place(_same_device(q), stream):
-        Hkv = cache.k.shape[1]
-        if num_ctas is None:
-            num_ctas = fa_decode_cache_num_ctas(page_table.shape[0], H, Hkv, max_seqlen_q,
-                                                max_seqlen_k)
+    Hkv, dev = cache.k.shape[1], q.device
+    if num_ctas is None:
+        num_ctas, nbytes = _decode_cache_plan(index, page_table.shape[0], H, Hkv, d, max_seqlen_q,
+                                              max_seqlen_k)
+    else:
         nbytes = fa_decode_cache_workspace_bytes(H, Hkv, d, max_seqlen_q, num_ctas)
-        ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-        o = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        lse = torch.empty((H, total_q), dtype=torch.float32, device=dev)
-        fa_fwd_decode_cache(q, cache, o, lse, cu_seqlens_q, seqlens_k, page_table, max_seqlen_q,
-                            max_seqlen_k, scale, causal, num_ctas, ws, stream)
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
+    o = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    lse = torch.empty((H, total_q), dtype=torch.float32, device=dev)
+    fa_fwd_decode_cache(q, cache, o, lse, cu_seqlens_q, seqlens_k, page_table, max_seqlen_q,
+                        max_seqlen_k, d ** -0.5 if scale is None else scale, causal, num_ctas, ws)
     return o, lse
 
 
@@ -755,28 +822,35 @@ def fa_fwd_decode_shared(q, k_prefix, v_prefix, k, v, o, lse, cu_seqlens_q, cu_s
     """C ``fa_fwd_decode_shared``: q, o [total_q, H, d]; k_prefix, v_prefix [total_p, Hkv, d];
     k, v [total_k, Hkv, d] (bf16); lse [H, total_q] fp32 or None; cu_seqlens_q, cu_seqlens_k
     int32 [B + 1]; cu_groups (first sequence of each group), cu_seqlens_p int32 [groups + 1]."""
-    import torch
-
-    index = _same_device(q, k_prefix, v_prefix, k, v, o, lse, cu_seqlens_q, cu_seqlens_k,
-                         cu_groups, cu_seqlens_p, workspace)
+    torch = _torch()
     total_q, H, d = q.shape
     _check_decode_io(q, o, lse, d)
-    Hkv = int(k.shape[1])
-    for a, b in ((k, v), (k_prefix, v_prefix)):
-        _check_rows(a, b, Hkv, d)
-        if a.dtype != torch.bfloat16 or not a.is_contiguous() or not b.is_contiguous():
+    Hkv = k.shape[1]
+    _check_rows(k, v, Hkv, d)
+    _check_rows(k_prefix, v_prefix, Hkv, d)
+    for t in (k, v, k_prefix, v_prefix):
+        if t.dtype != torch.bfloat16 or not t.is_contiguous():
             raise ValueError("keys and values must be contiguous bfloat16")
     B, groups = cu_seqlens_q.numel() - 1, cu_groups.numel() - 1
     _int32("cu_seqlens_q", cu_seqlens_q, B + 1)
     _int32("cu_seqlens_k", cu_seqlens_k, B + 1)
     _int32("cu_groups", cu_groups, groups + 1)
     _int32("cu_seqlens_p", cu_seqlens_p, groups + 1)
-    _call(load().fa_fwd_decode_shared, index, stream, _ptr(q), _ptr(k_prefix), _ptr(v_prefix),
-          _ptr(k), _ptr(v), _ptr(o), _ptr(lse), _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
-          _ptr(cu_groups), _ptr(cu_seqlens_p), B, groups, int(max_seqlen_q), int(max_seqlen_k),
-          int(max_group_q), int(max_seqlen_p), total_q, int(k.shape[0]), int(k_prefix.shape[0]), H,
-          Hkv, d, float(scale), int(bool(causal)), int(num_ctas), _ptr(workspace),
+    index = _device(q, k_prefix, v_prefix, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, cu_groups,
+                    cu_seqlens_p, workspace)
+    _call(load().fa_fwd_decode_shared, index, stream, q.data_ptr(), k_prefix.data_ptr(),
+          v_prefix.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _at(lse),
+          cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), cu_groups.data_ptr(),
+          cu_seqlens_p.data_ptr(), B, groups, int(max_seqlen_q), int(max_seqlen_k),
+          int(max_group_q), int(max_seqlen_p), total_q, k.shape[0], k_prefix.shape[0], H, Hkv, d,
+          float(scale), 1 if causal else 0, int(num_ctas), workspace.data_ptr(),
           workspace.numel() * workspace.element_size())
+
+
+@functools.lru_cache(maxsize=None)
+def _decode_shared_ctas(index):
+    """fa_decode_shared_num_ctas of device `index` (the current one)."""
+    return fa_decode_shared_num_ctas()
 
 
 def forward_decode_shared(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seqlens_k, cu_groups,
@@ -784,20 +858,23 @@ def forward_decode_shared(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seqlens_
                           max_seqlen_p: int, scale: float | None = None, causal: bool = False,
                           num_ctas: int | None = None, stream=None):
     """Allocate O, LSE and the workspace and run fa_fwd_decode_shared."""
-    import torch
-
+    index = _device(q)
+    place = _place(index, stream)
+    if place is not None:
+        with place:
+            return forward_decode_shared(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seqlens_k,
+                                         cu_groups, cu_seqlens_p, max_seqlen_q, max_seqlen_k,
+                                         max_group_q, max_seqlen_p, scale, causal, num_ctas)
+    torch = _torch()
     total_q, H, d = q.shape
-    if scale is None:
-        scale = d ** -0.5
     dev = q.device
-    with _place(_same_device(q), stream):
-        if num_ctas is None:
-            num_ctas = fa_decode_shared_num_ctas()
-        ws = torch.empty(fa_decode_shared_workspace_bytes(total_q, H, d, num_ctas),
-                         dtype=torch.uint8, device=dev)
-        o = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        lse = torch.empty((H, total_q), dtype=torch.float32, device=dev)
-        fa_fwd_decode_shared(q, k_prefix, v_prefix, k, v, o, lse, cu_seqlens_q, cu_seqlens_k,
-                             cu_groups, cu_seqlens_p, max_seqlen_q, max_seqlen_k, max_group_q,
-                             max_seqlen_p, scale, causal, num_ctas, ws, stream)
+    if num_ctas is None:
+        num_ctas = _decode_shared_ctas(index)
+    ws = torch.empty(fa_decode_shared_workspace_bytes(total_q, H, d, num_ctas), dtype=torch.uint8,
+                     device=dev)
+    o = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    lse = torch.empty((H, total_q), dtype=torch.float32, device=dev)
+    fa_fwd_decode_shared(q, k_prefix, v_prefix, k, v, o, lse, cu_seqlens_q, cu_seqlens_k,
+                         cu_groups, cu_seqlens_p, max_seqlen_q, max_seqlen_k, max_group_q,
+                         max_seqlen_p, d ** -0.5 if scale is None else scale, causal, num_ctas, ws)
     return o, lse

@@ -97,7 +97,7 @@ __device__ __forceinline__ long long cache_row(const CacheParams& p, int b, int 
 
 }  // namespace
 
-template <class T, int D>
+template <class T, int D, bool WIDE>
 __global__ void __launch_bounds__(kCacheThreads) fa_cache_append_kernel(const CacheParams p)
 {
     constexpr int LR = D / 16;                // lanes of a row, 16 elements each
@@ -133,7 +133,8 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_append_kernel(const Ca
             for (int h = 0; h < WD; ++h) x[s][h] = make_uint4(0u, 0u, 0u, 0u);
             if (i < n && in_extent(off, 16, z ? p.v_ext : p.k_ext, p.status)) {
 #pragma unroll
-                for (int h = 0; h < WD; ++h) x[s][h] = reinterpret_cast<const uint4*>(src + off)[h];
+                for (int h = 0; h < WD; h += 2)
+                    load_32b<WIDE>(reinterpret_cast<const uint4*>(src + off) + h, x[s] + h);
             }
         }
 #pragma unroll
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_append_kernel(const Ca
 }
 
 // Rows whose page is missing from the table read as zero.
-template <class T, int D>
+template <class T, int D, bool WIDE>
 __global__ void __launch_bounds__(kCacheThreads) fa_cache_read_kernel(const CacheParams p)
 {
     constexpr int LR = D / 16;
@@ -219,7 +220,8 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_read_kernel(const Cach
             const long long off = (first + i) * rs + w.hk * hs + 16 * l;
             if (i < n && in_extent(off, 16, z ? p.v_ext : p.k_ext, p.status)) {
 #pragma unroll
-                for (int h = 0; h < WD; ++h) reinterpret_cast<uint4*>(dst + off)[h] = o[h];
+                for (int h = 0; h < WD; h += 2)
+                    store_32b<WIDE>(reinterpret_cast<uint4*>(dst + off) + h, o + h);
             }
         }
     }
@@ -233,24 +235,39 @@ static dim3 cache_grid(const CacheParams& p)
     return dim3(static_cast<unsigned>((warps + kCacheThreads / 32 - 1) / (kCacheThreads / 32)));
 }
 
-cudaError_t launch_cache_append(int d, int is_f32, const CacheParams& p, cudaStream_t st)
+template <class T, int D>
+static cudaError_t launch_append(const CacheParams& p, bool wide, cudaStream_t st)
 {
     const dim3 g = cache_grid(p), t(kCacheThreads);
-    if (d == 64)
-        return is_f32 ? launch_dependent(fa_cache_append_kernel<float, 64>, g, t, 0, st, p)
-                      : launch_dependent(fa_cache_append_kernel<__nv_bfloat16, 64>, g, t, 0, st, p);
-    return is_f32 ? launch_dependent(fa_cache_append_kernel<float, 128>, g, t, 0, st, p)
-                  : launch_dependent(fa_cache_append_kernel<__nv_bfloat16, 128>, g, t, 0, st, p);
+    return wide ? launch_dependent(fa_cache_append_kernel<T, D, true>, g, t, 0, st, p)
+                : launch_dependent(fa_cache_append_kernel<T, D, false>, g, t, 0, st, p);
+}
+
+template <class T, int D>
+static cudaError_t launch_read(const CacheParams& p, bool wide, cudaStream_t st)
+{
+    const dim3 g = cache_grid(p), t(kCacheThreads);
+    return wide ? launch_dependent(fa_cache_read_kernel<T, D, true>, g, t, 0, st, p)
+                : launch_dependent(fa_cache_read_kernel<T, D, false>, g, t, 0, st, p);
+}
+
+static bool cache_wide(const CacheParams& p, int es)
+{
+    return wide_rows(p.k, p.k_rs, p.k_hs, es) && wide_rows(p.v, p.v_rs, p.v_hs, es);
+}
+
+cudaError_t launch_cache_append(int d, int is_f32, const CacheParams& p, cudaStream_t st)
+{
+    const bool w = cache_wide(p, is_f32 ? 4 : 2);
+    if (d == 64) return is_f32 ? launch_append<float, 64>(p, w, st) : launch_append<__nv_bfloat16, 64>(p, w, st);
+    return is_f32 ? launch_append<float, 128>(p, w, st) : launch_append<__nv_bfloat16, 128>(p, w, st);
 }
 
 cudaError_t launch_cache_read(int d, int is_f32, const CacheParams& p, cudaStream_t st)
 {
-    const dim3 g = cache_grid(p), t(kCacheThreads);
-    if (d == 64)
-        return is_f32 ? launch_dependent(fa_cache_read_kernel<float, 64>, g, t, 0, st, p)
-                      : launch_dependent(fa_cache_read_kernel<__nv_bfloat16, 64>, g, t, 0, st, p);
-    return is_f32 ? launch_dependent(fa_cache_read_kernel<float, 128>, g, t, 0, st, p)
-                  : launch_dependent(fa_cache_read_kernel<__nv_bfloat16, 128>, g, t, 0, st, p);
+    const bool w = cache_wide(p, is_f32 ? 4 : 2);
+    if (d == 64) return is_f32 ? launch_read<float, 64>(p, w, st) : launch_read<__nv_bfloat16, 64>(p, w, st);
+    return is_f32 ? launch_read<float, 128>(p, w, st) : launch_read<__nv_bfloat16, 128>(p, w, st);
 }
 
 }  // namespace fa

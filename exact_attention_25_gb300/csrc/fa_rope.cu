@@ -35,16 +35,15 @@ __device__ __forceinline__ void turn_sincos(uint32_t t, float& s, float& c)
     if (quad == 1 || quad == 2) c = -c;
 }
 
+// 8 elements: 16 bytes of bf16, 32 of fp32.
 template <class T>
-struct Chunk;  // 8 elements
+struct Chunk;
 template <>
 struct Chunk<__nv_bfloat16> {
-    uint4 w;
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = w; }
+    uint4 w[1];
     __device__ __forceinline__ void get(float* f) const
     {
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        const uint32_t u[4] = {w[0].x, w[0].y, w[0].z, w[0].w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             f[2 * i] = __uint_as_float(u[i] << 16);
@@ -53,41 +52,78 @@ struct Chunk<__nv_bfloat16> {
     }
     __device__ __forceinline__ void put(const float* f)
     {
-        w = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                       pack_bf16x2(f[6], f[7]));
+        w[0] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
+                          pack_bf16x2(f[6], f[7]));
     }
 };
 template <>
 struct Chunk<float> {
-    float4 a, b;
-    __device__ __forceinline__ void load(const float* p)
-    {
-        a = reinterpret_cast<const float4*>(p)[0];
-        b = reinterpret_cast<const float4*>(p)[1];
-    }
-    __device__ __forceinline__ void store(float* p) const
-    {
-        reinterpret_cast<float4*>(p)[0] = a;
-        reinterpret_cast<float4*>(p)[1] = b;
-    }
+    uint4 w[2];
     __device__ __forceinline__ void get(float* f) const
     {
-        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            f[4 * i] = __uint_as_float(w[i].x);
+            f[4 * i + 1] = __uint_as_float(w[i].y);
+            f[4 * i + 2] = __uint_as_float(w[i].z);
+            f[4 * i + 3] = __uint_as_float(w[i].w);
+        }
     }
     __device__ __forceinline__ void put(const float* f)
     {
-        a = make_float4(f[0], f[1], f[2], f[3]);
-        b = make_float4(f[4], f[5], f[6], f[7]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]),
+                              __float_as_uint(f[4 * i + 2]), __float_as_uint(f[4 * i + 3]));
     }
 };
+
+// A lane's two chunks.  NEXT: hi follows lo.
+template <bool WIDE, bool NEXT>
+__device__ __forceinline__ void load_chunks(const __nv_bfloat16* lo, const __nv_bfloat16* hi,
+                                            Chunk<__nv_bfloat16>& a, Chunk<__nv_bfloat16>& b)
+{
+    if constexpr (NEXT && WIDE) {
+        uint4 w[2];
+        load_32b<true>(lo, w);
+        a.w[0] = w[0];
+        b.w[0] = w[1];
+    } else {
+        a.w[0] = *reinterpret_cast<const uint4*>(lo);
+        b.w[0] = *reinterpret_cast<const uint4*>(hi);
+    }
+}
+template <bool WIDE, bool NEXT>
+__device__ __forceinline__ void load_chunks(const float* lo, const float* hi, Chunk<float>& a, Chunk<float>& b)
+{
+    load_32b<WIDE>(lo, a.w);
+    load_32b<WIDE>(hi, b.w);
+}
+template <bool WIDE, bool NEXT>
+__device__ __forceinline__ void store_chunks(__nv_bfloat16* lo, __nv_bfloat16* hi,
+                                             const Chunk<__nv_bfloat16>& a, const Chunk<__nv_bfloat16>& b)
+{
+    if constexpr (NEXT && WIDE) {
+        const uint4 w[2] = {a.w[0], b.w[0]};
+        store_32b<true>(lo, w);
+    } else {
+        *reinterpret_cast<uint4*>(lo) = a.w[0];
+        *reinterpret_cast<uint4*>(hi) = b.w[0];
+    }
+}
+template <bool WIDE, bool NEXT>
+__device__ __forceinline__ void store_chunks(float* lo, float* hi, const Chunk<float>& a, const Chunk<float>& b)
+{
+    store_32b<WIDE>(lo, a.w);
+    store_32b<WIDE>(hi, b.w);
+}
 
 constexpr int kRopeThreads = 256;
 constexpr int kRopeUnroll = 4;  // head steps whose loads are in flight together
 
 }  // namespace
 
-template <class T, int D, bool INTERLEAVED>
+template <class T, int D, bool INTERLEAVED, bool WIDE>
 __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_constant__ RopeParams p)
 {
     constexpr int C = D / 16;     // lanes of a head, 8 pairs (16 elements) each
@@ -147,10 +183,7 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_cons
                 const long long off = tok * p.x_rs[z] + (h - (z ? p.H : 0)) * p.x_hs[z];
                 on[u] = in_extent(off, D, p.x_ext[z], p.status);
                 const T* src = static_cast<const T*>(p.x[z]) + off;
-                if (on[u]) {
-                    a[u].load(src + lo);
-                    b[u].load(src + hi);
-                }
+                if (on[u]) load_chunks<WIDE, INTERLEAVED>(src + lo, src + hi, a[u], b[u]);
             }
         }
 #pragma unroll
@@ -178,8 +211,7 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_cons
             const long long off = tok * p.y_rs[z] + (h - (z ? p.H : 0)) * p.y_hs[z];
             if (!in_extent(off, D, p.y_ext[z], p.status)) continue;
             T* dst = static_cast<T*>(p.y[z]) + off;
-            a[u].store(dst + lo);
-            b[u].store(dst + hi);
+            store_chunks<WIDE, INTERLEAVED>(dst + lo, dst + hi, a[u], b[u]);
         }
     }
 }
@@ -194,9 +226,18 @@ static cudaError_t launch_rope_impl(RopeParams p, int interleaved, cudaStream_t 
     p.parts = want < 1 ? 1 : (want > steps ? steps : want);
     const long long warps = static_cast<long long>(p.total) * p.parts;
     const dim3 grid(static_cast<unsigned>((warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32)));
+    // 32-byte accesses where every row allows them; bf16 halves that lie apart are 16 bytes anyway
+    bool wide = interleaved || sizeof(T) == 4;
+    for (int z = 0; z < 2; ++z)
+        wide = wide && wide_rows(p.x[z], p.x_rs[z], p.x_hs[z], sizeof(T)) &&
+               wide_rows(p.y[z], p.y_rs[z], p.y_hs[z], sizeof(T));
+    const dim3 block(kRopeThreads);
     if (interleaved)
-        return launch_dependent(fa_rope_kernel<T, D, true>, grid, dim3(kRopeThreads), 0, st, p);
-    return launch_dependent(fa_rope_kernel<T, D, false>, grid, dim3(kRopeThreads), 0, st, p);
+        return wide ? launch_dependent(fa_rope_kernel<T, D, true, true>, grid, block, 0, st, p)
+                    : launch_dependent(fa_rope_kernel<T, D, true, false>, grid, block, 0, st, p);
+    if (sizeof(T) == 4 && wide)
+        return launch_dependent(fa_rope_kernel<T, D, false, sizeof(T) == 4>, grid, block, 0, st, p);
+    return launch_dependent(fa_rope_kernel<T, D, false, false>, grid, block, 0, st, p);
 }
 
 cudaError_t launch_rope(int d, int is_f32, const RopeParams& p, int interleaved, cudaStream_t st,

@@ -168,6 +168,43 @@ __device__ __forceinline__ int packed_rows(const int* cu, int b, int total, int 
     return min(end - first, most);
 }
 
+// 32 bytes at once: where each thread of a warp takes 32 neighbouring bytes, 16-byte accesses would
+// use half of every 32-byte sector each.  The address is a multiple of 32 (WIDE), or of 16.
+template <bool WIDE>
+__device__ __forceinline__ void load_32b(const void* p, uint4* w)
+{
+    if constexpr (WIDE) {
+        asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=r"(w[0].x), "=r"(w[0].y), "=r"(w[0].z), "=r"(w[0].w), "=r"(w[1].x),
+                       "=r"(w[1].y), "=r"(w[1].z), "=r"(w[1].w)
+                     : "l"(p)
+                     : "memory");
+    } else {
+        w[0] = reinterpret_cast<const uint4*>(p)[0];
+        w[1] = reinterpret_cast<const uint4*>(p)[1];
+    }
+}
+template <bool WIDE>
+__device__ __forceinline__ void store_32b(void* p, const uint4* w)
+{
+    if constexpr (WIDE) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0].x),
+                     "r"(w[0].y), "r"(w[0].z), "r"(w[0].w), "r"(w[1].x), "r"(w[1].y), "r"(w[1].z),
+                     "r"(w[1].w)
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(p)[0] = w[0];
+        reinterpret_cast<uint4*>(p)[1] = w[1];
+    }
+}
+
+// Whether a tensor's rows can be taken 32 bytes at a time.
+inline bool wide_rows(const void* p, long long rs, long long hs, int elem_bytes)
+{
+    return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(rs * elem_bytes) |
+             static_cast<uintptr_t>(hs * elem_bytes)) & 31u) == 0;
+}
+
 // Launch as a programmatic dependent of the work before it on the stream: the grid's launch and
 // set-up overlap that work's end.  Every kernel launched so waits (griddepcontrol.wait) in all
 // of its threads before it touches global memory, so stream order is kept.
