@@ -3,11 +3,12 @@
 The computation lives in ``libfa.so`` (hand-written CUDA: TMA, tcgen05/TMEM, warp-specialised
 roles) behind the C ABI of ``include/fa.h``.  This module is the thin Python binding: the
 ``fa_*`` functions mirror the C entry points one to one and only marshal torch tensors into
-pointers and sizes; ``forward``/``backward`` additionally allocate the outputs with torch.
+pointers and sizes; ``forward``/``backward`` additionally allocate the outputs with torch.  The
+serving calls (rotary positions, the paged cache, the decodes over it and over shared prefixes) do
+the same through a small native module.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import math
@@ -428,107 +429,52 @@ def forward_decode(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max_s
     return o, lse
 
 
-# --------------------------------------------------------------------------- serving helpers
-# These calls are made once for every token of a decode, so their host side is kept short: plain
-# ints for pointers and streams, one check of each property, one device lookup.
+# --------------------------------------------------------------------------- serving calls
+# Made once for every token and layer of a decode, so their host side is native (the _serve module,
+# csrc/serve_binding.cpp): it checks the tensors, allocates what is to be returned, and makes the C
+# call on the tensors' device and its current stream.  A call on another stream makes that the
+# current one first, so torch's allocator ties outputs and workspaces to it.
 
 @functools.lru_cache(maxsize=None)
-def _torch():
+def _native():
+    import torch  # noqa: F401  (the module links against torch's libraries)
+
+    try:
+        from . import _serve
+    except ImportError as e:
+        raise ImportError("the native binding is missing: build it with "
+                          "exact_attention_25_gb300.build.build_all() (there is no fallback "
+                          "implementation)") from e
+    return _serve
+
+
+def _entry(*names):
+    """Addresses of C entry points of the library in use."""
+    lib = _lib._lib or load()
+    try:
+        return lib.entry_addresses[names]
+    except AttributeError:
+        lib.entry_addresses = {}
+    except KeyError:
+        pass
+    at = tuple(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in names)
+    lib.entry_addresses[names] = at
+    return at
+
+
+def _on(stream, t):
+    """Context that makes ``stream``, a stream of t's device, the current one."""
     import torch
 
-    return torch
+    if stream.device_index != t.get_device():
+        raise ValueError("the stream belongs to another device than the tensors")
+    return torch.cuda.stream(stream)
 
 
-@functools.lru_cache(maxsize=None)
-def _raw_stream_of():
-    """device index -> cudaStream_t of torch's current stream there."""
-    torch = _torch()
-    fast = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return fast or (lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _device(*ts) -> int:
-    """The index of the tensors' one CUDA device; raises unless all lie on it."""
-    index = ts[0].get_device()
-    for t in ts:
-        if t is not None and t.get_device() != index:
-            raise ValueError("tensors must lie on one device")
-    if index < 0 or not ts[0].is_cuda:
-        raise ValueError("tensors must be CUDA tensors")
-    return index
-
-
-@contextlib.contextmanager
-def _switched(index, stream):
-    torch = _torch()
-    with torch.cuda.device(index):
-        if stream is None:
-            yield
-        else:
-            with torch.cuda.stream(stream):
-                yield
-
-
-def _place(index, stream):
-    """Context for a call that allocates: the tensors' device, and the stream the call runs on (so
-    that torch's allocator ties outputs and workspaces to it).  None where both are current."""
-    if stream is None and _torch().cuda.current_device() == index:
-        return None
-    return _switched(index, stream)
-
-
-def _call(fn, index, stream, *args):
-    """One C call on the tensors' device and on ``stream`` (default: that device's current)."""
-    raw = _raw_stream_of()(index) if stream is None else stream.cuda_stream
-    torch = _torch()
-    if torch.cuda.current_device() == index:
-        rc = fn(*args, raw)
-    else:
-        with torch.cuda.device(index):
-            rc = fn(*args, raw)
-    if rc:
-        check(rc)
-
-
-def _at(t):
-    return None if t is None else t.data_ptr()
-
-
-def _view_strides(*ts):
-    """(row, head) element strides of [rows, heads, d] views, or None when all are contiguous."""
-    for t in ts:
-        if t is not None and not t.is_contiguous():
-            break
-    else:
-        return None
-    vals = []
-    for t in ts:
-        if t is None:
-            vals += [0, 0]
-            continue
-        if t.stride(2) != 1:
-            raise ValueError("packed views need contiguous head dimensions (stride 1 in d)")
-        # a dimension of one row or head is never stepped over: any valid step will do
-        rows, heads, d = t.shape
-        hs = t.stride(1) if heads > 1 else d
-        vals += [t.stride(0) if rows > 1 else heads * hs, hs]
-    return (ctypes.c_longlong * len(vals))(*vals)
-
-
-def _int32(name, t, *shape):
-    if t.dtype != _torch().int32:
-        raise TypeError(f"{name} must be int32")
-    if t.shape != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous, of shape {list(shape)}")
-
-
-def _dtype_of(t) -> int:
-    torch = _torch()
-    if t.dtype == torch.bfloat16:
-        return FA_BF16
-    if t.dtype == torch.float32:
-        return FA_F32
-    raise TypeError(f"unsupported dtype {t.dtype}; use bfloat16 or float32")
+def _done(result):
+    if result.__class__ is int:
+        check(result)
+    return result
 
 
 # --------------------------------------------------------------------------- rotary positions
@@ -546,6 +492,9 @@ class RopeTable:
             raise ValueError("inv_freq and axis must have one entry for each rotated pair")
         self._freq = (ctypes.c_double * self.pairs)(*self.inv_freq)
         self._axis = (ctypes.c_int * self.pairs)(*self.axis)
+        # what every call passes after the tensors
+        self._args = (ctypes.addressof(self._freq), ctypes.addressof(self._axis), self.axes,
+                      self.d, self.pairs, self.interleaved)
 
 
 @functools.lru_cache(maxsize=64)
@@ -568,58 +517,30 @@ def fa_rope(q, k, q_out, k_out, positions, table: RopeTable, inverse: bool = Fal
     """C ``fa_rope``: q, q_out [total, H, d], k, k_out [total, Hkv, d] (or both None), bf16 or
     fp32, contiguous or (row, head)-strided views; positions int32 [axes, total].  Outputs may
     be their inputs."""
-    index = _rope_check(q, k, positions, table)
-    if (k is None) != (k_out is None):
-        raise ValueError("k and k_out come together")
-    if q_out.shape != q.shape or q_out.dtype != q.dtype or (
-            k is not None and (k_out.shape != k.shape or k_out.dtype != q.dtype)):
-        raise ValueError("outputs must have their inputs' shape and dtype")
-    _device(q, q_out, k_out)
-    _rope_call(index, q, k, q_out, k_out, positions, table, inverse, stream)
-
-
-def _rope_check(q, k, positions, table):
-    total, _, d = q.shape
-    if table.d != d:
-        raise ValueError(f"the table is made for d = {table.d}")
-    if k is not None and (k.dtype != q.dtype or k.dim() != 3 or k.shape[0] != total
-                          or k.shape[2] != d):
-        raise ValueError("q and k must be [total, heads, d] of one dtype")
-    if positions.dim() != 2:
-        raise ValueError("positions must be [axes, total]")
-    _int32("positions", positions, max(table.axes, positions.shape[0]), total)
-    return _device(q, k, positions)
-
-
-def _rope_call(index, q, k, q_out, k_out, positions, table, inverse, stream):
-    total, H, d = q.shape
-    _call(load().fa_rope, index, stream, q.data_ptr(), _at(k), q_out.data_ptr(), _at(k_out),
-          positions.data_ptr(), table._freq, table._axis, _view_strides(q, k, q_out, k_out), total,
-          H, 0 if k is None else k.shape[1], d, positions.shape[0], table.pairs,
-          int(table.interleaved), 1 if inverse else 0, _dtype_of(q))
+    if q_out is None or (k is None) != (k_out is None):
+        raise ValueError("every input has its output")
+    if stream is not None:
+        with _on(stream, q):
+            return fa_rope(q, k, q_out, k_out, positions, table, inverse)
+    _done(_native().rope(*_entry("fa_rope"), q, k, q_out, k_out, positions, *table._args, inverse))
 
 
 def rope(q, k, positions, table: RopeTable, stream=None):
     """Allocate and return q and k (None: only q) turned by their positions."""
-    return _rope(q, k, positions, table, False, stream)
+    if stream is not None:
+        with _on(stream, q):
+            return rope(q, k, positions, table)
+    return _done(_native().rope(*_entry("fa_rope"), q, k, None, None, positions, *table._args,
+                                False))
 
 
 def rope_backward(dq, dk, positions, table: RopeTable, stream=None):
     """The gradients of ``rope``'s inputs from those of its outputs."""
-    return _rope(dq, dk, positions, table, True, stream)
-
-
-def _rope(q, k, positions, table, inverse, stream):
-    index = _rope_check(q, k, positions, table)
-    place = _place(index, stream)
-    if place is not None:
-        with place:
-            return _rope(q, k, positions, table, inverse, None)
-    torch = _torch()
-    q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device)
-    _rope_call(index, q, k, q_out, k_out, positions, table, inverse, None)
-    return q_out, k_out
+    if stream is not None:
+        with _on(stream, dq):
+            return rope_backward(dq, dk, positions, table)
+    return _done(_native().rope(*_entry("fa_rope"), dq, dk, None, None, positions, *table._args,
+                                True))
 
 
 # --------------------------------------------------------------------------- the paged e4m3 cache
@@ -644,47 +565,17 @@ def new_cache(num_pages: int, page_size: int, Hkv: int, d: int, device="cuda") -
     return PagedCache(k, v, ke, ve)
 
 
-def _cache_sizes(cache, page_table):
-    """(num_pages, Hkv, page_size, d, B, max_pages), the tensors checked against them."""
-    k, v, ke, ve = cache
-    shape = k.shape
-    if len(shape) != 4 or v.shape != shape:
-        raise ValueError("the cache's codes must be [num_pages, Hkv, page_size, d]")
-    if ke.shape != shape[:3] or ve.shape != shape[:3]:
-        raise ValueError("the cache's exponents must be [num_pages, Hkv, page_size]")
-    for t in cache:
-        if t.element_size() != 1 or not t.is_contiguous():
-            raise ValueError("the cache's tensors must be contiguous, of 1-byte elements")
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [B, max_pages]")
-    if page_table.dtype != _torch().int32:
-        raise TypeError("page_table must be int32")
-    if not page_table.is_contiguous():
-        raise ValueError("page_table must be contiguous")
-    return (*shape, *page_table.shape)
-
-
 def fa_cache_append(cache: PagedCache, k, v, cu_seqlens_new, seqlens_k, page_table,
                     max_seqlen_new: int, stream=None) -> None:
     """C ``fa_cache_append``: quantises the new rows k, v [total_new, Hkv, d] (bf16 or fp32,
     contiguous or strided) into the cache's pages; seqlens_k int32 [B] are the lengths after
-    the call."""
-    pages, Hkv, ps, d, B, max_pages = _cache_sizes(cache, page_table)
-    _check_rows(k, v, Hkv, d)
-    _int32("cu_seqlens_new", cu_seqlens_new, B + 1)
-    _int32("seqlens_k", seqlens_k, B)
-    kc, vc, ke, ve = cache
-    index = _device(k, v, kc, vc, ke, ve, cu_seqlens_new, seqlens_k, page_table)
-    _call(load().fa_cache_append, index, stream, k.data_ptr(), v.data_ptr(), _view_strides(k, v),
-          kc.data_ptr(), vc.data_ptr(), ke.data_ptr(), ve.data_ptr(), cu_seqlens_new.data_ptr(),
-          seqlens_k.data_ptr(), page_table.data_ptr(), B, int(max_seqlen_new), k.shape[0],
-          max_pages, pages, ps, Hkv, d, _dtype_of(k))
-
-
-def _check_rows(k, v, Hkv, d):
-    shape = k.shape
-    if len(shape) != 3 or shape[1] != Hkv or shape[2] != d or v.shape != shape or v.dtype != k.dtype:
-        raise ValueError("k and v must be [rows, Hkv, d] of one dtype")
+    the call, page_table int32 [B, max_pages]."""
+    if stream is not None:
+        with _on(stream, k):
+            return fa_cache_append(cache, k, v, cu_seqlens_new, seqlens_k, page_table,
+                                   max_seqlen_new)
+    _done(_native().cache_append(*_entry("fa_cache_append"), *cache, k, v, cu_seqlens_new,
+                                 seqlens_k, page_table, max_seqlen_new))
 
 
 cache_append = fa_cache_append
@@ -694,32 +585,28 @@ def fa_cache_read(cache: PagedCache, k, v, cu_seqlens_k, page_table, max_seqlen_
                   stream=None) -> None:
     """C ``fa_cache_read``: writes the cached rows of every sequence back to back into k, v
     [total_k, Hkv, d] (bf16 or fp32, contiguous or strided)."""
-    pages, Hkv, ps, d, B, max_pages = _cache_sizes(cache, page_table)
-    _check_rows(k, v, Hkv, d)
-    _int32("cu_seqlens_k", cu_seqlens_k, B + 1)
-    kc, vc, ke, ve = cache
-    index = _device(k, v, kc, vc, ke, ve, cu_seqlens_k, page_table)
-    _call(load().fa_cache_read, index, stream, kc.data_ptr(), vc.data_ptr(), ke.data_ptr(),
-          ve.data_ptr(), k.data_ptr(), v.data_ptr(), _view_strides(k, v), cu_seqlens_k.data_ptr(),
-          page_table.data_ptr(), B, int(max_seqlen_k), k.shape[0], max_pages, pages, ps, Hkv, d,
-          _dtype_of(k))
+    if k is None or v is None:
+        raise ValueError("k and v must be given")
+    if stream is not None:
+        with _on(stream, k):
+            return fa_cache_read(cache, k, v, cu_seqlens_k, page_table, max_seqlen_k)
+    _done(_native().cache_read(*_entry("fa_cache_read"), *cache, k, v, cu_seqlens_k, page_table,
+                               max_seqlen_k, 0, False))
 
 
 def cache_read(cache: PagedCache, cu_seqlens_k, page_table, max_seqlen_k: int, total_k: int,
                dtype=None, stream=None):
-    """Allocate K and V ([total_k, Hkv, d], bf16 unless dtype says otherwise) and run
+    """Allocate K and V ([total_k, Hkv, d], bf16 unless dtype is torch.float32) and run
     fa_cache_read."""
-    place = _place(_device(cache.k), stream)
-    if place is not None:
-        with place:
+    import torch
+
+    if dtype not in (None, torch.bfloat16, torch.float32):
+        raise TypeError(f"unsupported dtype {dtype}; use bfloat16 or float32")
+    if stream is not None:
+        with _on(stream, cache.k):
             return cache_read(cache, cu_seqlens_k, page_table, max_seqlen_k, total_k, dtype)
-    torch = _torch()
-    _, Hkv, _, d = cache.k.shape
-    dev, dtype = cache.k.device, dtype or torch.bfloat16
-    k = torch.empty((total_k, Hkv, d), dtype=dtype, device=dev)
-    v = torch.empty((total_k, Hkv, d), dtype=dtype, device=dev)
-    fa_cache_read(cache, k, v, cu_seqlens_k, page_table, max_seqlen_k)
-    return k, v
+    return _done(_native().cache_read(*_entry("fa_cache_read"), *cache, None, None, cu_seqlens_k,
+                                      page_table, max_seqlen_k, total_k, dtype is torch.float32))
 
 
 def fa_decode_cache_num_ctas(B: int, H: int, Hkv: int, max_seqlen_q: int,
@@ -735,71 +622,42 @@ def fa_decode_cache_workspace_bytes(H: int, Hkv: int, d: int, max_seqlen_q: int,
     return int(load().fa_decode_cache_workspace_bytes(H, Hkv, d, max_seqlen_q, num_ctas))
 
 
+_DECODE_CACHE = ("fa_fwd_decode_cache", "fa_decode_cache_num_ctas",
+                 "fa_decode_cache_workspace_bytes")
+
+
 def fa_fwd_decode_cache(q, cache: PagedCache, o, lse, cu_seqlens_q, seqlens_k, page_table,
                         max_seqlen_q: int, max_seqlen_k: int, scale: float, causal: bool,
                         num_ctas: int, workspace, stream=None) -> None:
     """C ``fa_fwd_decode_cache``: q, o [total_q, H, d] bf16, lse [H, total_q] fp32 or None;
-    workspace (fa_decode_cache_workspace_bytes) may be None for num_ctas = 1."""
-    pages, Hkv, ps, d, B, max_pages = _cache_sizes(cache, page_table)
-    _check_decode_io(q, o, lse, d)
-    _int32("cu_seqlens_q", cu_seqlens_q, B + 1)
-    _int32("seqlens_k", seqlens_k, B)
-    kc, vc, ke, ve = cache
-    index = _device(q, kc, vc, ke, ve, o, lse, cu_seqlens_q, seqlens_k, page_table, workspace)
-    total_q, H, _ = q.shape
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _call(load().fa_fwd_decode_cache, index, stream, q.data_ptr(), kc.data_ptr(), vc.data_ptr(),
-          ke.data_ptr(), ve.data_ptr(), o.data_ptr(), _at(lse), cu_seqlens_q.data_ptr(),
-          seqlens_k.data_ptr(), page_table.data_ptr(), B, int(max_seqlen_q), int(max_seqlen_k),
-          total_q, max_pages, pages, ps, H, Hkv, d, float(scale), 1 if causal else 0,
-          int(num_ctas), _at(workspace), nbytes)
-
-
-def _check_decode_io(q, o, lse, d):
-    torch = _torch()
-    shape = q.shape
-    if len(shape) != 3 or shape[2] != d or o.shape != shape:
-        raise ValueError("q and o must be [total_q, H, d]")
-    if q.dtype != torch.bfloat16 or o.dtype != torch.bfloat16:
-        raise TypeError("q and o must be bfloat16")
-    if not q.is_contiguous() or not o.is_contiguous():
-        raise ValueError("q and o must be contiguous")
-    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous()
-                            or lse.shape != (shape[1], shape[0])):
-        raise ValueError("lse must be contiguous fp32 [H, total_q]")
-
-
-@functools.lru_cache(maxsize=256)
-def _decode_cache_plan(index, B, H, Hkv, d, max_q, max_k):
-    """(thread blocks, workspace bytes) for these sizes on device `index` (the current one)."""
-    n = fa_decode_cache_num_ctas(B, H, Hkv, max_q, max_k)
-    return n, fa_decode_cache_workspace_bytes(H, Hkv, d, max_q, n)
+    cu_seqlens_q int32 [B + 1], seqlens_k int32 [B], page_table int32 [B, max_pages]; workspace
+    (fa_decode_cache_workspace_bytes) may be None for num_ctas = 1."""
+    if o is None:
+        raise ValueError("o must be given")
+    if num_ctas < 1:
+        raise ValueError("num_ctas must be >= 1")
+    if stream is not None:
+        with _on(stream, q):
+            return fa_fwd_decode_cache(q, cache, o, lse, cu_seqlens_q, seqlens_k, page_table,
+                                       max_seqlen_q, max_seqlen_k, scale, causal, num_ctas,
+                                       workspace)
+    _done(_native().decode_cache(*_entry(*_DECODE_CACHE), q, *cache, o, lse, workspace,
+                                 cu_seqlens_q, seqlens_k, page_table, max_seqlen_q, max_seqlen_k,
+                                 scale, causal, num_ctas))
 
 
 def forward_decode_cache(q, cache: PagedCache, cu_seqlens_q, seqlens_k, page_table,
                          max_seqlen_q: int, max_seqlen_k: int, scale: float | None = None,
                          causal: bool = False, num_ctas: int | None = None, stream=None):
     """Allocate O, LSE (and the workspace) and run fa_fwd_decode_cache."""
-    index = _device(q)
-    place = _place(index, stream)
-    if place is not None:
-        with place:
+    if stream is not None:
+        with _on(stream, q):
             return forward_decode_cache(q, cache, cu_seqlens_q, seqlens_k, page_table,
                                         max_seqlen_q, max_seqlen_k, scale, causal, num_ctas)
-    torch = _torch()
-    total_q, H, d = q.shape
-    Hkv, dev = cache.k.shape[1], q.device
-    if num_ctas is None:
-        num_ctas, nbytes = _decode_cache_plan(index, page_table.shape[0], H, Hkv, d, max_seqlen_q,
-                                              max_seqlen_k)
-    else:
-        nbytes = fa_decode_cache_workspace_bytes(H, Hkv, d, max_seqlen_q, num_ctas)
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=dev) if nbytes else None
-    o = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    lse = torch.empty((H, total_q), dtype=torch.float32, device=dev)
-    fa_fwd_decode_cache(q, cache, o, lse, cu_seqlens_q, seqlens_k, page_table, max_seqlen_q,
-                        max_seqlen_k, d ** -0.5 if scale is None else scale, causal, num_ctas, ws)
-    return o, lse
+    return _done(_native().decode_cache(
+        *_entry(*_DECODE_CACHE), q, *cache, None, None, None, cu_seqlens_q, seqlens_k, page_table,
+        max_seqlen_q, max_seqlen_k, q.shape[-1] ** -0.5 if scale is None else scale, causal,
+        num_ctas or 0))
 
 
 # --------------------------------------------------------------------------- shared prefixes
@@ -815,6 +673,10 @@ def fa_decode_shared_workspace_bytes(total_q: int, H: int, d: int, num_ctas: int
     return int(load().fa_decode_shared_workspace_bytes(total_q, H, d, num_ctas))
 
 
+_DECODE_SHARED = ("fa_fwd_decode_shared", "fa_decode_shared_num_ctas",
+                  "fa_decode_shared_workspace_bytes")
+
+
 def fa_fwd_decode_shared(q, k_prefix, v_prefix, k, v, o, lse, cu_seqlens_q, cu_seqlens_k,
                          cu_groups, cu_seqlens_p, max_seqlen_q: int, max_seqlen_k: int,
                          max_group_q: int, max_seqlen_p: int, scale: float, causal: bool,
@@ -822,35 +684,20 @@ def fa_fwd_decode_shared(q, k_prefix, v_prefix, k, v, o, lse, cu_seqlens_q, cu_s
     """C ``fa_fwd_decode_shared``: q, o [total_q, H, d]; k_prefix, v_prefix [total_p, Hkv, d];
     k, v [total_k, Hkv, d] (bf16); lse [H, total_q] fp32 or None; cu_seqlens_q, cu_seqlens_k
     int32 [B + 1]; cu_groups (first sequence of each group), cu_seqlens_p int32 [groups + 1]."""
-    torch = _torch()
-    total_q, H, d = q.shape
-    _check_decode_io(q, o, lse, d)
-    Hkv = k.shape[1]
-    _check_rows(k, v, Hkv, d)
-    _check_rows(k_prefix, v_prefix, Hkv, d)
-    for t in (k, v, k_prefix, v_prefix):
-        if t.dtype != torch.bfloat16 or not t.is_contiguous():
-            raise ValueError("keys and values must be contiguous bfloat16")
-    B, groups = cu_seqlens_q.numel() - 1, cu_groups.numel() - 1
-    _int32("cu_seqlens_q", cu_seqlens_q, B + 1)
-    _int32("cu_seqlens_k", cu_seqlens_k, B + 1)
-    _int32("cu_groups", cu_groups, groups + 1)
-    _int32("cu_seqlens_p", cu_seqlens_p, groups + 1)
-    index = _device(q, k_prefix, v_prefix, k, v, o, lse, cu_seqlens_q, cu_seqlens_k, cu_groups,
-                    cu_seqlens_p, workspace)
-    _call(load().fa_fwd_decode_shared, index, stream, q.data_ptr(), k_prefix.data_ptr(),
-          v_prefix.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), _at(lse),
-          cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), cu_groups.data_ptr(),
-          cu_seqlens_p.data_ptr(), B, groups, int(max_seqlen_q), int(max_seqlen_k),
-          int(max_group_q), int(max_seqlen_p), total_q, k.shape[0], k_prefix.shape[0], H, Hkv, d,
-          float(scale), 1 if causal else 0, int(num_ctas), workspace.data_ptr(),
-          workspace.numel() * workspace.element_size())
-
-
-@functools.lru_cache(maxsize=None)
-def _decode_shared_ctas(index):
-    """fa_decode_shared_num_ctas of device `index` (the current one)."""
-    return fa_decode_shared_num_ctas()
+    if o is None:
+        raise ValueError("o must be given")
+    if num_ctas < 1:
+        raise ValueError("num_ctas must be >= 1")
+    if stream is not None:
+        with _on(stream, q):
+            return fa_fwd_decode_shared(q, k_prefix, v_prefix, k, v, o, lse, cu_seqlens_q,
+                                        cu_seqlens_k, cu_groups, cu_seqlens_p, max_seqlen_q,
+                                        max_seqlen_k, max_group_q, max_seqlen_p, scale, causal,
+                                        num_ctas, workspace)
+    _done(_native().decode_shared(*_entry(*_DECODE_SHARED), q, k_prefix, v_prefix, k, v, o, lse,
+                                  workspace, cu_seqlens_q, cu_seqlens_k, cu_groups, cu_seqlens_p,
+                                  max_seqlen_q, max_seqlen_k, max_group_q, max_seqlen_p, scale,
+                                  causal, num_ctas))
 
 
 def forward_decode_shared(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seqlens_k, cu_groups,
@@ -858,23 +705,12 @@ def forward_decode_shared(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seqlens_
                           max_seqlen_p: int, scale: float | None = None, causal: bool = False,
                           num_ctas: int | None = None, stream=None):
     """Allocate O, LSE and the workspace and run fa_fwd_decode_shared."""
-    index = _device(q)
-    place = _place(index, stream)
-    if place is not None:
-        with place:
+    if stream is not None:
+        with _on(stream, q):
             return forward_decode_shared(q, k_prefix, v_prefix, k, v, cu_seqlens_q, cu_seqlens_k,
                                          cu_groups, cu_seqlens_p, max_seqlen_q, max_seqlen_k,
                                          max_group_q, max_seqlen_p, scale, causal, num_ctas)
-    torch = _torch()
-    total_q, H, d = q.shape
-    dev = q.device
-    if num_ctas is None:
-        num_ctas = _decode_shared_ctas(index)
-    ws = torch.empty(fa_decode_shared_workspace_bytes(total_q, H, d, num_ctas), dtype=torch.uint8,
-                     device=dev)
-    o = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    lse = torch.empty((H, total_q), dtype=torch.float32, device=dev)
-    fa_fwd_decode_shared(q, k_prefix, v_prefix, k, v, o, lse, cu_seqlens_q, cu_seqlens_k,
-                         cu_groups, cu_seqlens_p, max_seqlen_q, max_seqlen_k, max_group_q,
-                         max_seqlen_p, d ** -0.5 if scale is None else scale, causal, num_ctas, ws)
-    return o, lse
+    return _done(_native().decode_shared(
+        *_entry(*_DECODE_SHARED), q, k_prefix, v_prefix, k, v, None, None, None, cu_seqlens_q,
+        cu_seqlens_k, cu_groups, cu_seqlens_p, max_seqlen_q, max_seqlen_k, max_group_q,
+        max_seqlen_p, q.shape[-1] ** -0.5 if scale is None else scale, causal, num_ctas or 0))

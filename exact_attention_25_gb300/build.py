@@ -21,6 +21,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfa.so")
 BUILD_CHECKED = os.path.join(PKG, "_build_checked")
 LIB_CHECKED = os.path.join(PKG, "libfa_checked.so")
+BINDING = os.path.join(PKG, "_serve.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
          "-I", os.path.join(ROOT, "include")]
@@ -83,10 +84,42 @@ def build(force: bool = False, verbose_ptxas: bool = False, checked: bool = Fals
     return lib
 
 
+def build_binding(force: bool = False) -> str:
+    """Compile the native binding of the serving calls (``_serve.so``, a Python extension that
+    allocates through torch and calls the C entry points by address); returns its path."""
+    import sysconfig
+
+    import torch
+
+    src = os.path.join(CSRC, "serve_binding.cpp")
+    header = os.path.join(ROOT, "include", "fa.h")
+    if (not force and os.path.exists(BINDING)
+            and os.path.getmtime(BINDING) > max(os.path.getmtime(src), os.path.getmtime(header))):
+        return BINDING
+    tdir = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(tdir, "include"),
+           "-isystem", os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
+           "-isystem", os.path.join(cuda, "include"), src, "-o", tmp,
+           "-L", os.path.join(tdir, "lib"), "-Wl,-rpath," + os.path.join(tdir, "lib"),
+           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, BINDING)
+    return BINDING
+
+
 def build_all(force: bool = False) -> list[str]:
-    """Both variants, compiled concurrently."""
-    with cf.ThreadPoolExecutor(max_workers=2) as ex:
-        return list(ex.map(lambda c: build(force, checked=c), (False, True)))
+    """Both variants and the native binding, compiled concurrently."""
+    with cf.ThreadPoolExecutor(max_workers=3) as ex:
+        jobs = [ex.submit(build, force, checked=c) for c in (False, True)]
+        jobs.append(ex.submit(build_binding, force))
+        return [j.result() for j in jobs]
 
 
 if __name__ == "__main__":
