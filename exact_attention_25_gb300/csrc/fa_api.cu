@@ -1599,11 +1599,12 @@ extern "C" int fa_fwd_decode_shared(const void* q, const void* k_prefix, const v
     max_seqlen_p = std::min(max_seqlen_p, total_p);
     const int tok = std::min(128 / G, total_q);
     const long long places =
-        static_cast<long long>(num_groups) * Hkv * ((max_group_q + tok - 1) / tok) * ((max_seqlen_p + 127) / 128 + fa::kUnitCost) +
-        static_cast<long long>(B) * Hkv * ((max_seqlen_q + tok - 1) / tok) * ((max_seqlen_k + 127) / 128 + fa::kUnitCost);
+        static_cast<long long>(num_groups) * Hkv * ((max_group_q + tok - 1) / tok) * ((max_seqlen_p + 127) / 128 + fa::kSharedUnitCost) +
+        static_cast<long long>(B) * Hkv * ((max_seqlen_q + tok - 1) / tok) * ((max_seqlen_k + 127) / 128 + fa::kSharedUnitCost);
     if (places >= (1LL << 31) || static_cast<long long>(B) * H * max_seqlen_q >= (1LL << 31) ||
-        static_cast<long long>(B) + num_groups >= (1LL << 31) - 64)
-        return fail(FA_ERR_TOO_LARGE, "the batch must have fewer than 2^31 blocks of 128 keys, and B*H*max_seqlen_q < 2^31");
+        static_cast<long long>(B) + num_groups > 16384)
+        return fail(FA_ERR_TOO_LARGE, "the batch must have fewer than 2^31 blocks of 128 keys, B*H*max_seqlen_q < 2^31 "
+                                      "and at most 16384 sequences and groups");
     const size_t need = fa_decode_shared_workspace_bytes(total_q, H, d, num_ctas);
     if (!workspace || workspace_bytes < need)
         return fail(FA_ERR_WORKSPACE, "workspace must hold " + std::to_string(need) + " bytes");
@@ -1625,6 +1626,8 @@ extern "C" int fa_fwd_decode_shared(const void* q, const void* k_prefix, const v
     p.total_q = total_q; p.total_k = total_k; p.total_p = total_p;
     p.tile_tokens = tok;
     p.ctas = num_ctas;
+    p.head_groups = std::min(Hkv, num_ctas);
+    p.parts = num_ctas / p.head_groups;
     p.scale_log2 = scale * fa::kLog2e; p.causal = causal;
     p.status = di->status; p.wait_limit_ns = g_wait_limit_ns; p.debug_flags = g_debug_flags;
     const int cut = (g_debug_flags & fa::kDebugShrinkExtents) ? 1 : 0;

@@ -19,7 +19,7 @@ namespace fa {
 
 namespace {
 
-constexpr int kCacheThreads = 256;
+constexpr int kCacheThreads = 128;
 constexpr int kCacheTokens = 16;  // tokens of a warp: pages hold a multiple of this
 
 // 16 elements of a row as floats
@@ -58,6 +58,40 @@ __device__ __forceinline__ void pack16(const float* f, uint4* w, const float*)
     for (int h = 0; h < 4; ++h)
         w[h] = make_uint4(__float_as_uint(f[4 * h]), __float_as_uint(f[4 * h + 1]),
                           __float_as_uint(f[4 * h + 2]), __float_as_uint(f[4 * h + 3]));
+}
+
+// The largest |x| of a lane's 16 elements as fp32 bits (infinities and NaNs largest of all), and the
+// same over the finite ones.  bf16 values compare as 16-bit integers, two at a time.
+__device__ __forceinline__ uint32_t amax16(const uint4* w, const __nv_bfloat16*)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t u[4] = {w[h].x, w[h].y, w[h].z, w[h].w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m = __vmaxu2(m, u[i] & 0x7fff7fffu);
+    }
+    return max(m << 16, m & 0xffff0000u);
+}
+__device__ __forceinline__ uint32_t amax16(const uint4* w, const float*)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+        m = max(max(m, w[h].x & 0x7fffffffu), w[h].y & 0x7fffffffu);
+        m = max(max(m, w[h].z & 0x7fffffffu), w[h].w & 0x7fffffffu);
+    }
+    return m;
+}
+__device__ __forceinline__ uint32_t amax16_finite(const float* f)
+{
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const uint32_t a = __float_as_uint(f[i]) & 0x7fffffffu;
+        m = max(m, a < 0x7f800000u ? a : 0u);
+    }
+    return m;
 }
 
 // The biased exponent of a row whose largest finite |x| has the bits `amax`: with amax = m 2^E
@@ -139,22 +173,25 @@ __global__ void __launch_bounds__(kCacheThreads) fa_cache_append_kernel(const Ca
         }
 #pragma unroll
         for (int s = 0; s < NI; ++s) {
-            float f[16];
-            unpack16(x[s], f, src);
-            uint32_t amax = 0;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const uint32_t a = __float_as_uint(f[i]) & 0x7fffffffu;
-                amax = max(amax, a < 0x7f800000u ? a : 0u);
-            }
+            uint32_t amax = amax16(x[s], src);
 #pragma unroll
             for (int m = 1; m < LR; m *= 2) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, m));
+            float f[16];
+            unpack16(x[s], f, src);
+            const bool odd = amax >= 0x7f800000u;
+            if (__any_sync(0xffffffffu, odd)) {  // a row with infinities or NaNs, rarely
+                uint32_t fin = amax16_finite(f);
+#pragma unroll
+                for (int m = 1; m < LR; m *= 2) fin = max(fin, __shfl_xor_sync(0xffffffffu, fin, m));
+                amax = fin;
+                // the conversion would saturate an infinity: x * 0 is NaN for it and for NaN
+#pragma unroll
+                for (int i = 0; i < 16; ++i) f[i] = fmaf(f[i], 0.0f, f[i]);
+            }
             const int e = row_exponent(amax);
             const float scale = __uint_as_float(static_cast<uint32_t>(254 - e) << 23);  // 2^-(e-127)
-            // adding x * 0 turns an infinity into NaN (the conversion would saturate it) and
-            // leaves everything else as it is
 #pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] = fmaf(f[i], 0.0f, f[i] * scale);
+            for (int i = 0; i < 16; ++i) f[i] *= scale;
             const uint4 c = make_uint4(
                 pack_e4m3x4(f[0], f[1], f[2], f[3]), pack_e4m3x4(f[4], f[5], f[6], f[7]),
                 pack_e4m3x4(f[8], f[9], f[10], f[11]), pack_e4m3x4(f[12], f[13], f[14], f[15]));

@@ -158,43 +158,21 @@ __device__ __forceinline__ void sequence_work(const CacheDecodeParams& p, int b,
     u.in_seq = ((u.nq * p.G + p.rows_cta - 1) >> p.rows_shift) * p.Hkv;
 }
 
-// All lanes of a warp: the line's shares and, for the first place of share c, its sequence (u)
-// and `at`, its distance from that sequence's first place.  The search is skipped when the share
-// starts at the line's end.
+// All lanes of a warp: the line's shares and, for the first place of share c, its sequence (u) and
+// its distance from that sequence's first place.
 __device__ __forceinline__ Shares find_share(const CacheDecodeParams& p, int c, Unit& u, int& at)
 {
-    const int lane = threadIdx.x & 31;
-    auto work = [&](int b) {
-        if (b >= p.B) return 0;
-        Unit v;
-        sequence_work(p, b, v);
-        return v.in_seq * (v.nblk + kUnitCost);
-    };
-    const int w0 = work(lane);
-    int total = w0;
-    for (int b0 = 32; b0 < p.B; b0 += 32) total += work(b0 + lane);
-    total = __reduce_add_sync(0xffffffffu, total);
-    const Shares sh(total, p.ctas);
-    const int pos = sh.start(c);
-    if (pos >= total) return sh;
-    int run = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        const int w = b0 == 0 ? w0 : work(b0 + lane);
-        int sum = w;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int up = __shfl_up_sync(0xffffffffu, sum, d);
-            if (lane >= d) sum += up;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, run + sum > pos);
-        if (past) {
-            const int src = __ffs(past) - 1;
-            at = pos - run - __shfl_sync(0xffffffffu, sum - w, src);
-            sequence_work(p, b0 + src, u);
-            break;
-        }
-        run += __shfl_sync(0xffffffffu, sum, 31);
-    }
+    int b = 0;
+    const Shares sh = find_share(
+        p.B, p.ctas, c,
+        [&](int x) {
+            if (x >= p.B) return 0;
+            Unit v;
+            sequence_work(p, x, v);
+            return v.in_seq * (v.nblk + kUnitCost);
+        },
+        b, at);
+    if (sh.start(c) < sh.total) sequence_work(p, b, u);
     return sh;
 }
 

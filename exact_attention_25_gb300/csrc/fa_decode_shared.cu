@@ -8,17 +8,24 @@
 //
 // What bounds it: reading prefix and own keys once (HBM), and for large groups the exponentials of
 // tokens x heads x prefix scores.  Both kinds of work are units of one line (units, below) shared
-// out evenly over the SMs, so memory-bound and arithmetic-bound units run side by side.
+// out evenly over the SMs, so memory-bound and arithmetic-bound units run side by side.  Every
+// key/value head has a line of its own, the same for all, and CTA c works on head c mod Hkv: so the
+// CTAs of the heads read the same tokens at the same time.  (In one line over all heads each read its
+// 256-byte pieces of the token rows at a time of its own, and HBM gave 4 TB/s.)
 //
 // A unit is a tile of up to 128 query rows (row r = i * G + g: token i of the tile, head g of the G
 // that share the K/V head) against the keys of one prefix or sequence.  Roles (6 warps): warps 0-3
 // softmax (thread = tile row = TMEM lane), warp 4 TMA producer, warp 5 TMEM allocator and MMA
-// issuer.  All of them run over the CTA's whole share without a barrier between units: Q tiles and
-// O accumulators alternate between two buffers, so a unit's first scores are computed while the
-// softmax warps still write out the unit before it.  TMEM: two S buffers [0,128), [128,256) (P of a
-// block, bf16 pairs, overwrites the upper half of its S buffer), two O buffers from 256 on.
+// issuer.  All of them run over the CTA's whole share without a barrier between units: O accumulators
+// alternate between two buffers and Q is free after a unit's last scores, so the next unit's first
+// scores are computed while the softmax warps still write out the one before.  The rings take all the
+// rest of shared memory: at 1500 clocks a block of 64 KB, a copy's latency of about 3000 under load
+// needs 130 KB in flight beside the tiles in use (five tiles and a second Q buffer: 2000-2300 clocks).  TMEM: two S buffers [0,128), [128,256) (P of a
+// block, bf16 pairs, overwrites the lower half of its S buffer), two O buffers from 256 on.
 #include "fa_serve.cuh"
 #include "tc_ptx.cuh"
+
+#include <type_traits>
 
 namespace fa {
 
@@ -33,8 +40,8 @@ struct SharedCfg {
     static constexpr int PANEL_BYTES = 128 * 128;  // 128 rows x 128 bytes
     static constexpr int TILE_BYTES = PANELS * PANEL_BYTES;
     static constexpr int KST = D == 128 ? 3 : 6;   // stages of the K and V rings
-    static constexpr int VST = D == 128 ? 2 : 5;
-    static constexpr int SMEM_BYTES = (2 + KST + VST) * TILE_BYTES + 1024;
+    static constexpr int VST = KST;
+    static constexpr int SMEM_BYTES = (1 + KST + VST) * TILE_BYTES + 1024;
     static constexpr int THREADS = 192;
     static constexpr uint32_t TMEM_COLS = 512;
     static constexpr float RESCALE_THRESHOLD = 8.0f;  // log2 units, as in the forward kernel
@@ -46,13 +53,13 @@ struct SharedUnit {
     int hk, tile;          // key/value head, tile of tokens
     int tok0, ntok;        // the item's tokens: first row, count
     int k0, nk, nblk;      // its keys
-    int in_item;           // units of the item
+    int in_item;           // tiles of tokens of the item (units for each head)
     int jb, J;             // this share's blocks of the unit: [jb, jb + J)
     int first;             // the share's first unit
     int odd;               // V holds infinities or NaNs that only some of the tile's rows see
 };
 
-// Sizes of an item: in_item units of nblk blocks each (none without tokens or keys).
+// Sizes of an item: for each head in_item units of nblk blocks (none without tokens or keys).
 __device__ __forceinline__ void shared_item(const SharedDecodeParams& p, int x, SharedUnit& u)
 {
     u.item = x;
@@ -66,7 +73,7 @@ __device__ __forceinline__ void shared_item(const SharedDecodeParams& p, int x, 
         u.nk = packed_rows(p.cu_k, x - p.groups, p.total_k, p.max_k, u.k0);
     }
     u.nblk = (u.nk + kSB - 1) / kSB;
-    u.in_item = u.nk > 0 ? (u.ntok + p.tile_tokens - 1) / p.tile_tokens * p.Hkv : 0;
+    u.in_item = u.nk > 0 ? (u.ntok + p.tile_tokens - 1) / p.tile_tokens : 0;
 }
 
 __device__ __forceinline__ int shared_places(const SharedDecodeParams& p, int x)
@@ -74,41 +81,23 @@ __device__ __forceinline__ int shared_places(const SharedDecodeParams& p, int x)
     if (x >= p.groups + p.B) return 0;
     SharedUnit u;
     shared_item(p, x, u);
-    return u.in_item * (u.nblk + kUnitCost);
+    return u.in_item * (u.nblk + kSharedUnitCost);
 }
 
-// All lanes of a warp: the places of the items before `stop` (all of them: the line's length).
-__device__ __forceinline__ int places_before(const SharedDecodeParams& p, int stop)
+// All lanes of a warp: the line's length, and the places of the items before x[0] and x[1].
+__device__ __forceinline__ int count_places(const SharedDecodeParams& p, const int* x, int* before)
 {
-    const int lane = threadIdx.x & 31;
-    int sum = 0;
-    for (int x0 = 0; x0 < stop; x0 += 32) sum += x0 + lane < stop ? shared_places(p, x0 + lane) : 0;
-    return __reduce_add_sync(0xffffffffu, sum);
-}
-
-// All lanes of a warp: the item at place pos of the line (below its length), and pos's distance
-// from the item's first place.
-__device__ __forceinline__ void find_item(const SharedDecodeParams& p, int pos, SharedUnit& u, int& at)
-{
-    const int lane = threadIdx.x & 31, items = p.groups + p.B;
-    int run = 0;
-    for (int x0 = 0; x0 < items; x0 += 32) {
-        const int w = shared_places(p, x0 + lane);
-        int sum = w;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int up = __shfl_up_sync(0xffffffffu, sum, d);
-            if (lane >= d) sum += up;
-        }
-        const uint32_t past = __ballot_sync(0xffffffffu, run + sum > pos);
-        if (past) {
-            const int src = __ffs(past) - 1;
-            at = pos - run - __shfl_sync(0xffffffffu, sum - w, src);
-            shared_item(p, x0 + src, u);
-            return;
-        }
-        run += __shfl_sync(0xffffffffu, sum, 31);
+    const int items = p.groups + p.B;
+    int sum = 0, b0 = 0, b1 = 0;
+    for (int i = threadIdx.x & 31; i < items; i += 32) {
+        const int w = shared_places(p, i);
+        sum += w;
+        b0 += i < x[0] ? w : 0;
+        b1 += i < x[1] ? w : 0;
     }
+    before[0] = __reduce_add_sync(0xffffffffu, b0);
+    before[1] = __reduce_add_sync(0xffffffffu, b1);
+    return __reduce_add_sync(0xffffffffu, sum);
 }
 
 // Two bf16 values, infinities and NaNs replaced by zero.
@@ -118,6 +107,55 @@ __device__ __forceinline__ uint32_t finite_bf16x2(uint32_t v)
     if ((v & 0x7f800000u) == 0x7f800000u) v &= 0x0000ffffu;
     return v;
 }
+
+// V of keys that some row of a unit does not see must not reach it as 0 * inf or 0 * NaN.  Of rows
+// [first, last) of a block's V tile (to the end of the 16-key step that the last key lies in), those
+// from `end` on, past the unit's keys, are zeroed; of the others, which some queries see, what is not
+// finite is taken out, and given back to those queries at the unit's end (add_odd_v).  Each softmax warp
+// takes every fourth row.  Returns whether this lane took anything out.
+template <int D>
+__device__ __noinline__ bool clear_unseen_v(uint8_t* tile, int first, int end, int last)
+{
+    using C = SharedCfg<D>;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int LB = D / 16;  // bytes of a row for each lane: 4 or 8
+    const int at = lane * LB;
+    uint8_t* base = tile + (at >> 7) * C::PANEL_BYTES + (at & 127);
+    bool odd = false;
+    for (int row = first + warp; row < last; row += 4) {
+        uint32_t* w = reinterpret_cast<uint32_t*>(base + row * 128);
+#pragma unroll
+        for (int c = 0; c < LB / 4; ++c) {
+            if (row >= end) {
+                w[c] = 0u;
+            } else if (finite_bf16x2(w[c]) != w[c]) {
+                w[c] = finite_bf16x2(w[c]);
+                odd = true;
+            }
+        }
+    }
+    fence_proxy_async_smem();
+    return odd;
+}
+
+// Adds what is not finite in V rows [key0, key1) of a sequence to the row at dst.
+template <int D>
+__device__ __noinline__ void add_odd_v(const SharedDecodeParams& p, float* dst, const SharedUnit& un, int key0, int key1)
+{
+    for (int key = key0; key < key1; ++key) {
+        const long long off = (static_cast<long long>(un.k0 + key) * p.Hkv + un.hk) * D;
+        if (!in_extent(off, D, p.v_ext, p.status)) continue;
+        for (int c = 0; c < D; ++c) {
+            const float v = __bfloat162float(p.v[off + c]);
+            if (!(fabsf(v) < INFINITY)) dst[c] += v;
+        }
+    }
+}
+
+// A value that all lanes hold, in a form that the compiler knows to be the same in all of them: what the
+// MMA warp's loops depend on must be, or every operand of every MMA is moved to a uniform register on
+// its own (1370 clocks to issue the eight MMAs of a P V product instead of 600).
+__device__ __forceinline__ int warp_uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
 
 // S = Q K^T over D/16 k-steps (both operands K-major in 128B-swizzled panels).
 template <int D, int PANEL>
@@ -130,13 +168,19 @@ __device__ __forceinline__ void shared_issue_qk(uint32_t d_tmem, uint64_t qdesc,
     }
 }
 
-// O += P V: P (bf16 pairs) from TMEM, V (MN-major) from shared memory; 8 k-steps of 16 keys.
+// O += P V: P (bf16 pairs) from TMEM, V (MN-major) from shared memory; k-steps of 16 keys.
 __device__ __forceinline__ void shared_issue_pv(uint32_t d_tmem, uint32_t p_tmem, uint64_t vdesc,
-                                                uint32_t idesc, uint32_t acc_first)
+                                                uint32_t idesc, uint32_t acc_first, int steps)
 {
+    if (steps == 8) {
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks)
-        mma_ts_w(d_tmem, p_tmem + 8u * ks, sdesc_adv(vdesc, ks * 2048), idesc, ks > 0 ? 1u : acc_first);
+        for (int ks = 0; ks < 8; ++ks)
+            mma_ts_w(d_tmem, p_tmem + 8u * ks, sdesc_adv(vdesc, ks * 2048), idesc, ks > 0 ? 1u : acc_first);
+    } else {
+#pragma unroll 1
+        for (int ks = 0; ks < steps; ++ks)
+            mma_ts_w(d_tmem, p_tmem + 8u * ks, sdesc_adv(vdesc, ks * 2048), idesc, ks > 0 ? 1u : acc_first);
+    }
 }
 
 }  // namespace
@@ -154,10 +198,10 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* sQ = smem;
-    uint8_t* sK = sQ + 2 * C::TILE_BYTES;
+    uint8_t* sK = sQ + C::TILE_BYTES;
     uint8_t* sV = sK + C::KST * C::TILE_BYTES;
 
-    __shared__ __align__(8) uint64_t bar_qfull[2], bar_qempty[2];
+    __shared__ __align__(8) uint64_t bar_qfull, bar_qempty;
     __shared__ __align__(8) uint64_t bar_kfull[C::KST], bar_kempty[C::KST];
     __shared__ __align__(8) uint64_t bar_vfull[C::VST], bar_vempty[C::VST];
     __shared__ __align__(8) uint64_t bar_unit[kSharedUnits];
@@ -172,9 +216,9 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
+        mbar_init(&bar_qfull, 1);
+        mbar_init(&bar_qempty, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar_qfull[i], 1);
-            mbar_init(&bar_qempty[i], 1);
             mbar_init(&bar_sfull[i], 1);
             mbar_init(&bar_ofree[i], 4);
         }
@@ -211,18 +255,31 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
     const Watchdog wd{&abort_flag, p.status, p.wait_limit_ns};
     dependent_begin();
     const int cta = static_cast<int>(blockIdx.x);
+    // the items' places, by all warps, in the V ring (free until the first copy)
+    int* s_places = reinterpret_cast<int*>(sV);
+    const int items = p.groups + p.B;
+    for (int x = threadIdx.x; x < items; x += C::THREADS) s_places[x] = shared_places(p, x);
+    fence_proxy_async_smem();
+    __syncthreads();
 
     if (warp == 4) {
         // ------------------------------------------------------------- TMA producer
         // Copies in the order in which the products use them: K of block n, then V of block n - 1.
-        const Shares sh(places_before(p, p.groups + p.B), p.ctas);
-        int left = sh.start(cta + 1) - sh.start(cta);
+        // this CTA's heads are hg, hg + head_groups, ...: nh of them, taken in turn within a tile
+        const int hg = cta % p.head_groups, part = cta / p.head_groups;
+        const int nh = (p.Hkv - hg + p.head_groups - 1) / p.head_groups;
         SharedUnit un;
-        int at = 0, ui = 0, place = 0;
+        int at = 0, item = 0, ui = 0, place = 0, left = 0;
+        if (part < p.parts) {
+            const Shares sh = find_share(
+                items, p.parts, part, [&](int x) { return x < items ? s_places[x] * nh : 0; }, item, at);
+            left = sh.start(part + 1) - sh.start(part);
+        }
+        __syncwarp();
         if (left > 0) {
-            find_item(p, sh.start(cta), un, at);
-            ui = at / (un.nblk + kUnitCost);
-            place = at - ui * (un.nblk + kUnitCost);
+            shared_item(p, item, un);
+            ui = at / (un.nblk + kSharedUnitCost);
+            place = at - ui * (un.nblk + kSharedUnitCost);
         }
         bool ok = true;
         int n = 0, k = 0;                // blocks and units so far
@@ -240,12 +297,12 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
         };
         int v_issued = 0;
         while (ok && left > 0) {
-            const int end = min(un.nblk + kUnitCost, place + left);
+            const int end = min(un.nblk + kSharedUnitCost, place + left);
             left -= end - place;
-            un.hk = ui % p.Hkv;
-            un.tile = ui / p.Hkv;
-            un.jb = max(0, place - kUnitCost);
-            un.J = max(0, end - kUnitCost) - un.jb;
+            un.tile = ui / nh;
+            un.hk = hg + (ui - un.tile * nh) * p.head_groups;
+            un.jb = max(0, place - kSharedUnitCost);
+            un.J = max(0, end - kSharedUnitCost) - un.jb;
             un.first = k == 0;
             un.odd = 0;
             const CUtensorMap* k_map = un.item < p.groups ? &tm_kp : &tm_k;
@@ -259,14 +316,13 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
                     __syncwarp();
                     // Q: one 3-D box of (64 columns, G heads, tile_tokens tokens) per panel, rows in
                     // (token, head) order; tile rows past it are never written and never stored
-                    const int qs = k & 1;
-                    ok = warp_wait_all(&bar_qempty[qs], ((k >> 1) & 1) ^ 1, wd, kSiteSharedEmpty);
+                    ok = warp_wait_all(&bar_qempty, (k & 1) ^ 1, wd, kSiteSharedEmpty);
                     if (!ok) break;
-                    mbar_arrive_expect_tx_w(&bar_qfull[qs],
+                    mbar_arrive_expect_tx_w(&bar_qfull,
                                             static_cast<uint32_t>(C::PANELS * 128 * p.G * p.tile_tokens));
                     for (int pn = 0; pn < C::PANELS; ++pn)
-                        tma_load_3d_w(sQ + qs * C::TILE_BYTES + pn * C::PANEL_BYTES, &tm_q, &bar_qfull[qs],
-                                      64 * pn, un.hk * p.G, un.tok0 + un.tile * p.tile_tokens);
+                        tma_load_3d_w(sQ + pn * C::PANEL_BYTES, &tm_q, &bar_qfull, 64 * pn, un.hk * p.G,
+                                      un.tok0 + un.tile * p.tile_tokens);
                     ++k;
                 }
                 const int s = n % C::KST;
@@ -285,7 +341,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
                 v_row = row;
             }
             place = 0;
-            if (left > 0 && ++ui >= un.in_item) {
+            if (left > 0 && ++ui >= un.in_item * nh) {
                 ui = 0;
                 do shared_item(p, un.item + 1, un);
                 while (un.in_item == 0);
@@ -302,7 +358,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
         // no copy may land after the CTA exits (bounded waits that ignore the abort flag)
         volatile int no_abort = 0;
         const Watchdog wd_drain{&no_abort, p.status, p.wait_limit_ns};
-        for (int i = max(0, k - 2); i < k; ++i) mbar_wait(&bar_qfull[i & 1], (i >> 1) & 1, wd_drain, kSiteSharedDrain);
+        if (k > 0) mbar_wait(&bar_qfull, (k - 1) & 1, wd_drain, kSiteSharedDrain);
         for (int i = max(0, n - C::KST); i < n; ++i)
             mbar_wait(&bar_kfull[i % C::KST], (i / C::KST) & 1, wd_drain, kSiteSharedDrain);
         for (int i = max(0, v_issued - C::VST); i < v_issued; ++i)
@@ -320,31 +376,34 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
         int committed_k = 0, committed_v = 0;
         bool ok = true;
         // the unit and block of the next S
-        int ku = 0, kj = 0, kJ = 0;
+        int ku = 0, kj = 0, kJ = 0, k_left = 0;
         // Issues S of block n if there is one: 1 issued, 0 none, -1 a wait gave up.
         auto issue_s = [&](int n) {
             if (kj == kJ) {
                 if (kJ > 0) ++ku;
                 if (!warp_wait_all(&bar_unit[ku % kSharedUnits], (ku / kSharedUnits) & 1, wd, kSiteSharedUnit)) return -1;
-                kJ = s_unit[ku % kSharedUnits].J;
+                const SharedUnit& un = s_unit[ku % kSharedUnits];
+                kJ = warp_uniform(un.J);
+                k_left = warp_uniform(un.nk - un.jb * kSB);
                 kj = 0;
                 if (kJ == 0) return 0;
-                if (!warp_wait_all(&bar_qfull[ku & 1], (ku >> 1) & 1, wd, kSiteSharedQ)) return -1;
+                if (!warp_wait_all(&bar_qfull, ku & 1, wd, kSiteSharedQ)) return -1;
             }
             const int s = n % C::KST;
             if (!warp_wait_all(&bar_kfull[s], (n / C::KST) & 1, wd, kSiteSharedK)) return -1;
             tc_fence_after();
-            shared_issue_qk<D, C::PANEL_BYTES>(tbase + 128u * (n & 1), sdesc_adv(dq0, (ku & 1) * C::TILE_BYTES),
-                                               sdesc_adv(dk0, s * C::TILE_BYTES), kIdS);
+            shared_issue_qk<D, C::PANEL_BYTES>(warp_uniform(tbase + 128 * (n & 1)), dq0,
+                                               sdesc_adv(dk0, warp_uniform(s * C::TILE_BYTES)), kIdS);
             mma_commit_w(&bar_sfull[n & 1]);
             mma_commit_w(&bar_kempty[s]);
             committed_k = n + 1;
-            if (++kj == kJ) mma_commit_w(&bar_qempty[ku & 1]);
+            if (++kj == kJ) mma_commit_w(&bar_qempty);
             return 1;
         };
         int more = issue_s(0);
         ok = more >= 0;
-        int vu = 0, vj = 0, vJ = ok && more ? s_unit[0].J : 0;  // unit and block of the next P V
+        // unit and block of the next P V, the unit's blocks here and keys from its first block here on
+        int vu = 0, vj = 0, vJ = kJ, v_left = k_left;
         for (int n = 0; ok && more > 0; ++n) {
             more = issue_s(n + 1);
             if (more < 0 || !warp_wait_all(&bar_pfull, n & 1, wd, kSiteSharedP)) { ok = false; break; }
@@ -355,8 +414,10 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
                 break;
             }
             tc_fence_after();
-            shared_issue_pv(tbase + 256u + 128u * (vu & 1), tbase + 128u * (n & 1) + 64u,
-                            sdesc_adv(dv0, s * C::TILE_BYTES), kIdPV, vj > 0 ? 1u : 0u);
+            // (16-key steps behind the unit's last key are left out)
+            shared_issue_pv(warp_uniform(tbase + 256 + 128 * (vu & 1)), warp_uniform(tbase + 128 * (n & 1)),
+                            sdesc_adv(dv0, warp_uniform(s * C::TILE_BYTES)), kIdPV, warp_uniform(vj > 0),
+                            warp_uniform(min(8, (v_left - vj * kSB + 15) / 16)));
             mma_commit_w(&bar_pv);
             mma_commit_w(&bar_vempty[s]);
             committed_v = n + 1;
@@ -364,6 +425,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
                 ++vu;
                 vj = 0;
                 vJ = kJ;
+                v_left = k_left;
             }
         }
         volatile int no_abort = 0;
@@ -404,130 +466,158 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
                 jmask = min(jmask, seen / kSB);
                 klim = min(klim, ti + shift);
             }
+            const int tok_tile = min(p.tile_tokens, un.ntok - un.tile * p.tile_tokens);
+            const bool valid = i < tok_tile;
+            const bool any_valid = __any_sync(0xffffffffu, valid);
             float m = -INFINITY, l = 0.0f, lr = 0.0f;
-            for (int jj = 0; jj < J; ++jj, ++n) {
-                const int j = jb + jj;
+            // One block.  MASKED blocks come last; apart, so that the others' loop holds neither the
+            // mask nor what follows it (with both in one loop every block took a third longer).
+            auto block = [&](auto masked_c, int j) {
+                constexpr bool MASKED = decltype(masked_c)::value;
                 const uint32_t tS = tbase + lane_base + 128u * (n & 1);
                 if (!warp_wait_all(&bar_sfull[n & 1], (n >> 1) & 1, wd, kSiteSharedS)) {
                     ok = false;
-                    break;
+                    return;
                 }
                 tc_fence_after();
-                uint32_t sr32[128];
-                tmem_ld32(tS + 0, sr32);
-                tmem_ld32(tS + 32, sr32 + 32);
-                tmem_ld32(tS + 64, sr32 + 64);
-                tmem_ld32(tS + 96, sr32 + 96);
-                tmem_wait_ld();
-                reg_fence32(sr32);
-                reg_fence32(sr32 + 32);
-                reg_fence32(sr32 + 64);
-                reg_fence32(sr32 + 96);
-                float x[128];
-#pragma unroll
-                for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(sr32[c]);
-                if (prescale) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c) x[c] *= c2;
-                }
-                if (j >= jmask) {
-                    const int lim = klim - j * kSB;  // last visible key column in this block
-#pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c > lim) x[c] = -INFINITY;
-                }
-                float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
-#pragma unroll
-                for (int c = 4; c < 124; c += 8) {
-                    mx0 = fmax3(mx0, x[c], x[c + 1]);
-                    mx1 = fmax3(mx1, x[c + 2], x[c + 3]);
-                    mx2 = fmax3(mx2, x[c + 4], x[c + 5]);
-                    mx3 = fmax3(mx3, x[c + 6], x[c + 7]);
-                }
-                mx0 = fmax3(mx0, x[124], x[125]);
-                mx1 = fmax3(mx1, x[126], x[127]);
-                const float mt = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * cf;
-                // rescale only when the max grew by more than the threshold (exact either way)
                 float alpha = 1.0f;
-                const bool need = mt > m + C::RESCALE_THRESHOLD;
-                if (need) {
-                    alpha = ex2(m - mt);
-                    m = mt;
-                    l *= alpha;
-                    lr *= alpha;
-                }
-                const float neg_m = (m == -INFINITY) ? 0.0f : -m;
-                const uint64_t cf2 = f2_make(cf, cf), nm2 = f2_make(neg_m, neg_m);
-                uint64_t lsa = f2_make(0.f, 0.f), lsb = lsa, lra = lsa, lrb = lsa;
+                bool need = false;
+                if (!MASKED && any_valid) {  // (else P stays what it was: rows that are never stored)
+                    uint32_t sr32[128];
+                    tmem_ld32(tS + 0, sr32);
+                    tmem_ld32(tS + 32, sr32 + 32);
+                    tmem_ld32(tS + 64, sr32 + 64);
+                    tmem_ld32(tS + 96, sr32 + 96);
+                    tmem_wait_ld();
+                    reg_fence32(sr32);
+                    reg_fence32(sr32 + 32);
+                    reg_fence32(sr32 + 64);
+                    reg_fence32(sr32 + 96);
+                    float x[128];
 #pragma unroll
-                for (int cb = 0; cb < 4; ++cb) {
-                    uint32_t pk[16];
+                    for (int c = 0; c < 128; ++c) x[c] = __uint_as_float(sr32[c]);
+                    if (prescale) {
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        const int e = cb * 32 + c;
-                        float p0, p1, p2, p3;
-                        f2_split(f2_fma(f2_make(x[e], x[e + 1]), cf2, nm2), p0, p1);
-                        f2_split(f2_fma(f2_make(x[e + 2], x[e + 3]), cf2, nm2), p2, p3);
-                        p0 = ex2(p0);
-                        p1 = ex2(p1);
-                        p2 = ex2(p2);
-                        p3 = ex2(p3);
-                        const uint32_t w01 = pack_bf16x2(p0, p1);
-                        const uint32_t w23 = pack_bf16x2(p2, p3);
-                        lsa = f2_add(lsa, f2_make(p0, p1));
-                        lsb = f2_add(lsb, f2_make(p2, p3));
-                        // lr sums the bf16-rounded weights the P V product uses
-                        lra = f2_add(lra, f2_make(__uint_as_float(w01 << 16), __uint_as_float(w01 & 0xFFFF0000u)));
-                        lrb = f2_add(lrb, f2_make(__uint_as_float(w23 << 16), __uint_as_float(w23 & 0xFFFF0000u)));
-                        pk[c / 2] = w01;
-                        pk[c / 2 + 1] = w23;
+                        for (int c = 0; c < 128; ++c) x[c] *= c2;
                     }
-                    tmem_st16(tS + 64u + 16u * cb, pk);
+                    float mx0 = x[0], mx1 = x[1], mx2 = x[2], mx3 = x[3];
+#pragma unroll
+                    for (int c = 4; c < 124; c += 8) {
+                        mx0 = fmax3(mx0, x[c], x[c + 1]);
+                        mx1 = fmax3(mx1, x[c + 2], x[c + 3]);
+                        mx2 = fmax3(mx2, x[c + 4], x[c + 5]);
+                        mx3 = fmax3(mx3, x[c + 6], x[c + 7]);
+                    }
+                    mx0 = fmax3(mx0, x[124], x[125]);
+                    mx1 = fmax3(mx1, x[126], x[127]);
+                    const float mt = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * cf;
+                    // rescale only when the max grew by more than the threshold (exact either way)
+                    need = mt > m + C::RESCALE_THRESHOLD;
+                    if (need) {
+                        alpha = ex2(m - mt);
+                        m = mt;
+                        l *= alpha;
+                        lr *= alpha;
+                    }
+                    const float neg_m = (m == -INFINITY) ? 0.0f : -m;
+                    const uint64_t cf2 = f2_make(cf, cf), nm2 = f2_make(neg_m, neg_m);
+                    uint64_t lsa = f2_make(0.f, 0.f), lsb = lsa, lra = lsa, lrb = lsa;
+#pragma unroll
+                    for (int cb = 0; cb < 4; ++cb) {
+                        uint32_t pk[16];
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            const int e = cb * 32 + c;
+                            float p0, p1, p2, p3;
+                            f2_split(f2_fma(f2_make(x[e], x[e + 1]), cf2, nm2), p0, p1);
+                            f2_split(f2_fma(f2_make(x[e + 2], x[e + 3]), cf2, nm2), p2, p3);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            p2 = ex2(p2);
+                            p3 = ex2(p3);
+                            const uint32_t w01 = pack_bf16x2(p0, p1);
+                            const uint32_t w23 = pack_bf16x2(p2, p3);
+                            lsa = f2_add(lsa, f2_make(p0, p1));
+                            lsb = f2_add(lsb, f2_make(p2, p3));
+                            // lr sums the bf16-rounded weights the P V product uses
+                            lra = f2_add(lra, f2_make(__uint_as_float(w01 << 16), __uint_as_float(w01 & 0xFFFF0000u)));
+                            lrb = f2_add(lrb, f2_make(__uint_as_float(w23 << 16), __uint_as_float(w23 & 0xFFFF0000u)));
+                            pk[c / 2] = w01;
+                            pk[c / 2 + 1] = w23;
+                        }
+                        tmem_st16(tS + 16u * cb, pk);
+                    }
+                    {
+                        float a0, a1, b0, b1;
+                        f2_split(f2_add(lsa, lsb), a0, a1);
+                        f2_split(f2_add(lra, lrb), b0, b1);
+                        l += a0 + a1;
+                        lr += b0 + b1;
+                    }
                 }
-                {
-                    float a0, a1, b0, b1;
-                    f2_split(f2_add(lsa, lsb), a0, a1);
-                    f2_split(f2_add(lra, lrb), b0, b1);
-                    l += a0 + a1;
-                    lr += b0 + b1;
+                if (MASKED && any_valid) {
+                    // 32 columns at a time, up to the last that any row needs; P of a chunk goes where
+                    // S of that chunk or of one before it was.  Rolled up: these blocks are one in a
+                    // unit, and code that is fetched for them alone costs more than their time.
+                    const int lim = klim - j * kSB;  // last visible key column in this block
+                    const int chunks = min(4, (nk - j * kSB + 31) / 32);
+                    float mt = -INFINITY;
+#pragma unroll 1
+                    for (int cb = 0; cb < chunks; ++cb) {
+                        uint32_t v[32];
+                        tmem_ld32(tS + 32u * cb, v);
+                        tmem_wait_ld();
+                        reg_fence32(v);
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (32 * cb + c <= lim) mt = fmaxf(mt, __uint_as_float(v[c]) * c2);
+                    }
+                    need = mt > m + C::RESCALE_THRESHOLD;
+                    if (need) {
+                        alpha = ex2(m - mt);
+                        m = mt;
+                        l *= alpha;
+                        lr *= alpha;
+                    }
+                    const float neg_m = (m == -INFINITY) ? 0.0f : -m;
+#pragma unroll 1
+                    for (int cb = 0; cb < chunks; ++cb) {
+                        uint32_t v[32], pk[16];
+                        tmem_ld32(tS + 32u * cb, v);
+                        tmem_wait_ld();
+                        reg_fence32(v);
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            float w[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const float xs = __uint_as_float(v[c + e]);
+                                w[e] = 32 * cb + c + e <= lim ? ex2(fmaf(xs, c2, neg_m)) : 0.0f;
+                                l += w[e];
+                            }
+                            pk[c / 2] = pack_bf16x2(w[0], w[1]);
+                            lr += __uint_as_float(pk[c / 2] << 16) + __uint_as_float(pk[c / 2] & 0xFFFF0000u);
+                        }
+                        tmem_st16(tS + 16u * cb, pk);
+                    }
                 }
-                if (j >= jmask) {
-                    // V of keys that some row does not see must not reach it as 0 * inf or 0 * NaN:
-                    // rows past the keys' end (whatever lies there) are zeroed; of rows that some
-                    // queries see, what is not finite is taken out here and given back to those
-                    // queries at the unit's end.
-                    const int key = j * kSB + r;
-                    if (__any_sync(0xffffffffu, key >= seen)) {
+                if constexpr (MASKED) {
+                    const int first = max(0, seen - j * kSB), end = nk - j * kSB;
+                    const int last = min(kSB, (end + 15) & ~15);
+                    if (first < last) {
                         const int s = n % C::VST;
                         if (!warp_wait_all(&bar_vfull[s], (n / C::VST) & 1, wd, kSiteSharedV)) {
                             ok = false;
-                            break;
+                            return;
                         }
-                        if (key >= seen) {
-                            for (int c = 0; c < D / 8; ++c) {
-                                uint4* at = reinterpret_cast<uint4*>(
-                                    sV + s * C::TILE_BYTES + (c / 8) * C::PANEL_BYTES + r * 128 + (c % 8) * 16);
-                                if (key >= nk) {
-                                    *at = make_uint4(0u, 0u, 0u, 0u);
-                                    continue;
-                                }
-                                const uint4 v = *at;
-                                const uint4 f = make_uint4(finite_bf16x2(v.x), finite_bf16x2(v.y),
-                                                           finite_bf16x2(v.z), finite_bf16x2(v.w));
-                                if (f.x != v.x || f.y != v.y || f.z != v.z || f.w != v.w) {
-                                    *at = f;
-                                    un.odd = 1;
-                                }
-                            }
-                        }
-                        fence_proxy_async_smem();
+                        if (clear_unseen_v<D>(sV + s * C::TILE_BYTES, first, end, last)) un.odd = 1;
                     }
                 }
                 // O holds the unit's blocks before this one once their last P V product has run
-                if (jj > 0) {
+                if (j > jb) {
                     if (!warp_wait_all(&bar_pv, (n - 1) & 1, wd, kSiteSharedO)) {
                         ok = false;
-                        break;
+                        return;
                     }
                     tc_fence_after();
                     if (__any_sync(0xffffffffu, need)) {
@@ -547,15 +637,17 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar_pfull);
-            }
+                ++n;
+            };
+            const int j1 = jb + J, j0 = min(j1, max(jb, jmask));
+            for (int j = jb; ok && j < j0; ++j) block(std::false_type{}, j);
+            for (int j = j0; ok && j < j1; ++j) block(std::true_type{}, j);
             // ------------------------------------------------------------- the unit's result
             // O normalised by its own weights and its natural-log LSE, in fp32 for the merge: to
             // the row's place if the share holds the whole unit, else to the share's part.
             if (ok) ok = warp_wait_all(&bar_pv, (n - 1) & 1, wd, kSiteSharedO);
             if (!ok) break;
             tc_fence_after();
-            const int tok_tile = min(p.tile_tokens, un.ntok - un.tile * p.tile_tokens);
-            const bool valid = i < tok_tile;
             const bool whole = J == un.nblk;
             const int h = un.hk * p.G + g;
             const float inv_l = lr > 0.0f ? 1.0f / lr : (lr == 0.0f ? 0.0f : NAN);
@@ -568,7 +660,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
             const bool in = valid && in_extent(row, 1, p.part_ext, p.status);
             const bool odd = *static_cast<volatile int*>(&un.odd) != 0;
 #pragma unroll 1
-            for (int ch = 0; ch < D / 32; ++ch) {
+            for (int ch = 0; any_valid && ch < D / 32; ++ch) {
                 uint32_t o[32];
                 tmem_ld32(tO + 32u * ch, o);
                 tmem_wait_ld();
@@ -576,21 +668,11 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
                 if (!in) continue;
 #pragma unroll
                 for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * inv_l);
-                if (odd) {
-                    const int key1 = min(min(nk, (jb + J) * kSB), klim + 1);
-                    for (int key = max(seen, jb * kSB); key < key1; ++key) {
-                        const long long off = (static_cast<long long>(un.k0 + key) * p.Hkv + un.hk) * D + 32 * ch;
-                        if (!in_extent(off, 32, p.v_ext, p.status)) continue;
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            const float v = __bfloat162float(p.v[off + c]);
-                            if (!(fabsf(v) < INFINITY)) o[c] = __float_as_uint(__uint_as_float(o[c]) + v);
-                        }
-                    }
-                }
                 st_row<4>(p.o_part + row * D + 32 * ch, o);
             }
             if (in) p.lse_part[row] = lse_row;
+            if (in && odd)
+                add_odd_v<D>(p, p.o_part + row * D, un, max(seen, jb * kSB), min(min(nk, (jb + J) * kSB), klim + 1));
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_ofree[k & 1]);
@@ -641,20 +723,23 @@ __global__ void __launch_bounds__(128) fa_decode_shared_merge_kernel(const Share
                 break;
             }
         }
-        const Shares sh(places_before(p, p.groups + p.B), p.ctas);
-        const int hk = h / p.G;
+        const int items[2] = {x, p.groups + b};
+        int before[2];
+        const int all = count_places(p, items, before);
+        const int hk = h / p.G, hg = hk % p.head_groups, hj = hk / p.head_groups;
+        const int nh = (p.Hkv - hg + p.head_groups - 1) / p.head_groups;
+        const Shares sh(all * nh, p.parts);
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
             const int ti = tok - u[z].tok0;
             if (u[z].in_item == 0 || ti < 0 || ti >= u[z].ntok) continue;
             const int tile = ti / p.tile_tokens;
-            const int start = places_before(p, u[z].item) +
-                              (tile * p.Hkv + hk) * (u[z].nblk + kUnitCost) + kUnitCost;
-            c0[z] = sh.share_of(start);
-            const int c1 = sh.share_of(start + u[z].nblk - 1);
-            count[z] = c1 - c0[z] + 1;
-            whole[z] = c1 == c0[z];
-            lead[z] = sh.start(c0[z]) >= start - kUnitCost ? 0 : 1;
+            const int start = before[z] * nh + (tile * nh + hj) * (u[z].nblk + kSharedUnitCost) + kSharedUnitCost;
+            const int s0 = sh.share_of(start), s1 = sh.share_of(start + u[z].nblk - 1);
+            c0[z] = s0 * p.head_groups + hg;
+            count[z] = s1 - s0 + 1;
+            whole[z] = s1 == s0;
+            lead[z] = sh.start(s0) >= start - kSharedUnitCost ? 0 : 1;
             row[z] = whole[z] ? (static_cast<long long>(z ? p.total_q : 0) + tok) * p.H + h
                               : p.part_row0 + (ti - tile * p.tile_tokens) * p.G + (h - hk * p.G);
         }
@@ -664,7 +749,8 @@ __global__ void __launch_bounds__(128) fa_decode_shared_merge_kernel(const Share
     auto row_of = [&](int k) {
         const int z = k < count[0] ? 0 : 1;
         const int c = z ? k - count[0] : k;
-        return whole[z] ? row[z] : row[z] + (2ll * (c0[z] + c) + (c == 0 ? lead[z] : 0)) * 128;
+        return whole[z] ? row[z]
+                        : row[z] + (2ll * (c0[z] + c * p.head_groups) + (c == 0 ? lead[z] : 0)) * 128;
     };
     const int parts = count[0] + count[1];
     float mx = -INFINITY, sum = 0.0f, acc[EPL];

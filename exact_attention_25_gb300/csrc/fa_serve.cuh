@@ -67,7 +67,8 @@ struct CacheParams {
 constexpr int kCacheBlock = 128;  // keys of a block of the cache decode
 
 // What a unit (below) costs besides its blocks (queries, merge of the warps, output), in blocks.
-constexpr int kUnitCost = 2;
+constexpr int kUnitCost = 2;        // cache decode
+constexpr int kSharedUnitCost = 3;  // shared prefixes (64 over one of 32000: 64 us; 2: 72, 1: 74)
 
 // Split-KV decode over the paged cache.  The work is a line of units: for every sequence, for
 // every `rows_cta` query rows of a group and every key/value head, kUnitCost places and one place
@@ -101,7 +102,9 @@ struct CacheDecodeParams {
 
 // Decode with shared prefixes: the same kind of line, over the groups' prefixes and then the
 // sequences' own keys, in units of one tile of query rows (tile_tokens tokens times the G heads of
-// a group, at most 128) and one key/value head.
+// a group, at most 128) and one key/value head.  Every one of head_groups sets of heads (head hk is
+// in set hk mod head_groups) has a line of its own, in `parts` shares: CTA c takes share
+// c / head_groups of set c mod head_groups.
 struct SharedDecodeParams {
     __nv_bfloat16* o;          // [total_q, H, d]
     float* lse;                // [H, total_q] (may be null)
@@ -120,7 +123,7 @@ struct SharedDecodeParams {
     int max_q, max_k, max_group_q, max_p;
     int total_q, total_k, total_p;
     int tile_tokens;
-    int ctas;
+    int ctas, head_groups, parts;
     float scale_log2;
     int causal;
     int* status;
@@ -144,6 +147,42 @@ struct Shares {
         return pos < cut ? pos / (per + 1) : more + (pos - cut) / per;
     }
 };
+
+// All lanes of a warp: the shares of a line of `items` items of places(x) places each (0 for x past
+// the last), and, for the first place of share c, its item and `at`, its distance from the item's
+// first place.  Neither is set when the share starts at the line's end.
+template <class F>
+__device__ __forceinline__ Shares find_share(int items, int ctas, int c, F places, int& item, int& at)
+{
+    const int lane = threadIdx.x & 31;
+    const int w0 = places(lane);  // (most batches have no more than 32 items)
+    int total = w0;
+#pragma unroll 1
+    for (int x0 = 32; x0 < items; x0 += 32) total += places(x0 + lane);
+    const Shares sh(__reduce_add_sync(0xffffffffu, total), ctas);
+    const int pos = sh.start(c);
+    if (pos >= sh.total) return sh;
+    int run = 0;
+#pragma unroll 1
+    for (int x0 = 0; x0 < items; x0 += 32) {
+        const int w = x0 == 0 ? w0 : places(x0 + lane);
+        int sum = w;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int up = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += up;
+        }
+        const uint32_t past = __ballot_sync(0xffffffffu, run + sum > pos);
+        if (past) {
+            const int src = __ffs(past) - 1;
+            at = pos - run - __shfl_sync(0xffffffffu, sum - w, src);
+            item = x0 + src;
+            break;
+        }
+        run += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    return sh;
+}
 
 // 2^(byte - 127), the scale an exponent byte stands for; 255 is NaN.
 __device__ __forceinline__ float exp_byte_scale(uint32_t byte)

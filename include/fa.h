@@ -463,7 +463,8 @@ int fa_decode_cache_ctas_for(int B, int H, int Hkv, int max_seqlen_q, int max_se
  * fa_decode_shared_num_ctas: one for each SM), and a second kernel merges each query's parts.
  * workspace: fa_decode_shared_workspace_bytes(total_q, H, d, num_ctas) bytes, overwritten.  A query
  * that sees no key gets O = 0, lse = -inf; rows that belong to no sequence are left as they are;
- * what lies in k and v behind the sequences may be anything.  bf16 only, forward only. */
+ * what lies in k and v behind the sequences may be anything.  B + num_groups is at most 16384.  bf16
+ * only, forward only. */
 int fa_fwd_decode_shared(const void* q, const void* k_prefix, const void* v_prefix, const void* k,
                          const void* v, void* o, float* lse, const int* cu_seqlens_q,
                          const int* cu_seqlens_k, const int* cu_groups, const int* cu_seqlens_p,
