@@ -1499,6 +1499,12 @@ extern "C" int fa_fwd_decode_cache(const void* q, const void* k_cache, const voi
         std::min(max_seqlen_k, INT_MAX - 1024), static_cast<long long>(max_pages) * page_size));
     if (cache_blocks(B, H, Hkv, max_seqlen_q, max_seqlen_k, fa::kUnitCost) >= (1LL << 31))
         return fail(FA_ERR_TOO_LARGE, "the batch must have fewer than 2^31 blocks of 128 keys");
+    {
+        // what the kernel divides by H / Hkv and by Hkv (FastDiv)
+        const long long G = H / Hkv, sets = (max_seqlen_q * G + 63) / 8;
+        if ((max_seqlen_q * G + 64) * G >= (1LL << 32) || sets * Hkv * Hkv >= (1LL << 32))
+            return fail(FA_ERR_TOO_LARGE, "max_seqlen_q*(H/Hkv)^2 and max_seqlen_q*H*Hkv / 8 must be < 2^32");
+    }
     const size_t need = fa_decode_cache_workspace_bytes(H, Hkv, d, max_seqlen_q, num_ctas);
     if (need > 0) {
         if (!workspace || workspace_bytes < need)
@@ -1519,7 +1525,7 @@ extern "C" int fa_fwd_decode_cache(const void* q, const void* k_cache, const voi
     p.ke = static_cast<const uint8_t*>(k_exp);
     p.ve = static_cast<const uint8_t*>(v_exp);
     p.cu_q = cu_seqlens_q; p.seqlens = seqlens_k; p.table = page_table;
-    p.B = B; p.H = H; p.Hkv = Hkv; p.G = H / Hkv;
+    p.B = B; p.H = H; p.Hkv = Hkv; p.G = fa::FastDiv(H / Hkv); p.heads = fa::FastDiv(Hkv);
     p.max_q = max_seqlen_q; p.max_k = max_seqlen_k; p.total_q = total_q;
     p.max_pages = max_pages; p.num_pages = num_pages; p.page_shift = shift;
     p.ctas = num_ctas;
@@ -1601,6 +1607,9 @@ extern "C" int fa_fwd_decode_shared(const void* q, const void* k_prefix, const v
     const long long places =
         static_cast<long long>(num_groups) * Hkv * ((max_group_q + tok - 1) / tok) * ((max_seqlen_p + 127) / 128 + fa::kSharedUnitCost) +
         static_cast<long long>(B) * Hkv * ((max_seqlen_q + tok - 1) / tok) * ((max_seqlen_k + 127) / 128 + fa::kSharedUnitCost);
+    // (tokens are divided by the tile's: FastDiv)
+    if ((std::max(max_group_q, max_seqlen_q) + 128LL) * tok >= (1LL << 32))
+        return fail(FA_ERR_TOO_LARGE, "max_seqlen_q and max_group_q must be < 2^25");
     if (places >= (1LL << 31) || static_cast<long long>(B) * H * max_seqlen_q >= (1LL << 31) ||
         static_cast<long long>(B) + num_groups > 16384)
         return fail(FA_ERR_TOO_LARGE, "the batch must have fewer than 2^31 blocks of 128 keys, B*H*max_seqlen_q < 2^31 "
@@ -1621,10 +1630,10 @@ extern "C" int fa_fwd_decode_shared(const void* q, const void* k_prefix, const v
     p.part_row0 = 2LL * total_q * H;
     p.v = static_cast<const __nv_bfloat16*>(v);
     p.cu_q = cu_seqlens_q; p.cu_k = cu_seqlens_k; p.cu_g = cu_groups; p.cu_p = cu_seqlens_p;
-    p.B = B; p.groups = num_groups; p.H = H; p.Hkv = Hkv; p.G = G;
+    p.B = B; p.groups = num_groups; p.H = H; p.Hkv = Hkv; p.G = fa::FastDiv(G);
     p.max_q = max_seqlen_q; p.max_k = max_seqlen_k; p.max_group_q = max_group_q; p.max_p = max_seqlen_p;
     p.total_q = total_q; p.total_k = total_k; p.total_p = total_p;
-    p.tile_tokens = tok;
+    p.tile_tokens = fa::FastDiv(tok);
     p.ctas = num_ctas;
     p.head_groups = std::min(Hkv, num_ctas);
     p.parts = num_ctas / p.head_groups;

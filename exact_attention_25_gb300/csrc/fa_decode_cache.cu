@@ -155,7 +155,7 @@ __device__ __forceinline__ void sequence_work(const CacheDecodeParams& p, int b,
     u.nq = packed_rows(p.cu_q, b, p.total_q, p.max_q, u.q0);
     u.nk = min(max(p.seqlens[b], 0), p.max_k);
     u.nblk = max(1, (u.nk + kKB - 1) / kKB);
-    u.in_seq = ((u.nq * p.G + p.rows_cta - 1) >> p.rows_shift) * p.Hkv;
+    u.in_seq = ((u.nq * p.G.d + p.rows_cta - 1) >> p.rows_shift) * p.Hkv;
 }
 
 // All lanes of a warp: the line's shares and, for the first place of share c, its sequence (u) and
@@ -179,7 +179,7 @@ __device__ __forceinline__ Shares find_share(const CacheDecodeParams& p, int c, 
 // Row set and head of the sequence's unit i.
 __device__ __forceinline__ void unit_at(const CacheDecodeParams& p, int i, Unit& u)
 {
-    const int set = static_cast<unsigned>(i) / static_cast<unsigned>(p.Hkv);
+    const int set = p.heads(i);
     u.row0 = set << p.rows_shift;
     u.hk = i - set * p.Hkv;
 }
@@ -265,17 +265,19 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
                     mbar_arrive(&bar_unit[k % kUnits]);
                 }
                 // the unit's queries, ahead of the compute warps
-                const int rows = min(un.nq * p.G - un.row0, p.rows_cta);
+                const int rows = min(un.nq * p.G.d - un.row0, p.rows_cta);
+#pragma unroll 1
                 for (int r = lane; r < rows; r += 32) {
-                    const int i = (un.row0 + r) / p.G, h = (un.row0 + r) - i * p.G;
+                    const int i = p.G(un.row0 + r), h = (un.row0 + r) - i * p.G.d;
                     const __nv_bfloat16* q =
-                        p.q + (static_cast<long long>(un.q0 + i) * p.H + un.hk * p.G + h) * D;
+                        p.q + (static_cast<long long>(un.q0 + i) * p.H + un.hk * p.G.d + h) * D;
                     for (int c = 0; c < D; c += 64)
                         asm volatile("prefetch.global.L1 [%0];" ::"l"(q + c));
                 }
                 ++k;
             }
             int base = -1, ids = -1;                          // page ids base + lane
+#pragma unroll 1
             for (int jj = 0; jj < un.J; ++jj, ++it) {
                 const int s = it % C::STAGES;
                 const int pos = (un.jb + jj) * kKB;
@@ -295,6 +297,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
                 if (!ok) break;
                 if (lane == 0) {
                     int bits = 0;
+#pragma unroll 1
                     for (int i = 0; i < np; ++i)
                         if (got >> i & 1) bits |= ((1 << groups_pp) - 1) << (i * groups_pp);
                     s_valid[s] = bits;
@@ -349,25 +352,26 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
     const uint32_t sel_lo = swap ? 0x1504u : 0x5140u, sel_hi = swap ? 0x3726u : 0x7362u;
     int it = 0;       // blocks through the ring so far
     int rounds = 0;   // merges so far
+#pragma unroll 1
     for (int k = 0;; ++k) {
         if (!warp_wait_all(&bar_unit[k % kUnits], (k / kUnits) & 1, wd, kSiteCacheFull)) return;
         const Unit& un = s_unit[k % kUnits];
         if (un.J == 0) return;
-        const int rows = min(un.nq * p.G - un.row0, p.rows_cta);
+        const int rows = min(un.nq * p.G.d - un.row0, p.rows_cta);
         // element offset of query row r's o row, and its lse
         auto out_off = [&](int r) {
-            const int i = (un.row0 + r) / p.G, h = (un.row0 + r) - i * p.G;
-            return (static_cast<long long>(un.q0 + i) * p.H + un.hk * p.G + h) * D;
+            const int i = p.G(un.row0 + r), h = (un.row0 + r) - i * p.G.d;
+            return (static_cast<long long>(un.q0 + i) * p.H + un.hk * p.G.d + h) * D;
         };
         auto stat_off = [&](int r) {
-            const int i = (un.row0 + r) / p.G, h = (un.row0 + r) - i * p.G;
-            return static_cast<long long>(un.hk * p.G + h) * p.total_q + un.q0 + i;
+            const int i = p.G(un.row0 + r), h = (un.row0 + r) - i * p.G.d;
+            return static_cast<long long>(un.hk * p.G.d + h) * p.total_q + un.q0 + i;
         };
         // last key that query row r of the tile sees (-1: none, or no such row)
         auto limit = [&](int r) {
             r += tile * TR;
             if (r >= rows) return -1;
-            return p.causal ? min(un.nk - 1, (un.row0 + r) / p.G + un.nk - un.nq) : un.nk - 1;
+            return p.causal ? min(un.nk - 1, p.G(un.row0 + r) + un.nk - un.nq) : un.nk - 1;
         };
         uint32_t qb[NR][KS][2];    // query row 8 n + g, the thread's elements
         float cx[NR][2];           // rows 8 n + 2 t + e: logit (base 2) per unit of the product
@@ -375,8 +379,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
 #pragma unroll
         for (int n = 0; n < NR; ++n) {
             const int r = tile * TR + 8 * n + g;
-            float f[CH][16];
-            float mx = 0.0f;
+            uint32_t u[CH][8], amax = 0;
 #pragma unroll
             for (int c = 0; c < CH; ++c) {
                 uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
@@ -387,32 +390,28 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
                         w[1] = reinterpret_cast<const uint4*>(p.q + off)[1];
                     }
                 }
-                const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    f[c][2 * i] = __uint_as_float(u[i] << 16);
-                    f[c][2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+                for (int i = 0; i < 2; ++i) {
+                    u[c][4 * i] = w[i].x; u[c][4 * i + 1] = w[i].y;
+                    u[c][4 * i + 2] = w[i].z; u[c][4 * i + 3] = w[i].w;
                 }
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float a = fabsf(f[c][i]);
-                    if (a < INFINITY) mx = fmaxf(mx, a);
-                }
+                for (int i = 0; i < 8; ++i) amax = __vmaxu2(amax, u[c][i] & 0x7fff7fffu);
             }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            // 2^a brings the row's largest magnitude to [2^14, 2^15)
-            const int a = min(14 + 127 - static_cast<int>(__float_as_uint(mx) >> 23), 126);
+            amax = max(amax & 0xffffu, amax >> 16);
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            // 2^a brings the row's largest magnitude to [2^14, 2^15).  (In a row with an infinity or
+            // a NaN the rest vanishes beside it, as it does in its logits.)
+            const int a = min(14 + 127 - static_cast<int>(amax >> 7), 126);
             const float up = __uint_as_float(static_cast<uint32_t>(127 + a) << 23);
             const float down = p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - a) << 23);
 #pragma unroll
             for (int c = 0; c < CH; ++c)
 #pragma unroll
-                for (int s = 0; s < 4; ++s)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        qb[n][4 * c + s][i] =
-                            pack_f16x2(f[c][4 * s + 2 * i] * up, f[c][4 * s + 2 * i + 1] * up);
+                for (int i = 0; i < 8; ++i)
+                    qb[n][4 * c + i / 2][i & 1] = pack_f16x2(__uint_as_float(u[c][i] << 16) * up,
+                                                             __uint_as_float(u[c][i] & 0xFFFF0000u) * up);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 cx[n][e] = __shfl_sync(0xffffffffu, down, 4 * (2 * t + e));
@@ -640,6 +639,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
         };
 
         const int j1 = un.jb + un.J;
+#pragma unroll 1
         for (int j = un.jb; j < j1; ++j, ++it) {
             const int s = it % C::STAGES;
             if (!warp_wait_all(&bar_full[s], (it / C::STAGES) & 1, wd, kSiteCacheFull)) return;
@@ -649,11 +649,13 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
             // steps in the clear go U at a time
             constexpr int U = NR == 1 ? 2 : 1;
             if (most >= 0)  // (else there is no query row in this warp's tile)
+#pragma unroll 1
                 for (int gi = slot; gi < kKB / 16; gi += U * slots) {
                     const int last = gi + (U - 1) * slots;
                     if ((valid >> gi & 1) && (valid >> last & 1) && j * kKB + last * 16 + 15 <= least) {
                         step(std::false_type{}, std::integral_constant<int, U>{}, kt, ex, j, gi, slots);
                     } else {
+#pragma unroll 1
                         for (int i = gi; i <= last; i += slots)
                             if ((valid >> i & 1) && j * kKB + i * 16 <= most)
                                 step(std::true_type{}, std::integral_constant<int, 1>{}, kt, ex, j, i, slots);
@@ -727,15 +729,15 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
                 if (lane == 0) mbar_arrive(&bar_taken[i]);
                 return true;
             };
-            if (slots > 1) {
-                if (2 * slot >= slots) {
-                    if (!give(warp & 1)) return;
-                } else {
-                    if (!take(warp & 1)) return;
-                    if (slots == 4 && (slot == 1 ? !give(2) : !take(2))) return;
-                }
-                ++rounds;
+#pragma unroll 1
+            for (int half = slots / 2; half > 0; half /= 2) {
+                // slots half .. 2 half - 1 give to those below; buffers 0, 1 in the first round, 2
+                // in the second of four slots
+                const int x = half == 1 && slots == 4 ? 2 : warp & 1;
+                if (slot >= 2 * half) continue;
+                if (slot >= half ? !give(x) : !take(x)) return;
             }
+            ++rounds;
             if (slot != 0) continue;
             // ---- O = o 2^(M - frame) / (l 2^m); a row that saw no key has l = 0.  The power is
             // applied in halves: each is representable where the whole may not be.
@@ -810,7 +812,7 @@ __global__ void __launch_bounds__(kMergeThreads) fa_decode_cache_merge_kernel(co
     }
     unit_at(p, ui, u);
     const int c1 = sh.share_of(start + u.nblk - 1);  // the last share in it
-    const int rows = min(u.nq * p.G - u.row0, p.rows_cta);
+    const int rows = min(u.nq * p.G.d - u.row0, p.rows_cta);
     const int parts = c1 - c0 + 1;
     // share c0's part is its last unit, which is also its first if the share starts in its places
     const int lead = sh.start(c0) >= start - kUnitCost ? 0 : 1;
@@ -870,7 +872,7 @@ __global__ void __launch_bounds__(kMergeThreads) fa_decode_cache_merge_kernel(co
                 }
             }
         }
-        const int i = (u.row0 + r) / p.G, h = u.hk * p.G + (u.row0 + r) - i * p.G;
+        const int i = p.G(u.row0 + r), h = u.hk * p.G.d + (u.row0 + r) - i * p.G.d;
         const long long row = (static_cast<long long>(u.q0 + i) * p.H + h) * D + EPL * lane;
         const long long stat = static_cast<long long>(h) * p.total_q + u.q0 + i;
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;

@@ -73,7 +73,7 @@ __device__ __forceinline__ void shared_item(const SharedDecodeParams& p, int x, 
         u.nk = packed_rows(p.cu_k, x - p.groups, p.total_k, p.max_k, u.k0);
     }
     u.nblk = (u.nk + kSB - 1) / kSB;
-    u.in_item = u.nk > 0 ? (u.ntok + p.tile_tokens - 1) / p.tile_tokens : 0;
+    u.in_item = u.nk > 0 ? p.tile_tokens(u.ntok + p.tile_tokens.d - 1) : 0;
 }
 
 __device__ __forceinline__ int shared_places(const SharedDecodeParams& p, int x)
@@ -89,6 +89,7 @@ __device__ __forceinline__ int count_places(const SharedDecodeParams& p, const i
 {
     const int items = p.groups + p.B;
     int sum = 0, b0 = 0, b1 = 0;
+#pragma unroll 1
     for (int i = threadIdx.x & 31; i < items; i += 32) {
         const int w = shared_places(p, i);
         sum += w;
@@ -122,6 +123,7 @@ __device__ __noinline__ bool clear_unseen_v(uint8_t* tile, int first, int end, i
     const int at = lane * LB;
     uint8_t* base = tile + (at >> 7) * C::PANEL_BYTES + (at & 127);
     bool odd = false;
+#pragma unroll 1
     for (int row = first + warp; row < last; row += 4) {
         uint32_t* w = reinterpret_cast<uint32_t*>(base + row * 128);
 #pragma unroll
@@ -142,6 +144,7 @@ __device__ __noinline__ bool clear_unseen_v(uint8_t* tile, int first, int end, i
 template <int D>
 __device__ __noinline__ void add_odd_v(const SharedDecodeParams& p, float* dst, const SharedUnit& un, int key0, int key1)
 {
+#pragma unroll 1
     for (int key = key0; key < key1; ++key) {
         const long long off = (static_cast<long long>(un.k0 + key) * p.Hkv + un.hk) * D;
         if (!in_extent(off, D, p.v_ext, p.status)) continue;
@@ -258,6 +261,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
     // the items' places, by all warps, in the V ring (free until the first copy)
     int* s_places = reinterpret_cast<int*>(sV);
     const int items = p.groups + p.B;
+#pragma unroll 1
     for (int x = threadIdx.x; x < items; x += C::THREADS) s_places[x] = shared_places(p, x);
     fence_proxy_async_smem();
     __syncthreads();
@@ -306,6 +310,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
             un.first = k == 0;
             un.odd = 0;
             const CUtensorMap* k_map = un.item < p.groups ? &tm_kp : &tm_k;
+#pragma unroll 1
             for (int jj = 0; ok && jj < un.J; ++jj, ++n) {
                 const int row = un.k0 + (un.jb + jj) * kSB;
                 if (jj == 0) {
@@ -319,10 +324,10 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
                     ok = warp_wait_all(&bar_qempty, (k & 1) ^ 1, wd, kSiteSharedEmpty);
                     if (!ok) break;
                     mbar_arrive_expect_tx_w(&bar_qfull,
-                                            static_cast<uint32_t>(C::PANELS * 128 * p.G * p.tile_tokens));
+                                            static_cast<uint32_t>(C::PANELS * 128 * p.G.d * p.tile_tokens.d));
                     for (int pn = 0; pn < C::PANELS; ++pn)
-                        tma_load_3d_w(sQ + pn * C::PANEL_BYTES, &tm_q, &bar_qfull, 64 * pn, un.hk * p.G,
-                                      un.tok0 + un.tile * p.tile_tokens);
+                        tma_load_3d_w(sQ + pn * C::PANEL_BYTES, &tm_q, &bar_qfull, 64 * pn, un.hk * p.G.d,
+                                      un.tok0 + un.tile * p.tile_tokens.d);
                     ++k;
                 }
                 const int s = n % C::KST;
@@ -404,6 +409,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
         ok = more >= 0;
         // unit and block of the next P V, the unit's blocks here and keys from its first block here on
         int vu = 0, vj = 0, vJ = kJ, v_left = k_left;
+#pragma unroll 1
         for (int n = 0; ok && more > 0; ++n) {
             more = issue_s(n + 1);
             if (more < 0 || !warp_wait_all(&bar_pfull, n & 1, wd, kSiteSharedP)) { ok = false; break; }
@@ -440,7 +446,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
         // ------------------------------------------------------------- softmax (warps 0-3)
         const int r = threadIdx.x;  // tile row = TMEM lane
         const uint32_t lane_base = static_cast<uint32_t>(warp * 32) << 16;
-        const int i = r / p.G, g = r - i * p.G;  // token of the tile, head of the group
+        const int i = p.G(r), g = r - i * p.G.d;  // token of the tile, head of the group
         // x = S * c with c = scale * log2(e); for c <= 0 the scores are scaled first so that
         // masked entries stay -inf (as in the forward kernel).
         const float c2 = p.scale_log2;
@@ -455,18 +461,18 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
             const int J = un.J, jb = un.jb, nk = un.nk;
             if (J == 0) break;
             const uint32_t tO = tbase + lane_base + 256u + 128u * (k & 1);
-            const int ti = un.tile * p.tile_tokens + i;   // token of the item
+            const int ti = un.tile * p.tile_tokens.d + i;   // token of the item
             // Key blocks from jmask on need the element-wise mask (the causal edge, the ragged last
             // block); this row sees the keys [0, klim].  A prefix is seen whole by every query.
             int jmask = nk / kSB, klim = nk - 1;
             int seen = nk;  // keys that every row of the tile sees
             if (p.causal && un.item >= p.groups) {
                 const int shift = nk - un.ntok;  // bottom-right alignment
-                seen = min(seen, max(0, shift + un.tile * p.tile_tokens + 1));
+                seen = min(seen, max(0, shift + un.tile * p.tile_tokens.d + 1));
                 jmask = min(jmask, seen / kSB);
                 klim = min(klim, ti + shift);
             }
-            const int tok_tile = min(p.tile_tokens, un.ntok - un.tile * p.tile_tokens);
+            const int tok_tile = min(p.tile_tokens.d, un.ntok - un.tile * p.tile_tokens.d);
             const bool valid = i < tok_tile;
             const bool any_valid = __any_sync(0xffffffffu, valid);
             float m = -INFINITY, l = 0.0f, lr = 0.0f;
@@ -640,7 +646,9 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
                 ++n;
             };
             const int j1 = jb + J, j0 = min(j1, max(jb, jmask));
+#pragma unroll 1
             for (int j = jb; ok && j < j0; ++j) block(std::false_type{}, j);
+#pragma unroll 1
             for (int j = j0; ok && j < j1; ++j) block(std::true_type{}, j);
             // ------------------------------------------------------------- the unit's result
             // O normalised by its own weights and its natural-log LSE, in fp32 for the merge: to
@@ -649,7 +657,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
             if (!ok) break;
             tc_fence_after();
             const bool whole = J == un.nblk;
-            const int h = un.hk * p.G + g;
+            const int h = un.hk * p.G.d + g;
             const float inv_l = lr > 0.0f ? 1.0f / lr : (lr == 0.0f ? 0.0f : NAN);
             const float lse_row = l > 0.0f ? (m + __log2f(l)) * kLn2 : (l == 0.0f ? -INFINITY : NAN);
             long long row;
@@ -714,6 +722,7 @@ __global__ void __launch_bounds__(128) fa_decode_shared_merge_kernel(const Share
     if (here) {
         int x = 0;  // the group: groups are runs of sequences
         u[0].in_item = 0;
+#pragma unroll 1
         for (int g0 = 0; g0 < p.groups; g0 += 32) {
             const bool in = g0 + lane < p.groups && p.cu_g[g0 + lane] <= b && b < p.cu_g[g0 + lane + 1];
             const uint32_t some = __ballot_sync(0xffffffffu, in);
@@ -726,14 +735,14 @@ __global__ void __launch_bounds__(128) fa_decode_shared_merge_kernel(const Share
         const int items[2] = {x, p.groups + b};
         int before[2];
         const int all = count_places(p, items, before);
-        const int hk = h / p.G, hg = hk % p.head_groups, hj = hk / p.head_groups;
+        const int hk = p.G(h), hg = hk % p.head_groups, hj = hk / p.head_groups;
         const int nh = (p.Hkv - hg + p.head_groups - 1) / p.head_groups;
         const Shares sh(all * nh, p.parts);
 #pragma unroll
         for (int z = 0; z < 2; ++z) {
             const int ti = tok - u[z].tok0;
             if (u[z].in_item == 0 || ti < 0 || ti >= u[z].ntok) continue;
-            const int tile = ti / p.tile_tokens;
+            const int tile = p.tile_tokens(ti);
             const int start = before[z] * nh + (tile * nh + hj) * (u[z].nblk + kSharedUnitCost) + kSharedUnitCost;
             const int s0 = sh.share_of(start), s1 = sh.share_of(start + u[z].nblk - 1);
             c0[z] = s0 * p.head_groups + hg;
@@ -741,7 +750,7 @@ __global__ void __launch_bounds__(128) fa_decode_shared_merge_kernel(const Share
             whole[z] = s1 == s0;
             lead[z] = sh.start(s0) >= start - kSharedUnitCost ? 0 : 1;
             row[z] = whole[z] ? (static_cast<long long>(z ? p.total_q : 0) + tok) * p.H + h
-                              : p.part_row0 + (ti - tile * p.tile_tokens) * p.G + (h - hk * p.G);
+                              : p.part_row0 + (ti - tile * p.tile_tokens.d) * p.G.d + (h - hk * p.G.d);
         }
     }
     dependent_begin();

@@ -66,6 +66,20 @@ struct CacheParams {
 
 constexpr int kCacheBlock = 128;  // keys of a block of the cache decode
 
+// Division by a number known on the host: x / d = (x * m) >> 32 with m = floor(2^32 / d) + 1, exact for
+// x * d < 2^32 (m d exceeds 2^32 by at most d).  A division in line is some 25 instructions, and these
+// kernels' first microseconds go by what they have to fetch.
+struct FastDiv {
+    unsigned long long m;
+    int d;
+    FastDiv() = default;
+    explicit FastDiv(int v) : m((1ull << 32) / static_cast<unsigned>(v) + 1), d(v) {}
+    __device__ __forceinline__ int operator()(int x) const
+    {
+        return static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(x)) * m) >> 32);
+    }
+};
+
 // What a unit (below) costs besides its blocks (queries, merge of the warps, output), in blocks.
 constexpr int kUnitCost = 2;        // cache decode
 constexpr int kSharedUnitCost = 3;  // shared prefixes (64 over one of 32000: 64 us; 2: 72, 1: 74)
@@ -86,7 +100,9 @@ struct CacheDecodeParams {
     const int* cu_q;           // [B + 1]
     const int* seqlens;        // [B] keys of each sequence
     const int* table;          // [B, max_pages]
-    int B, H, Hkv, G;          // G = H / Hkv
+    int B, H, Hkv;
+    FastDiv G;                 // H / Hkv
+    FastDiv heads;             // Hkv
     int max_q, max_k, total_q;
     int max_pages, num_pages, page_shift;
     int ctas;
@@ -119,10 +135,11 @@ struct SharedDecodeParams {
     const int* cu_k;           // [B + 1]
     const int* cu_g;           // [groups + 1] first sequence of each group
     const int* cu_p;           // [groups + 1] first row of each group's prefix
-    int B, groups, H, Hkv, G;
+    int B, groups, H, Hkv;
+    FastDiv G;                 // H / Hkv
     int max_q, max_k, max_group_q, max_p;
     int total_q, total_k, total_p;
-    int tile_tokens;
+    FastDiv tile_tokens;
     int ctas, head_groups, parts;
     float scale_log2;
     int causal;
