@@ -106,7 +106,7 @@ def build_binding(force: bool = False) -> str:
            "-isystem", os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
            "-isystem", os.path.join(cuda, "include"), src, "-o", tmp,
            "-L", os.path.join(tdir, "lib"), "-Wl,-rpath," + os.path.join(tdir, "lib"),
-           "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+           "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed for {src}:\n{res.stdout}\n{res.stderr}")

@@ -7,7 +7,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -108,6 +108,13 @@ struct Device {
         if (t.device() != d) value_error("tensors must lie on one device");
     }
 };
+
+// A new contiguous tensor from torch's allocator, on the current stream (no dispatch: this is most of
+// a small call's time).
+at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, const Device& dev)
+{
+    return at::detail::empty_cuda(sizes, type, dev.d, std::nullopt);
+}
 
 int dtype_of(const at::Tensor& t)
 {
@@ -254,11 +261,11 @@ PyObject* rope(Args a)
     const c10::cuda::CUDAGuard guard(dev.cuda());
     at::Tensor q_new, k_new;
     if (!qo) {
-        q_new = at::empty(q.sizes(), q.options());
+        q_new = empty(q.sizes(), q.scalar_type(), dev);
         qo = &q_new;
     }
     if (!ko && k) {
-        k_new = at::empty(k->sizes(), k->options());
+        k_new = empty(k->sizes(), k->scalar_type(), dev);
         ko = &k_new;
     }
     if ((k == nullptr) != (ko == nullptr)) value_error("k and k_out come together");
@@ -331,9 +338,9 @@ PyObject* cache_read(Args a)
     if (!k || !v) {
         if (k || v) value_error("k and v come together");
         if (total < 0) value_error("total_k must not be negative");
-        const auto options = at::TensorOptions().dtype(fp32 ? at::kFloat : at::kBFloat16).device(dev.d);
-        k_new = at::empty({total, c.Hkv, c.d}, options);
-        v_new = at::empty({total, c.Hkv, c.d}, options);
+        const auto type = fp32 ? at::kFloat : at::kBFloat16;
+        k_new = empty({total, c.Hkv, c.d}, type, dev);
+        v_new = empty({total, c.Hkv, c.d}, type, dev);
         k = &k_new;
         v = &v_new;
     }
@@ -365,12 +372,12 @@ struct DecodeOut {
     void make(const at::Tensor& q, const Device& dev, size_t bytes)
     {
         if (!o) {
-            o_new = at::empty(q.sizes(), q.options());
-            lse_new = at::empty({q.size(1), q.size(0)}, q.options().dtype(at::kFloat));
+            o_new = empty(q.sizes(), q.scalar_type(), dev);
+            lse_new = empty({q.size(1), q.size(0)}, at::kFloat, dev);
             o = &o_new;
             lse = &lse_new;
             if (bytes) {
-                ws_new = at::empty({static_cast<int64_t>(bytes)}, q.options().dtype(at::kByte));
+                ws_new = empty({static_cast<int64_t>(bytes)}, at::kByte, dev);
                 ws = &ws_new;
             }
         }
