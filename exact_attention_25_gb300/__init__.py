@@ -497,12 +497,17 @@ class RopeTable:
                       self.d, self.pairs, self.interleaved)
 
 
-@functools.lru_cache(maxsize=64)
 def rope_table(d: int, sections, base: float = 10000.0, per_axis: bool = False,
                interleaved: bool = False) -> RopeTable:
     """The table of a head of d elements whose first sum(sections) pairs turn, sections[a] of
     them by axis a.  Frequencies run base^(-i / pairs) over all rotated pairs, or, per_axis,
     base^(-i / sections[a]) afresh for each axis."""
+    return _rope_table(int(d), tuple(int(n) for n in sections), float(base), bool(per_axis),
+                       bool(interleaved))
+
+
+@functools.lru_cache(maxsize=64)
+def _rope_table(d, sections, base, per_axis, interleaved):
     pairs = sum(sections)
     freq, axis = [], []
     for a, n in enumerate(sections):

@@ -1330,6 +1330,17 @@ int cache_rows_params(const void* k, const void* v, const long long* strides, vo
     if (!aligned16(k) || !aligned16(v) || !aligned4(cu))
         return fail(FA_ERR_MISALIGNED, "k and v must be 16-byte aligned (cu_seqlens 4-byte)");
     if (max_rows > total) max_rows = total;
+    {
+        const size_t codes = static_cast<size_t>(num_pages) * Hkv * page_size;
+        const size_t rows = strides ? 0 : static_cast<size_t>(total) * Hkv * d * (dtype == FA_F32 ? 4 : 2);
+        const Span cache[4] = {{kc, codes * d}, {vc, codes * d}, {ke, codes}, {ve, codes}};
+        // (strided views may interleave: not checked)
+        const Span out[2] = {{strides ? nullptr : k, rows}, {strides ? nullptr : v, rows}};
+        // append writes the cache, read writes k and v: either way they lie apart
+        if (outputs_overlap(cache, 4, out, 2) || (!seqlens && outputs_overlap(out, 2, cache, 0)))
+            return fail(FA_ERR_INVALID_ARG, "the cache's tensors must not overlap one another, k or v (nor k and v "
+                                            "one another where they are written)");
+    }
     const int heads[2] = {Hkv, Hkv};
     long long rs[2], hs[2];
     if (int rc = packed_or_user_strides(strides, 2, heads, d, dtype == FA_F32 ? 4 : 8, rs, hs)) return rc;
@@ -1494,10 +1505,10 @@ extern "C" int fa_fwd_decode_cache(const void* q, const void* k_cache, const voi
     if (static_cast<long long>(total_q) * H * d >= (1LL << 31))
         return fail(FA_ERR_TOO_LARGE, "total_q*H*d must be < 2^31");
     if (max_seqlen_q > total_q) max_seqlen_q = total_q;
-    // no sequence is longer than its row of the table (and block ends stay below 2^31)
-    max_seqlen_k = static_cast<int>(std::min<long long>(
+    // no more keys are read than a row of the table has room for (and block ends stay below 2^31)
+    const int table_k = static_cast<int>(std::min<long long>(
         std::min(max_seqlen_k, INT_MAX - 1024), static_cast<long long>(max_pages) * page_size));
-    if (cache_blocks(B, H, Hkv, max_seqlen_q, max_seqlen_k, fa::kUnitCost) >= (1LL << 31))
+    if (cache_blocks(B, H, Hkv, max_seqlen_q, table_k, fa::kUnitCost) >= (1LL << 31))
         return fail(FA_ERR_TOO_LARGE, "the batch must have fewer than 2^31 blocks of 128 keys");
     {
         // what the kernel divides by H / Hkv and by Hkv (FastDiv)
@@ -1510,6 +1521,17 @@ extern "C" int fa_fwd_decode_cache(const void* q, const void* k_cache, const voi
         if (!workspace || workspace_bytes < need)
             return fail(FA_ERR_WORKSPACE, "workspace must hold " + std::to_string(need) + " bytes");
         if (!aligned16(workspace)) return fail(FA_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    }
+    {
+        const size_t codes = static_cast<size_t>(num_pages) * Hkv * page_size;
+        const Span out[3] = {{o, static_cast<size_t>(total_q) * H * d * 2},
+                             {lse, lse ? static_cast<size_t>(total_q) * H * 4 : 0},
+                             {need ? workspace : nullptr, need}};
+        const Span in[8] = {{q, out[0].n}, {k_cache, codes * d}, {v_cache, codes * d}, {k_exp, codes}, {v_exp, codes},
+                            {cu_seqlens_q, (B + 1ull) * 4}, {seqlens_k, B * 4ull},
+                            {page_table, static_cast<size_t>(B) * max_pages * 4}};
+        if (outputs_overlap(out, 3, in, 8))
+            return fail(FA_ERR_INVALID_ARG, "o, lse and the workspace must not overlap one another or an input");
     }
     DeviceInfo* di = nullptr;
     if (int rc = device_info(&di)) return rc;
@@ -1526,7 +1548,7 @@ extern "C" int fa_fwd_decode_cache(const void* q, const void* k_cache, const voi
     p.ve = static_cast<const uint8_t*>(v_exp);
     p.cu_q = cu_seqlens_q; p.seqlens = seqlens_k; p.table = page_table;
     p.B = B; p.H = H; p.Hkv = Hkv; p.G = fa::FastDiv(H / Hkv); p.heads = fa::FastDiv(Hkv);
-    p.max_q = max_seqlen_q; p.max_k = max_seqlen_k; p.total_q = total_q;
+    p.max_q = max_seqlen_q; p.max_k = max_seqlen_k; p.total_q = total_q; p.table_k = table_k;
     p.max_pages = max_pages; p.num_pages = num_pages; p.page_shift = shift;
     p.ctas = num_ctas;
     p.rows_cta = cache_rows_cta(static_cast<long long>(max_seqlen_q) * (H / Hkv));
@@ -1556,6 +1578,23 @@ extern "C" int fa_fwd_decode_cache(const void* q, const void* k_cache, const voi
 namespace {
 
 constexpr int kSharedMaxCtas = 1024;
+
+// Sets of heads: a line for every head where the CTAs go round, else the fewest heads to a line that
+// leave over a tenth fewer CTAs idle.  (96 heads on 152 CTAs: one head to a line keeps 96 of them at
+// work; two keep 144.)
+int shared_head_groups(int Hkv, int ctas)
+{
+    int best = std::min(Hkv, ctas);
+    for (int nh = 2; nh <= std::min(Hkv, 8); ++nh) {
+        const int g = (Hkv + nh - 1) / nh;
+        if (g > ctas) continue;
+        // a line's CTAs take (heads of the line) / (CTAs of the line) of a head's time
+        const long long t = (Hkv + g - 1) / g, n = ctas / g;
+        const long long bt = (Hkv + best - 1) / best, bn = ctas / best;
+        if (10 * t * bn < 9 * bt * n) best = g;
+    }
+    return best;
+}
 
 size_t shared_rows(int total_q, int H, int ctas) { return static_cast<size_t>(2) * total_q * H + 256 * static_cast<size_t>(ctas); }
 
@@ -1618,6 +1657,16 @@ extern "C" int fa_fwd_decode_shared(const void* q, const void* k_prefix, const v
     if (!workspace || workspace_bytes < need)
         return fail(FA_ERR_WORKSPACE, "workspace must hold " + std::to_string(need) + " bytes");
     if (!aligned16(workspace)) return fail(FA_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+    {
+        const size_t row = static_cast<size_t>(Hkv) * d * 2;
+        const Span out[3] = {{o, static_cast<size_t>(total_q) * H * d * 2},
+                             {lse, lse ? static_cast<size_t>(total_q) * H * 4 : 0}, {workspace, need}};
+        const Span in[9] = {{q, out[0].n}, {k_prefix, total_p * row}, {v_prefix, total_p * row}, {k, total_k * row},
+                            {v, total_k * row}, {cu_seqlens_q, (B + 1ull) * 4}, {cu_seqlens_k, (B + 1ull) * 4},
+                            {cu_groups, (num_groups + 1ull) * 4}, {cu_seqlens_p, (num_groups + 1ull) * 4}};
+        if (outputs_overlap(out, 3, in, 9))
+            return fail(FA_ERR_INVALID_ARG, "o, lse and the workspace must not overlap one another or an input");
+    }
     DeviceInfo* di = nullptr;
     if (int rc = device_info(&di)) return rc;
     fa::SharedDecodeParams p{};
@@ -1635,7 +1684,7 @@ extern "C" int fa_fwd_decode_shared(const void* q, const void* k_prefix, const v
     p.total_q = total_q; p.total_k = total_k; p.total_p = total_p;
     p.tile_tokens = fa::FastDiv(tok);
     p.ctas = num_ctas;
-    p.head_groups = std::min(Hkv, num_ctas);
+    p.head_groups = shared_head_groups(Hkv, num_ctas);
     p.parts = num_ctas / p.head_groups;
     p.scale_log2 = scale * fa::kLog2e; p.causal = causal;
     p.status = di->status; p.wait_limit_ns = g_wait_limit_ns; p.debug_flags = g_debug_flags;

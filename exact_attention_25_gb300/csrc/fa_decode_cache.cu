@@ -141,7 +141,8 @@ __device__ __forceinline__ int kperm(int n)
 // One unit's part of a share.
 struct Unit {
     int b, hk, row0;       // sequence, key/value head, first query row
-    int q0, nq, nk, nblk;  // the sequence: first token, tokens, keys, blocks
+    int q0, nq, nk, nblk;  // the sequence: first token, tokens, keys in the table, blocks
+    int shift;             // causal: token i sees the keys up to i + shift
     int in_seq;            // units of the sequence
     int jb, J;             // this share's blocks of the unit: [jb, jb + J)
     int flags;             // kFirst: the share's first unit
@@ -153,7 +154,9 @@ __device__ __forceinline__ void sequence_work(const CacheDecodeParams& p, int b,
 {
     u.b = b;
     u.nq = packed_rows(p.cu_q, b, p.total_q, p.max_q, u.q0);
-    u.nk = min(max(p.seqlens[b], 0), p.max_k);
+    const int len = min(max(p.seqlens[b], 0), p.max_k);
+    u.nk = min(len, p.table_k);
+    u.shift = len - u.nq;
     u.nblk = max(1, (u.nk + kKB - 1) / kKB);
     u.in_seq = ((u.nq * p.G.d + p.rows_cta - 1) >> p.rows_shift) * p.Hkv;
 }
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
                 if (++ui == un.in_seq) {
                     ui = 0;
                     do sequence_work(p, un.b + 1, un);
-                    while (un.in_seq == 0);
+                    while (un.in_seq == 0 && un.b + 1 < p.B);
                 }
             }
         }
@@ -371,7 +374,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
         auto limit = [&](int r) {
             r += tile * TR;
             if (r >= rows) return -1;
-            return p.causal ? min(un.nk - 1, p.G(un.row0 + r) + un.nk - un.nq) : un.nk - 1;
+            return p.causal ? min(un.nk - 1, p.G(un.row0 + r) + un.shift) : un.nk - 1;
         };
         uint32_t qb[NR][KS][2];    // query row 8 n + g, the thread's elements
         float cx[NR][2];           // rows 8 n + 2 t + e: logit (base 2) per unit of the product

@@ -16,12 +16,12 @@
 // A unit is a tile of up to 128 query rows (row r = i * G + g: token i of the tile, head g of the G
 // that share the K/V head) against the keys of one prefix or sequence.  Roles (6 warps): warps 0-3
 // softmax (thread = tile row = TMEM lane), warp 4 TMA producer, warp 5 TMEM allocator and MMA
-// issuer.  All of them run over the CTA's whole share without a barrier between units: O accumulators
-// alternate between two buffers and Q is free after a unit's last scores, so the next unit's first
-// scores are computed while the softmax warps still write out the one before.  The rings take all the
-// rest of shared memory: at 1500 clocks a block of 64 KB, a copy's latency of about 3000 under load
-// needs 130 KB in flight beside the tiles in use (five tiles and a second Q buffer: 2000-2300 clocks).  TMEM: two S buffers [0,128), [128,256) (P of a
-// block, bf16 pairs, overwrites the lower half of its S buffer), two O buffers from 256 on.
+// issuer.  All of them run over the CTA's whole share without a barrier between units: Q is free after
+// a unit's last scores, so the next unit's first scores are computed while the softmax warps still
+// write out the one before.  The rings take the rest of shared memory: copies have a latency of some
+// 3000 clocks under load, a block of 64 KB is due every 1500, so 130 KB have to be in flight beside the
+// tiles in use.  TMEM: two S buffers [0, 128), [128, 256) (P of a block, bf16 pairs, overwrites the lower
+// half of its S buffer), O from 256 on.
 #include "fa_serve.cuh"
 #include "tc_ptx.cuh"
 
@@ -64,7 +64,8 @@ __device__ __forceinline__ void shared_item(const SharedDecodeParams& p, int x, 
 {
     u.item = x;
     if (x < p.groups) {
-        const int b0 = min(max(p.cu_g[x], 0), p.B), b1 = min(max(p.cu_g[x + 1], b0), p.B);
+        const int b0 = min(max(p.cu_g[x], 0), p.B);
+        const int b1 = min(max(p.cu_g[x + 1], b0), p.B);
         u.tok0 = min(max(p.cu_q[b0], 0), p.total_q);
         u.ntok = min(min(max(p.cu_q[b1], u.tok0), p.total_q) - u.tok0, p.max_group_q);
         u.nk = packed_rows(p.cu_p, x, p.total_p, p.max_p, u.k0);
@@ -84,7 +85,7 @@ __device__ __forceinline__ int shared_places(const SharedDecodeParams& p, int x)
     return u.in_item * (u.nblk + kSharedUnitCost);
 }
 
-// All lanes of a warp: the line's length, and the places of the items before x[0] and x[1].
+// All lanes of a warp of the merge kernel: the line's length, and the places of the items before x[0] and x[1].
 __device__ __forceinline__ int count_places(const SharedDecodeParams& p, const int* x, int* before)
 {
     const int items = p.groups + p.B;
@@ -155,11 +156,6 @@ __device__ __noinline__ void add_odd_v(const SharedDecodeParams& p, float* dst, 
     }
 }
 
-// A value that all lanes hold, in a form that the compiler knows to be the same in all of them: what the
-// MMA warp's loops depend on must be, or every operand of every MMA is moved to a uniform register on
-// its own (1370 clocks to issue the eight MMAs of a P V product instead of 600).
-__device__ __forceinline__ int warp_uniform(int v) { return __reduce_max_sync(0xffffffffu, v); }
-
 // S = Q K^T over D/16 k-steps (both operands K-major in 128B-swizzled panels).
 template <int D, int PANEL>
 __device__ __forceinline__ void shared_issue_qk(uint32_t d_tmem, uint64_t qdesc, uint64_t kdesc, uint32_t idesc)
@@ -211,7 +207,6 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
     __shared__ __align__(8) uint64_t bar_sfull[2];  // S of a block landed in buffer b
     __shared__ __align__(8) uint64_t bar_pfull;     // softmax wrote P (and rescaled O)
     __shared__ __align__(8) uint64_t bar_pv;        // the P V product of a block has run
-    __shared__ __align__(8) uint64_t bar_ofree[2];  // O buffer b has been read out
     __shared__ __align__(8) uint64_t bar_drain;
     __shared__ SharedUnit s_unit[kSharedUnits];
     __shared__ uint32_t tmem_slot;
@@ -221,10 +216,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
     if (threadIdx.x == 0) {
         mbar_init(&bar_qfull, 1);
         mbar_init(&bar_qempty, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar_sfull[i], 1);
-            mbar_init(&bar_ofree[i], 4);
-        }
+        for (int i = 0; i < 2; ++i) mbar_init(&bar_sfull[i], 1);
         for (int s = 0; s < C::KST; ++s) {
             mbar_init(&bar_kfull[s], 1);
             mbar_init(&bar_kempty[s], 1);
@@ -349,7 +341,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
             if (left > 0 && ++ui >= un.in_item * nh) {
                 ui = 0;
                 do shared_item(p, un.item + 1, un);
-                while (un.in_item == 0);
+                while (un.in_item == 0 && un.item + 1 < items);
             }
         }
         if (ok && n > 0) {
@@ -388,8 +380,8 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
                 if (kJ > 0) ++ku;
                 if (!warp_wait_all(&bar_unit[ku % kSharedUnits], (ku / kSharedUnits) & 1, wd, kSiteSharedUnit)) return -1;
                 const SharedUnit& un = s_unit[ku % kSharedUnits];
-                kJ = warp_uniform(un.J);
-                k_left = warp_uniform(un.nk - un.jb * kSB);
+                kJ = un.J;
+                k_left = un.nk - un.jb * kSB;
                 kj = 0;
                 if (kJ == 0) return 0;
                 if (!warp_wait_all(&bar_qfull, ku & 1, wd, kSiteSharedQ)) return -1;
@@ -397,8 +389,8 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
             const int s = n % C::KST;
             if (!warp_wait_all(&bar_kfull[s], (n / C::KST) & 1, wd, kSiteSharedK)) return -1;
             tc_fence_after();
-            shared_issue_qk<D, C::PANEL_BYTES>(warp_uniform(tbase + 128 * (n & 1)), dq0,
-                                               sdesc_adv(dk0, warp_uniform(s * C::TILE_BYTES)), kIdS);
+            shared_issue_qk<D, C::PANEL_BYTES>(tbase + 128 * (n & 1), dq0,
+                                               sdesc_adv(dk0, s * C::TILE_BYTES), kIdS);
             mma_commit_w(&bar_sfull[n & 1]);
             mma_commit_w(&bar_kempty[s]);
             committed_k = n + 1;
@@ -407,28 +399,23 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
         };
         int more = issue_s(0);
         ok = more >= 0;
-        // unit and block of the next P V, the unit's blocks here and keys from its first block here on
-        int vu = 0, vj = 0, vJ = kJ, v_left = k_left;
+        // block of the next P V in its unit, the unit's blocks here and keys from its first block here on
+        int vj = 0, vJ = kJ, v_left = k_left;
 #pragma unroll 1
         for (int n = 0; ok && more > 0; ++n) {
             more = issue_s(n + 1);
             if (more < 0 || !warp_wait_all(&bar_pfull, n & 1, wd, kSiteSharedP)) { ok = false; break; }
             const int s = n % C::VST;
             if (!warp_wait_all(&bar_vfull[s], (n / C::VST) & 1, wd, kSiteSharedV)) { ok = false; break; }
-            if (vj == 0 && !warp_wait_all(&bar_ofree[vu & 1], ((vu >> 1) & 1) ^ 1, wd, kSiteSharedO)) {
-                ok = false;
-                break;
-            }
             tc_fence_after();
             // (16-key steps behind the unit's last key are left out)
-            shared_issue_pv(warp_uniform(tbase + 256 + 128 * (vu & 1)), warp_uniform(tbase + 128 * (n & 1)),
-                            sdesc_adv(dv0, warp_uniform(s * C::TILE_BYTES)), kIdPV, warp_uniform(vj > 0),
-                            warp_uniform(min(8, (v_left - vj * kSB + 15) / 16)));
+            shared_issue_pv(tbase + 256, tbase + 128 * (n & 1),
+                            sdesc_adv(dv0, s * C::TILE_BYTES), kIdPV, vj > 0,
+                            min(8, (v_left - vj * kSB + 15) / 16));
             mma_commit_w(&bar_pv);
             mma_commit_w(&bar_vempty[s]);
             committed_v = n + 1;
             if (++vj == vJ) {  // S of the next unit's first block was issued above: its size is kJ
-                ++vu;
                 vj = 0;
                 vJ = kJ;
                 v_left = k_left;
@@ -460,7 +447,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
             SharedUnit& un = s_unit[k % kSharedUnits];
             const int J = un.J, jb = un.jb, nk = un.nk;
             if (J == 0) break;
-            const uint32_t tO = tbase + lane_base + 256u + 128u * (k & 1);
+            const uint32_t tO = tbase + lane_base + 256u;
             const int ti = un.tile * p.tile_tokens.d + i;   // token of the item
             // Key blocks from jmask on need the element-wise mask (the causal edge, the ragged last
             // block); this row sees the keys [0, klim].  A prefix is seen whole by every query.
@@ -477,7 +464,7 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
             const bool any_valid = __any_sync(0xffffffffu, valid);
             float m = -INFINITY, l = 0.0f, lr = 0.0f;
             // One block.  MASKED blocks come last; apart, so that the others' loop holds neither the
-            // mask nor what follows it (with both in one loop every block took a third longer).
+            // mask nor what follows it.
             auto block = [&](auto masked_c, int j) {
                 constexpr bool MASKED = decltype(masked_c)::value;
                 const uint32_t tS = tbase + lane_base + 128u * (n & 1);
@@ -681,9 +668,8 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
             if (in) p.lse_part[row] = lse_row;
             if (in && odd)
                 add_odd_v<D>(p, p.o_part + row * D, un, max(seen, jb * kSB), min(min(nk, (jb + J) * kSB), klim + 1));
+            // (the next unit's first P V product overwrites O: it waits for this warp's next P)
             tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar_ofree[k & 1]);
         }
     }
 
@@ -724,7 +710,8 @@ __global__ void __launch_bounds__(128) fa_decode_shared_merge_kernel(const Share
         u[0].in_item = 0;
 #pragma unroll 1
         for (int g0 = 0; g0 < p.groups; g0 += 32) {
-            const bool in = g0 + lane < p.groups && p.cu_g[g0 + lane] <= b && b < p.cu_g[g0 + lane + 1];
+            const bool in = g0 + lane < p.groups && p.cu_g[g0 + lane] <= b &&
+                            b < p.cu_g[g0 + lane + 1];
             const uint32_t some = __ballot_sync(0xffffffffu, in);
             if (some) {
                 x = g0 + __ffs(some) - 1;

@@ -132,9 +132,9 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_cons
     dependent_begin();
     const int lane = threadIdx.x & 31;
     const int c = lane % C, hs = lane / C;
-    const int w = static_cast<int>(blockIdx.x) * (kRopeThreads / 32) + (threadIdx.x >> 5);
-    const int tok = w / p.parts, part = w - tok * p.parts;
-    if (tok >= p.total) return;
+    const unsigned w = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);  // (total may be 2^31 - 1)
+    if (w / p.parts >= static_cast<unsigned>(p.total)) return;
+    const int tok = static_cast<int>(w / p.parts), part = static_cast<int>(w - tok * p.parts);
     float ms[PP], mc[PP];
 #pragma unroll
     for (int e = 0; e < PP; ++e) {

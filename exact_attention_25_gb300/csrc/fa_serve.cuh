@@ -35,7 +35,7 @@ struct RopeParams {
     long long pos_ext;
     int total, H, Hkv;
     int pairs;                 // rotated pairs of a head, a multiple of 8
-    int parts;                 // warps per token
+    unsigned parts;            // warps per token
     float sign;                // -1 turns backwards (the gradient)
     int* status;
     unsigned long long turn[kRopeMaxPairs];  // turns per position, in units of 2^-64
@@ -104,6 +104,7 @@ struct CacheDecodeParams {
     FastDiv G;                 // H / Hkv
     FastDiv heads;             // Hkv
     int max_q, max_k, total_q;
+    int table_k;               // keys that a row of the table has room for
     int max_pages, num_pages, page_shift;
     int ctas;
     int row_tiles;             // row tiles of a CTA

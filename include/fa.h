@@ -29,8 +29,9 @@
  *   - Pointers are device pointers, 16-byte aligned.  The caller allocates and owns every
  *     buffer; the library allocates no device memory on these paths.
  *   - Outputs must not overlap one another, an input or the workspace: the backward's kernels
- *     run concurrently (dQ in the tail of dK/dV).  The backward entry points with contiguous
- *     tensors check this on the host (FA_ERR_INVALID_ARG); strided views are not checked.
+ *     run concurrently (dQ in the tail of dK/dV).  The backward entry points, fa_rope, the
+ *     cache's and the decodes over it and over shared prefixes check this on the host for
+ *     contiguous tensors (FA_ERR_INVALID_ARG); strided views are not checked.
  *   - stream is a cudaStream_t (NULL = legacy default stream).  Calls are asynchronous on it.
  *   - Return value: FA_OK (0) or a negative FA_ERR_* code.  Argument errors are detected on
  *     the host before anything is launched; nothing throws across the ABI.  Device-side
@@ -396,7 +397,7 @@ int fa_rope(const void* q, const void* k, void* q_out, void* k_out, const int* p
  * sequence b is row j % page_size of page page_table[b][j / page_size].  page_size is a power of
  * two in [16, 1024], num_pages*Hkv*page_size < 2^31.  A table entry outside [0, num_pages), and
  * positions past max_pages * page_size, hold nothing: writes to them are dropped, they read as
- * zero, and attention leaves their keys out.  Sequences may share pages that only get read; a
+ * zero, and attention leaves their keys out (the causal mask counts them all the same).  Sequences may share pages that only get read; a
  * page that a call writes must belong to one sequence.
  *
  * fa_cache_append quantises rows as they are written: k, v [total_new, Hkv, d] (dtype FA_BF16 or
