@@ -649,8 +649,11 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
             const int valid = s_valid[s];
             const uint8_t* kt = smem + s * 2 * C::TILE;
             const uint8_t* ex = smem + C::EXP0 + s * 2 * kKB;
-            // steps in the clear go U at a time
-            constexpr int U = NR == 1 ? 2 : 1;
+            // Steps in the clear go U at a time, so that one's products hide the other's latencies.  (16
+            // rows at d = 64: 16 sequences of up to 5000 keys, 32 rows: 18.0 us, one at a time 19.5.  At
+            // d = 128 their registers do not hold two: 8 sequences of 16 K keys, 16 rows: 95 us, one at a
+            // time 87.)
+            constexpr int U = NR == 1 || D == 64 ? 2 : 1;
             if (most >= 0)  // (else there is no query row in this warp's tile)
 #pragma unroll 1
                 for (int gi = slot; gi < kKB / 16; gi += U * slots) {

@@ -265,11 +265,13 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
         const int hg = cta % p.head_groups, part = cta / p.head_groups;
         const int nh = (p.Hkv - hg + p.head_groups - 1) / p.head_groups;
         SharedUnit un;
-        int at = 0, item = 0, ui = 0, place = 0, left = 0;
+        int at = 0, item = 0, ui = 0, place = 0, left = 0, line = 0;
+        Shares sh(0, 1);
         if (part < p.parts) {
-            const Shares sh = find_share(
+            sh = find_share(
                 items, p.parts, part, [&](int x) { return x < items ? s_places[x] * nh : 0; }, item, at);
-            left = sh.start(part + 1) - sh.start(part);
+            line = sh.start(part);  // the line's place that `place` of the unit is
+            left = sh.start(part + 1) - line;
         }
         __syncwarp();
         if (left > 0) {
@@ -301,10 +303,23 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
             un.J = max(0, end - kSharedUnitCost) - un.jb;
             un.first = k == 0;
             un.odd = 0;
+            // A prefix with several tiles of tokens is read by several CTAs.  Those of the later tiles
+            // take their blocks in the order in which the first tile's CTAs do (from where one of its
+            // shares starts, and round): then the blocks are read at the same time, and HBM gives each
+            // once.  The ragged last block stays last.
+            int rot = 0, full = un.J;
+            if (un.item < p.groups && un.tile > 0) {
+                if (un.jb + un.J == un.nblk && un.nk % kSB) --full;
+                const int first = line - place - un.tile * nh * (un.nblk + kSharedUnitCost) + kSharedUnitCost + un.jb;
+                rot = sh.start(sh.share_of(first) + 1) - first;
+                if (rot >= full) rot = 0;
+            }
+            line += end - place;
             const CUtensorMap* k_map = un.item < p.groups ? &tm_kp : &tm_k;
 #pragma unroll 1
             for (int jj = 0; ok && jj < un.J; ++jj, ++n) {
-                const int row = un.k0 + (un.jb + jj) * kSB;
+                const int jr = jj < full - rot ? jj + rot : jj < full ? jj + rot - full : jj;
+                const int row = un.k0 + (un.jb + jr) * kSB;
                 if (jj == 0) {
                     if (lane == 0) {
                         s_unit[k % kSharedUnits] = un;

@@ -82,7 +82,7 @@ struct FastDiv {
 
 // What a unit (below) costs besides its blocks (queries, merge of the warps, output), in blocks.
 constexpr int kUnitCost = 2;        // cache decode
-constexpr int kSharedUnitCost = 3;  // shared prefixes (64 over one of 32000: 64 us; 2: 72, 1: 74)
+constexpr int kSharedUnitCost = 3;  // shared prefixes (64 over one of 32000: 62 us; 4: 64, 2: 63, 1: 66)
 
 // Split-KV decode over the paged cache.  The work is a line of units: for every sequence, for
 // every `rows_cta` query rows of a group and every key/value head, kUnitCost places and one place
