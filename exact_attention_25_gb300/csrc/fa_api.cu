@@ -34,7 +34,7 @@ cudaError_t launch_vt_transpose(const void* v, void* vt, const Layout& L, int Kp
                                 cudaStream_t st);
 cudaError_t launch_rope(int d, int is_f32, const RopeParams& p, int interleaved, cudaStream_t st,
                         int num_sms);
-cudaError_t launch_cache_append(int d, int is_f32, const CacheParams& p, cudaStream_t st);
+cudaError_t launch_cache_append(int d, int is_f32, const CacheParams& p, cudaStream_t st, int num_sms);
 cudaError_t launch_cache_read(int d, int is_f32, const CacheParams& p, cudaStream_t st);
 cudaError_t launch_decode_cache(int d, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const CacheDecodeParams& p, cudaStream_t st);
@@ -1379,7 +1379,7 @@ extern "C" int fa_cache_append(const void* k, const void* v, const long long* st
     DeviceInfo* di = nullptr;
     if (int rc = device_info(&di)) return rc;
     p.status = di->status;
-    cudaError_t e = fa::launch_cache_append(d, dtype == FA_F32, p, static_cast<cudaStream_t>(stream));
+    cudaError_t e = fa::launch_cache_append(d, dtype == FA_F32, p, static_cast<cudaStream_t>(stream), di->sms);
     if (e != cudaSuccess) return cuda_fail(e, "cache append launch");
     return FA_OK;
 }

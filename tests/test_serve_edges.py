@@ -184,6 +184,35 @@ def test_shared_decode_of_many_heads(H, Hkv, d):
     test_decode_shared.check(got, test_decode_shared.reference(x, 0.1, True))
 
 
+# ------------------------------------------------------------------------------ large appends
+
+@gpu
+@pytest.mark.parametrize("strided", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_a_large_append_equals_small_ones(dtype, d, strided):
+    """A batch whose grid takes k and v in turn, against its sequences one by one, whose grids take
+    them side by side; a row of every kind of value in both."""
+    B, Hkv, page = 40, 6, 64
+    lens = [70 + 3 * b for b in range(B)]
+    table, pool = table_for(lens, page, 1, 5)
+    g = torch.Generator().manual_seed(d)
+    T = sum(lens)
+    x = torch.randn(2, T, Hkv, d + (8 if strided else 0), generator=g).to(dtype).cuda()[..., :d]
+    x[0, 5] = 0.0
+    x[1, T - 1, 2, 3] = float("inf")
+    x[0, T // 2, 1, 7] = float("nan")
+    starts = np.cumsum([0] + lens)
+    many, few = fa.new_cache(pool, page, Hkv, d), fa.new_cache(pool, page, Hkv, d)
+    fa.cache_append(many, x[0], x[1], cu(lens).cuda(), i32(*lens).cuda(), table.cuda(), max(lens))
+    for b, n in enumerate(lens):
+        k, v = (t[starts[b]:starts[b + 1]] for t in x)
+        fa.cache_append(few, k, v, i32(0, n).cuda(), i32(n).cuda(), table[b:b + 1].cuda(), n)
+    fa.fa_device_status()
+    for a, b in zip(many, few):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
 # ------------------------------------------------------------------------------ streams and graphs
 
 @gpu
