@@ -133,30 +133,8 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_cons
     const int lane = threadIdx.x & 31;
     const int c = lane % C, hs = lane / C;
     const unsigned w = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);  // (total may be 2^31 - 1)
-    if (w / p.parts >= static_cast<unsigned>(p.total)) return;
-    const int tok = static_cast<int>(w / p.parts), part = static_cast<int>(w - tok * p.parts);
-    float ms[PP], mc[PP];
-#pragma unroll
-    for (int e = 0; e < PP; ++e) {
-        const int pr = 8 * c + hs * PP + e;
-        ms[e] = 0.0f;
-        mc[e] = 1.0f;
-        if (pr < p.pairs) {
-            const long long at = static_cast<long long>(p.axis[pr]) * p.total + tok;
-            if (in_extent(at, 1, p.pos_ext, p.status)) {
-                const unsigned long long t =
-                    static_cast<unsigned long long>(static_cast<long long>(p.pos[at])) * p.turn[pr];
-                turn_sincos(static_cast<uint32_t>((t + 0x80000000ull) >> 32), ms[e], mc[e]);
-                ms[e] *= p.sign;
-            }
-        }
-    }
-    float sn[8], cs[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        sn[j] = __shfl_sync(0xffffffffu, ms[j % PP], c + C * (j / PP));
-        cs[j] = __shfl_sync(0xffffffffu, mc[j % PP], c + C * (j / PP));
-    }
+    const int tok = p.parts(static_cast<int>(w)), part = static_cast<int>(w - tok * static_cast<unsigned>(p.parts.d));
+    if (static_cast<unsigned>(tok) >= static_cast<unsigned>(p.total)) return;
     // lo, hi: the lane's two 8-element chunks of a head
     const bool turned = 8 * c < p.pairs;
     int lo, hi;
@@ -169,8 +147,8 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_cons
     }
     const int heads = p.H + p.Hkv;
     const int steps = (heads + HS - 1) / HS;
-    const int s0 = static_cast<int>(static_cast<long long>(steps) * part / p.parts);
-    const int s1 = static_cast<int>(static_cast<long long>(steps) * (part + 1) / p.parts);
+    const int s0 = part * p.per, s1 = min(s0 + p.per, steps);
+    float sn[8], cs[8];
     for (int s = s0; s < s1; s += kRopeUnroll) {
         Chunk<T> a[kRopeUnroll], b[kRopeUnroll];
         bool on[kRopeUnroll];
@@ -184,6 +162,29 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_cons
                 on[u] = in_extent(off, D, p.x_ext[z], p.status);
                 const T* src = static_cast<const T*>(p.x[z]) + off;
                 if (on[u]) load_chunks<WIDE, INTERLEAVED>(src + lo, src + hi, a[u], b[u]);
+            }
+        }
+        if (s == s0) {  // the angles, while the first heads are on their way
+            float ms[PP], mc[PP];
+#pragma unroll
+            for (int e = 0; e < PP; ++e) {
+                const int pr = 8 * c + hs * PP + e;
+                ms[e] = 0.0f;
+                mc[e] = 1.0f;
+                if (pr < p.pairs) {
+                    const long long at = static_cast<long long>(p.axis[pr]) * p.total + tok;
+                    if (in_extent(at, 1, p.pos_ext, p.status)) {
+                        const unsigned long long t =
+                            static_cast<unsigned long long>(static_cast<long long>(p.pos[at])) * p.turn[pr];
+                        turn_sincos(static_cast<uint32_t>((t + 0x80000000ull) >> 32), ms[e], mc[e]);
+                        ms[e] *= p.sign;
+                    }
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                sn[j] = __shfl_sync(0xffffffffu, ms[j % PP], c + C * (j / PP));
+                cs[j] = __shfl_sync(0xffffffffu, mc[j % PP], c + C * (j / PP));
             }
         }
 #pragma unroll
@@ -216,15 +217,17 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_cons
     }
 }
 
-// p.parts is chosen here: enough warps to fill the SMs when the tokens are few.
+// p.parts and p.per are chosen here: enough warps to fill the SMs when the tokens are few.
 template <class T, int D>
 static cudaError_t launch_rope_impl(RopeParams p, int interleaved, cudaStream_t st, int num_sms)
 {
     constexpr int HS = 32 / (D / 16);
     const int steps = (p.H + p.Hkv + HS - 1) / HS;
     const int want = (num_sms * 16 + p.total - 1) / p.total;
-    p.parts = want < 1 ? 1 : (want > steps ? steps : want);
-    const long long warps = static_cast<long long>(p.total) * p.parts;
+    const int parts = want < 1 ? 1 : (want > steps ? steps : want);
+    p.per = (steps + parts - 1) / parts;
+    p.parts = FastDiv((steps + p.per - 1) / p.per);  // (tokens * parts^2 < 2^32 where parts > 1)
+    const long long warps = static_cast<long long>(p.total) * p.parts.d;
     const dim3 grid(static_cast<unsigned>((warps + kRopeThreads / 32 - 1) / (kRopeThreads / 32)));
     // 32-byte accesses where every row allows them; bf16 halves that lie apart are 16 bytes anyway
     bool wide = interleaved || sizeof(T) == 4;

@@ -23,6 +23,20 @@ enum ServeWaitSite : int {
     kSiteSharedDrain,
 };
 
+// Division by a number known on the host: x / d = (x * m) >> 32 with m = floor(2^32 / d) + 1, exact for
+// x * d < 2^32 (m d exceeds 2^32 by at most d).  A division in line is some 25 instructions, and these
+// kernels' first microseconds go by what they have to fetch.
+struct FastDiv {
+    unsigned long long m;
+    int d;
+    FastDiv() = default;
+    explicit FastDiv(int v) : m((1ull << 32) / static_cast<unsigned>(v) + 1), d(v) {}
+    __device__ __forceinline__ int operator()(int x) const
+    {
+        return static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(x)) * m) >> 32);
+    }
+};
+
 constexpr int kRopeMaxPairs = 64;
 
 // Rotary positions.  Pair p of a head turns by positions[axis[p]][token] * turn[p] / 2^64 turns.
@@ -35,7 +49,8 @@ struct RopeParams {
     long long pos_ext;
     int total, H, Hkv;
     int pairs;                 // rotated pairs of a head, a multiple of 8
-    unsigned parts;            // warps per token
+    FastDiv parts;             // warps of a token ...
+    int per;                   // ... and the head steps of each
     float sign;                // -1 turns backwards (the gradient)
     int* status;
     unsigned long long turn[kRopeMaxPairs];  // turns per position, in units of 2^-64
@@ -65,20 +80,6 @@ struct CacheParams {
 };
 
 constexpr int kCacheBlock = 128;  // keys of a block of the cache decode
-
-// Division by a number known on the host: x / d = (x * m) >> 32 with m = floor(2^32 / d) + 1, exact for
-// x * d < 2^32 (m d exceeds 2^32 by at most d).  A division in line is some 25 instructions, and these
-// kernels' first microseconds go by what they have to fetch.
-struct FastDiv {
-    unsigned long long m;
-    int d;
-    FastDiv() = default;
-    explicit FastDiv(int v) : m((1ull << 32) / static_cast<unsigned>(v) + 1), d(v) {}
-    __device__ __forceinline__ int operator()(int x) const
-    {
-        return static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(x)) * m) >> 32);
-    }
-};
 
 // What a unit (below) costs besides its blocks (queries, merge of the warps, output), in blocks.
 constexpr int kUnitCost = 2;        // cache decode
