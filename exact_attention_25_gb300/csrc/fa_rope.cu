@@ -118,7 +118,7 @@ __device__ __forceinline__ void store_chunks(float* lo, float* hi, const Chunk<f
     store_32b<WIDE>(hi, b.w);
 }
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 constexpr int kRopeUnroll = 4;  // head steps whose loads are in flight together
 
 }  // namespace
@@ -129,9 +129,22 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_cons
     constexpr int C = D / 16;     // lanes of a head, 8 pairs (16 elements) each
     constexpr int HS = 32 / C;    // heads per step of a warp
     constexpr int PP = 8 / HS;    // angles a lane computes
-    dependent_begin();
     const int lane = threadIdx.x & 31;
     const int c = lane % C, hs = lane / C;
+    // The lane's pairs of the table.  Read through a generic address: as constants, with another index in
+    // every lane, they took a third of a small call (8 tokens: 3.0 us instead of 2.1).
+    const unsigned long long* turns = p.turn;
+    const unsigned char* axes = p.axis;
+    asm volatile("" : "+l"(turns), "+l"(axes));
+    unsigned long long turn[PP];
+    int axis[PP];
+#pragma unroll
+    for (int e = 0; e < PP; ++e) {
+        const int pr = 8 * c + hs * PP + e;
+        turn[e] = pr < p.pairs ? turns[pr] : 0;
+        axis[e] = pr < p.pairs ? axes[pr] : 0;
+    }
+    dependent_begin();
     const unsigned w = blockIdx.x * (kRopeThreads / 32) + (threadIdx.x >> 5);  // (total may be 2^31 - 1)
     const int tok = p.parts(static_cast<int>(w)), part = static_cast<int>(w - tok * static_cast<unsigned>(p.parts.d));
     if (static_cast<unsigned>(tok) >= static_cast<unsigned>(p.total)) return;
@@ -168,17 +181,14 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_cons
             float ms[PP], mc[PP];
 #pragma unroll
             for (int e = 0; e < PP; ++e) {
-                const int pr = 8 * c + hs * PP + e;
                 ms[e] = 0.0f;
                 mc[e] = 1.0f;
-                if (pr < p.pairs) {
-                    const long long at = static_cast<long long>(p.axis[pr]) * p.total + tok;
-                    if (in_extent(at, 1, p.pos_ext, p.status)) {
-                        const unsigned long long t =
-                            static_cast<unsigned long long>(static_cast<long long>(p.pos[at])) * p.turn[pr];
-                        turn_sincos(static_cast<uint32_t>((t + 0x80000000ull) >> 32), ms[e], mc[e]);
-                        ms[e] *= p.sign;
-                    }
+                const long long at = static_cast<long long>(axis[e]) * p.total + tok;
+                if (in_extent(at, 1, p.pos_ext, p.status)) {
+                    const unsigned long long t =
+                        static_cast<unsigned long long>(static_cast<long long>(p.pos[at])) * turn[e];
+                    turn_sincos(static_cast<uint32_t>((t + 0x80000000ull) >> 32), ms[e], mc[e]);
+                    ms[e] *= p.sign;
                 }
             }
 #pragma unroll
