@@ -39,7 +39,7 @@ cudaError_t launch_cache_read(int d, int is_f32, const CacheParams& p, cudaStrea
 cudaError_t launch_decode_cache(int d, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const CacheDecodeParams& p, cudaStream_t st);
 cudaError_t launch_decode_shared(int d, const CUtensorMap* maps, const SharedDecodeParams& p,
-                                 cudaStream_t st);
+                                 cudaStream_t st, int num_sms);
 
 // Device status word written by bounded waits that give up (0 = fine).
 __device__ int g_status_word;
@@ -1702,7 +1702,7 @@ extern "C" int fa_fwd_decode_shared(const void* q, const void* k_prefix, const v
     if (!rc) rc = make_map(&maps[3], k, Hkv, total_k, d, 128, true, krs, d);
     if (!rc) rc = make_map(&maps[4], v, Hkv, total_k, d, 128, true, krs, d);
     if (rc) return rc;
-    cudaError_t e = fa::launch_decode_shared(d, maps, p, static_cast<cudaStream_t>(stream));
+    cudaError_t e = fa::launch_decode_shared(d, maps, p, static_cast<cudaStream_t>(stream), di->sms);
     if (e != cudaSuccess) return cuda_fail(e, "shared decode launch");
     return FA_OK;
 }

@@ -789,16 +789,14 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
 }
 
 // Merge of the parts of every unit that several shares cut: CTA c takes the unit that the border
-// between shares c and c + 1 cuts, if that is the unit's first cut; a warp takes a query row:
-//     O = sum_s e^{lse_s} O_s / sum_s e^{lse_s},   lse = log sum_s e^{lse_s}.
-// Only parts that saw a key (lse_s > -inf) are read; a row without any gets O = 0, lse = -inf.
+// between shares c and c + 1 cuts, if that is the unit's first cut; a warp takes a query row.  A row
+// that saw no key in any part gets O = 0, lse = -inf.
 // It is always launched behind the attention kernel of its call, whose CTAs let it start only after
 // their own wait: so the lengths, which that wait has made visible, are read before this kernel's.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) fa_decode_cache_merge_kernel(const CacheDecodeParams p)
 {
     constexpr int EPL = D / 32;
-    constexpr int BATCH = 4;  // parts whose rows are in flight together
     const int lane = threadIdx.x & 31;
     const int c0 = static_cast<int>(blockIdx.x);
     Unit u;
@@ -825,59 +823,10 @@ __global__ void __launch_bounds__(kMergeThreads) fa_decode_cache_merge_kernel(co
     dependent_begin();
     const int r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);
     if (r < rows) {
-        float mx = -INFINITY, sum = 0.0f, acc[EPL];
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) acc[e] = 0.0f;
-        auto row_of = [&](int k) {
-            return static_cast<long long>(2 * (c0 + k) + (k == 0 ? lead : 0)) * p.rows_cta + r;
-        };
-        for (int s0 = 0; s0 < parts; s0 += 32) {
-            float ls = -INFINITY;
-            if (s0 + lane < parts && in_extent(row_of(s0 + lane), 1, p.part_ext / D, p.status))
-                ls = p.lse_part[row_of(s0 + lane)];
-            float bm = ls;
-            uint32_t live = __ballot_sync(0xffffffffu, !(ls == -INFINITY));  // NaN counts
-#pragma unroll
-            for (int d = 16; d; d >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, d));
-            if (!live) continue;
-            const float nm = fmaxf(mx, bm);
-            const float keep = mx == -INFINITY ? 0.0f : expf(mx - nm);
-            sum *= keep;
-#pragma unroll
-            for (int e = 0; e < EPL; ++e) acc[e] *= keep;
-            mx = nm;
-            const float wt = ls == -INFINITY ? 0.0f : expf(ls - nm);
-            while (live) {
-                float v[BATCH][EPL], ws[BATCH];
-#pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    ws[k] = 0.0f;
-#pragma unroll
-                    for (int e = 0; e < EPL; ++e) v[k][e] = 0.0f;
-                    if (live) {
-                        const int s = __ffs(live) - 1;
-                        live &= live - 1;
-                        ws[k] = __shfl_sync(0xffffffffu, wt, s);
-                        const long long po = row_of(s0 + s) * D + EPL * lane;
-                        if (in_extent(po, EPL, p.part_ext, p.status)) {
-                            if constexpr (EPL == 4) {
-                                const float4 x = *reinterpret_cast<const float4*>(p.o_part + po);
-                                v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
-                            } else {
-                                const float2 x = *reinterpret_cast<const float2*>(p.o_part + po);
-                                v[k][0] = x.x; v[k][1] = x.y;
-                            }
-                        }
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < BATCH; ++k) {
-                    sum += ws[k];
-#pragma unroll
-                    for (int e = 0; e < EPL; ++e) acc[e] = fmaf(ws[k], v[k][e], acc[e]);
-                }
-            }
-        }
+        float mx, sum, acc[EPL];
+        merge_parts<D, 16>(
+            parts, [&](int k) { return (2 * (c0 + k) + (k == 0 ? lead : 0)) * p.rows_cta + r; },
+            p.o_part, p.lse_part, p.part_ext / D, p.status, mx, sum, acc);
         const int i = p.G(u.row0 + r), h = u.hk * p.G.d + (u.row0 + r) - i * p.G.d;
         const long long row = (static_cast<long long>(u.q0 + i) * p.H + h) * D + EPL * lane;
         const long long stat = static_cast<long long>(h) * p.total_q + u.q0 + i;

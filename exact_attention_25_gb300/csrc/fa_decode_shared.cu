@@ -696,23 +696,20 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
 }
 
 // Merge: one warp for each query row (token and head) gathers the row's parts, those of its
-// group's prefix and those of its sequence's keys:
-//     O = sum_s e^{lse_s} O_s / sum_s e^{lse_s},   lse = log sum_s e^{lse_s}.
-// Only parts that saw a key (lse_s > -inf) are read; a row without any gets O = 0, lse = -inf.
+// group's prefix and those of its sequence's keys.  A row that saw no key in any gets O = 0, lse = -inf.
 // It is always launched behind the attention kernel of its call, whose CTAs let it start only after
 // their own wait: so the lengths, which that wait has made visible, are read before this kernel's.
-template <int D>
+template <int D, int BATCH>
 __global__ void __launch_bounds__(128) fa_decode_shared_merge_kernel(const SharedDecodeParams p)
 {
     constexpr int EPL = D / 32;
-    constexpr int BATCH = 4;  // parts whose rows are in flight together
     const int lane = threadIdx.x & 31;
     const int w = static_cast<int>(blockIdx.x) * 4 + (threadIdx.x >> 5);
     const int h = w % p.H;
     const int i = w / p.H % p.max_q, b = w / p.H / p.max_q;
     SharedUnit u[2];  // its group's prefix, its own keys
     int count[2] = {0, 0}, c0[2], lead[2];
-    long long row[2] = {0, 0};
+    int row[2] = {0, 0};
     bool here = b < p.B, whole[2] = {false, false};
     int tok = 0;
     if (here) {
@@ -751,68 +748,23 @@ __global__ void __launch_bounds__(128) fa_decode_shared_merge_kernel(const Share
             count[z] = s1 - s0 + 1;
             whole[z] = s1 == s0;
             lead[z] = sh.start(s0) >= start - kSharedUnitCost ? 0 : 1;
-            row[z] = whole[z] ? (static_cast<long long>(z ? p.total_q : 0) + tok) * p.H + h
-                              : p.part_row0 + (ti - tile * p.tile_tokens.d) * p.G.d + (h - hk * p.G.d);
+            row[z] = whole[z] ? ((z ? p.total_q : 0) + tok) * p.H + h
+                              : static_cast<int>(p.part_row0) + (ti - tile * p.tile_tokens.d) * p.G.d + (h - hk * p.G.d);
         }
     }
     dependent_begin();
     if (!here) return;
-    auto row_of = [&](int k) {
-        const int z = k < count[0] ? 0 : 1;
-        const int c = z ? k - count[0] : k;
-        return whole[z] ? row[z]
-                        : row[z] + (2ll * (c0[z] + c * p.head_groups) + (c == 0 ? lead[z] : 0)) * 128;
-    };
-    const int parts = count[0] + count[1];
-    float mx = -INFINITY, sum = 0.0f, acc[EPL];
-#pragma unroll
-    for (int e = 0; e < EPL; ++e) acc[e] = 0.0f;
-    for (int s0 = 0; s0 < parts; s0 += 32) {
-        const bool mine = s0 + lane < parts;
-        const long long r = mine ? row_of(s0 + lane) : 0;
-        float ls = -INFINITY;
-        if (mine && in_extent(r, 1, p.part_ext, p.status)) ls = p.lse_part[r];
-        float bm = ls;
-        uint32_t live = __ballot_sync(0xffffffffu, !(ls == -INFINITY));  // NaN counts
-#pragma unroll
-        for (int d = 16; d; d >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, d));
-        if (!live) continue;
-        const float nm = fmaxf(mx, bm);
-        const float keep = mx == -INFINITY ? 0.0f : expf(mx - nm);
-        sum *= keep;
-#pragma unroll
-        for (int e = 0; e < EPL; ++e) acc[e] *= keep;
-        mx = nm;
-        const float wt = ls == -INFINITY ? 0.0f : expf(ls - nm);
-        while (live) {
-            float v[BATCH][EPL], ws[BATCH];
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                ws[k] = 0.0f;
-#pragma unroll
-                for (int e = 0; e < EPL; ++e) v[k][e] = 0.0f;
-                if (live) {
-                    const int s = __ffs(live) - 1;
-                    live &= live - 1;
-                    ws[k] = __shfl_sync(0xffffffffu, wt, s);
-                    const float* src = p.o_part + __shfl_sync(0xffffffffu, r, s) * D + EPL * lane;
-                    if constexpr (EPL == 4) {
-                        const float4 x = *reinterpret_cast<const float4*>(src);
-                        v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
-                    } else {
-                        const float2 x = *reinterpret_cast<const float2*>(src);
-                        v[k][0] = x.x; v[k][1] = x.y;
-                    }
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < BATCH; ++k) {
-                sum += ws[k];
-#pragma unroll
-                for (int e = 0; e < EPL; ++e) acc[e] = fmaf(ws[k], v[k][e], acc[e]);
-            }
-        }
-    }
+    float mx, sum, acc[EPL];
+    merge_parts<D, BATCH>(
+        count[0] + count[1],
+        [&](int k) {
+            const bool z = k >= count[0];
+            const int c = z ? k - count[0] : k, first = (z ? row[1] : row[0]);
+            return (z ? whole[1] : whole[0]) ? first
+                                             : first + (2 * ((z ? c0[1] : c0[0]) + c * p.head_groups) +
+                                                        (c == 0 ? (z ? lead[1] : lead[0]) : 0)) * 128;
+        },
+        p.o_part, p.lse_part, p.part_ext, p.status, mx, sum, acc);
     const long long out = (static_cast<long long>(tok) * p.H + h) * D + EPL * lane;
     const long long stat = static_cast<long long>(h) * p.total_q + tok;
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -828,7 +780,8 @@ __global__ void __launch_bounds__(128) fa_decode_shared_merge_kernel(const Share
 }
 
 template <int D>
-static cudaError_t launch_decode_shared_impl(const CUtensorMap* maps, const SharedDecodeParams& p, cudaStream_t st)
+static cudaError_t launch_decode_shared_impl(const CUtensorMap* maps, const SharedDecodeParams& p, cudaStream_t st,
+                                             int num_sms)
 {
     using C = SharedCfg<D>;
     static bool attr_set[64] = {};
@@ -843,15 +796,22 @@ static cudaError_t launch_decode_shared_impl(const CUtensorMap* maps, const Shar
     cudaError_t e = launch_dependent(fa_decode_shared_kernel<D>, dim3(p.ctas), dim3(C::THREADS), C::SMEM_BYTES,
                                      st, maps[0], maps[1], maps[2], maps[3], maps[4], p);
     if (e != cudaSuccess) return e;
+    // The merge's CTAs start beside the attention's and wait there; with few rows they all fit with 16
+    // parts in flight each (8 queries: 12.2 us, 12.7 with 8), with many only with 8 (64 queries: 61.7 us,
+    // with 16 a second wave starts late, 65.4).
     const long long rows = static_cast<long long>(p.B) * p.max_q * p.H;
-    return launch_dependent(fa_decode_shared_merge_kernel<D>, dim3(static_cast<unsigned>((rows + 3) / 4)),
-                            dim3(128), 0, st, p);
+    const dim3 grid(static_cast<unsigned>((rows + 3) / 4));
+    return rows <= 8ll * num_sms
+               ? launch_dependent(fa_decode_shared_merge_kernel<D, 16>, grid, dim3(128), 0, st, p)
+               : launch_dependent(fa_decode_shared_merge_kernel<D, 8>, grid, dim3(128), 0, st, p);
 }
 
 // maps: q, k_prefix, v_prefix, k, v
-cudaError_t launch_decode_shared(int d, const CUtensorMap* maps, const SharedDecodeParams& p, cudaStream_t st)
+cudaError_t launch_decode_shared(int d, const CUtensorMap* maps, const SharedDecodeParams& p, cudaStream_t st,
+                                 int num_sms)
 {
-    return d == 64 ? launch_decode_shared_impl<64>(maps, p, st) : launch_decode_shared_impl<128>(maps, p, st);
+    return d == 64 ? launch_decode_shared_impl<64>(maps, p, st, num_sms)
+                   : launch_decode_shared_impl<128>(maps, p, st, num_sms);
 }
 
 }  // namespace fa
