@@ -236,8 +236,8 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
 
     if (warp == kComputeWarps) {
         // ------------------------------------------------------------- copies
-        // The share's units one after another; a unit's description goes to s_unit before its
-        // page ids are read, so the compute warps fetch its queries meanwhile.  (kUnits > STAGES + 1:
+        // The share's units one after another; a unit's description goes to s_unit while its first page
+        // ids are on their way, so the compute warps fetch its queries meanwhile.  (kUnits > STAGES + 1:
         // when a slot is written again, every warp has released a block of a later unit than the
         // one that it held.)
         Unit un;
@@ -262,7 +262,16 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
             un.jb = max(0, place - kUnitCost);
             un.J = max(0, end - kUnitCost) - un.jb;
             un.flags = k == 0 ? kFirst : 0;
+            // page ids base + lane; the first ones are on their way before anything else is done
+            int base = (un.jb * kKB) >> p.page_shift, ids = -1;
+            auto load_ids = [&]() {
+                const int idx = base + lane;
+                ids = -1;
+                if (idx < p.max_pages && (static_cast<long long>(idx) << p.page_shift) < un.nk)
+                    ids = p.table[static_cast<long long>(un.b) * p.max_pages + idx];
+            };
             if (un.J > 0) {
+                load_ids();
                 if (lane == 0) {
                     s_unit[k % kUnits] = un;
                     mbar_arrive(&bar_unit[k % kUnits]);
@@ -279,22 +288,17 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
                 }
                 ++k;
             }
-            int base = -1, ids = -1;                          // page ids base + lane
 #pragma unroll 1
             for (int jj = 0; jj < un.J; ++jj, ++it) {
                 const int s = it % C::STAGES;
                 const int pos = (un.jb + jj) * kKB;
                 const int first = pos >> p.page_shift;
-                if (base < 0 || first + np > base + 32) {
+                if (first + np > base + 32) {
                     base = first;
-                    const int idx = base + lane;
-                    ids = -1;
-                    if (idx < p.max_pages && (static_cast<long long>(idx) << p.page_shift) < un.nk)
-                        ids = p.table[static_cast<long long>(un.b) * p.max_pages + idx];
-                    if (ids >= p.num_pages) ids = -1;
+                    load_ids();
                 }
                 const int id = __shfl_sync(0xffffffffu, ids, (first - base + lane) & 31);
-                const bool mine = lane < np && id >= 0;
+                const bool mine = lane < np && id >= 0 && id < p.num_pages;
                 const uint32_t got = __ballot_sync(0xffffffffu, mine);
                 ok = warp_wait_all(&bar_empty[s], ((it / C::STAGES) & 1) ^ 1, wd, kSiteCacheEmpty);
                 if (!ok) break;
