@@ -8,7 +8,9 @@
 // makes the division by the scale exact, needs one byte, and makes reading back into bf16 exact.
 // Infinities and NaNs are stored as the NaN code and do not count towards the maximum.
 //
-// Both directions are HBM-bound: each element is read and written once.  A warp owns 16 tokens
+// Both directions are HBM-bound: each element is read and written once (reading 8 sequences of up to 16 K
+// tokens: 70 us, 96 % of the copy rate; writing 9
+// ragged prompts of up to 8 K: 35 us, 86 %, 64 even ones of 1 K: 60 us, 98 %).  A warp owns 16 tokens
 // of one head; the warps of a CTA take neighbouring heads of the same tokens, so a CTA touches
 // whole runs of the packed rows [token, head, d], while each warp touches one run of a page
 // [head, row, d].  All loads of a tensor's 16 rows are issued before any is used.
@@ -131,11 +133,10 @@ __device__ __forceinline__ long long cache_row(const CacheParams& p, int b, int 
 
 }  // namespace
 
-// Bytes bound it: 64 prompts of 1 K tokens and 8 heads of 128 bf16 elements take 60 us, 4.9 TB/s.  SPLIT:
-// half of the grid (y) takes k and half v; where the grid is small anyway the two then run side by side
+// SPLIT: half of the grid (y) takes k and half v; where the grid is small anyway the two then run side by side
 // (one new token for each of 64 sequences: 2.7 us, 3.2 in turn; 64 of 128 tokens: 11.0 and 10.5).  In turn
-// the loop over k and v stays rolled for bf16, whose warps then fit more often (60.5 us, unrolled 62.8),
-// and is unrolled for fp32 (101 us, rolled 107).
+// the loop over k and v stays rolled for bf16, whose warps then fit more often (64 of 1 K tokens: 60.5 us,
+// unrolled 62.8), and is unrolled for fp32 (101 us, rolled 107).
 template <class T, int D, bool WIDE, bool SPLIT>
 __global__ void __launch_bounds__(kCacheThreads) fa_cache_append_kernel(const CacheParams p)
 {

@@ -3,14 +3,19 @@
 // two.  Nothing is rounded on the way in: the result is exact attention on the cached values up
 // to fp32 accumulation and the f16 rounding of the softmax weights.
 //
-// What bounds it: the codes, read once (2 * Nk * Hkv * d bytes a sequence).  At the copy rate an
-// SM receives about 23 bytes a clock, so tcgen05 has no place here although a decode tile of
-// bf16 keys uses it: the codes would have to become 16-bit operands in shared memory, and one
+// What bounds it: the codes, read once (2 * Nk * Hkv * d bytes a sequence): 8 sequences of up to 32 K
+// keys, 8 heads of 128: 61 us, 89 % of the copy rate; 64 of up to 4 K: 50 us, 80 %.  With 16 query rows a
+// head at d = 128 (8 sequences of 16 K: 88 us, 45 %) a step's chain of products, exponentials and products,
+// of which the registers hold only one at a time.  Calls of one or two blocks a CTA are a chain of
+// latencies: one sequence of 4 K keys 9.7 us, of which lengths 0.9, page ids 1.1, copies and products 2-3,
+// the warps' merge 1, the parts' stores 0.5, and the merge kernel 2.3.
+// At the copy rate an SM receives about 23 bytes a clock, so tcgen05 has no place here although a decode
+// tile of bf16 keys uses it: the codes would have to become 16-bit operands in shared memory, and one
 // write by the copy, a read and a double-width write by the conversion and a double-width read
 // by the tensor core (6 bytes of shared-memory traffic a code, 140 a clock) exceed the 128 bytes
 // a clock that shared memory moves; kind::f8f6f4 would want Q and the weights in 8 bits too.
 // Here the codes are converted between shared memory and mma.sync fragments instead, in
-// registers: 2 bytes of traffic a code, 0.18 m16n8k16 a clock.
+// registers: 2 bytes of traffic a code, and 0.09 m16n8k16 a clock for 8 query rows, of 0.5.
 //
 // Layout of a CTA: warps 0-3 compute, warp 4 copies pages to a ring of 128-key blocks by TMA
 // (swizzled rows, plus the rows' exponent bytes).  A group's query rows (row i * G + g: query
@@ -18,9 +23,9 @@
 // w % row_tiles and on every (4 / row_tiles)-th 16-key step of a block, with its own online
 // softmax; the warps' results merge through shared memory at the end of a unit.  The copies run
 // ahead over unit boundaries.  Two CTAs an SM, each with an equal share of the whole batch's blocks
-// (CacheDecodeParams), found from the lengths on the device: a fixed number of ranges a sequence
-// left 30-45 % of the slots idle on ragged batches, and finer ranges cost every CTA its 4-5 us of
-// dependent loads (lengths, table, copies, output) again.
+// (CacheDecodeParams), found from the lengths on the device: a fixed number of ranges a sequence left
+// SMs idle on ragged batches (the first of the above at best 71 us), and finer ranges cost every CTA its
+// chain of latencies again.
 //
 // Both products are computed transposed, with the keys (S^T = K Q^T) or the columns of V (O^T =
 // V^T P^T) as the 16 rows of the m16n8k16 product and the query rows as its 8 columns: a decode

