@@ -9,11 +9,11 @@
 // Infinities and NaNs are stored as the NaN code and do not count towards the maximum.
 //
 // Both directions are HBM-bound: each element is read and written once (reading 8 sequences of up to 16 K
-// tokens: 70 us, 96 % of the copy rate; writing 9
-// ragged prompts of up to 8 K: 35 us, 86 %, 64 even ones of 1 K: 60 us, 98 %).  A warp owns 16 tokens
-// of one head; the warps of a CTA take neighbouring heads of the same tokens, so a CTA touches
-// whole runs of the packed rows [token, head, d], while each warp touches one run of a page
-// [head, row, d].  All loads of a tensor's 16 rows are issued before any is used.
+// tokens: 70 us, 96 % of the copy rate; writing 64 prompts of 1 K: 60 us, 98 %, 9 ragged ones of up to
+// 8 K, which leave half of the grid's warps without rows: 35 us, 86 %).  A warp owns 16 tokens of one head;
+// the warps of a CTA take neighbouring heads of the same tokens, so a CTA touches whole runs of the packed
+// rows [token, head, d], while each warp touches one run of a page [head, row, d].  All loads of a tensor's
+// 16 rows are issued before any is used.
 #include "fa_serve.cuh"
 #include "tc_ptx.cuh"
 
