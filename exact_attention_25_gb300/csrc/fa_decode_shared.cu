@@ -8,13 +8,14 @@
 //
 // What bounds it: reading prefix and own keys once (HBM), and for large groups the exponentials of
 // tokens x heads x prefix scores.  64 sequences with up to 1024 keys of their own over 32000 tokens, 32
-// heads over 8 of 128: 62 us, 253 MB from HBM (4.1 TB/s) and 421 MB from L2; 53 us without the softmax,
-// 57 without its products; a CTA's first three blocks take 10 us, when 152 cold rings fill at once.  8 sequences over 4 K
-// tokens: 12.2 us, a chain of latencies.  Both kinds of work are units of one line (units, below) shared
-// out evenly over the SMs, so memory-bound and arithmetic-bound units run side by side.  Every
-// key/value head has a line of its own, the same for all, and CTA c works on head c mod Hkv: so the
-// CTAs of the heads read the same tokens at the same time.  (In one line over all heads each read its
-// 256-byte pieces of the token rows at a time of its own, and HBM gave 4 TB/s.)
+// heads over 8 of 128: 62 us, 253 MB from HBM (4.1 TB/s) and 421 MB from L2 (the prefix is copied for each of
+// its two tiles); 53 us without the softmax, 57 without its products.  8 sequences over 4 K tokens: 12.2 us,
+// a chain of latencies.
+//
+// Both kinds of work are units of one line (units, below) shared out evenly over the SMs, so memory-bound
+// and arithmetic-bound units run side by side.  Every key/value head has a line of its own, the same for
+// all, and CTA c works on head c mod Hkv: so the CTAs of the heads read the same tokens at the same time.
+// (In one line over all heads each read its 256-byte pieces of the token rows at a time of its own: 70 us.)
 //
 // A unit is a tile of up to 128 query rows (row r = i * G + g: token i of the tile, head g of the G
 // that share the K/V head) against the keys of one prefix or sequence.  Roles (6 warps): warps 0-3

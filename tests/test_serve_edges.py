@@ -184,6 +184,69 @@ def test_shared_decode_of_many_heads(H, Hkv, d):
     test_decode_shared.check(got, test_decode_shared.reference(x, 0.1, True))
 
 
+# ------------------------------------------------------------------------------ odd values of seen keys
+
+@gpu
+@pytest.mark.parametrize("ctas", [None, 1, 7])
+@pytest.mark.parametrize("nq", [1, 9, 40])
+@pytest.mark.parametrize("d", [64, 128])
+def test_infinities_of_seen_keys_come_out(d, nq, ctas):
+    """V of keys that every query sees holds infinities and a NaN, in the prefix and in own keys: they
+    reach their columns and no other, whatever the number of rows of a tile."""
+    x = test_decode_shared.make([nq, nq], [300, 70], [0, 2], [500], 4, 2, d, nq)
+    at = {("vp", 3): (float("inf"), 5), ("vp", 450): (float("-inf"), 6), ("vp", 260): (float("nan"), 7),
+          ("v", 40): (float("inf"), 8), ("v", 200): (float("-inf"), 9), ("v", 310): (float("inf"), 10)}
+    clean = {n: t.clone() if torch.is_tensor(t) else t for n, t in x.items()}
+    for (name, j), (val, c) in at.items():
+        x[name][j, 1, c] = val
+        clean[name][j, 1, c] = 0.0
+    o, lse = test_decode_shared.run(x, 0.1, False, ctas)
+    fa.fa_device_status()
+    ref = test_decode_shared.reference(clean, 0.1, False)
+    for (name, j), (val, c) in at.items():
+        rows = slice(0, 2 * nq) if name == "vp" else slice(0, nq) if j < 300 else slice(nq, 2 * nq)
+        got = o[rows, 2:, c].float().cpu()  # heads 2, 3 read key/value head 1
+        assert (torch.isnan(got) if val != val else got == val).all(), (name, j)
+        ref[0][rows, 2:, c] = val
+    keep = ~(np.isinf(ref[0]) | np.isnan(ref[0]))
+    got = torch.where(torch.tensor(keep), o.double().cpu(), torch.tensor(0.0, dtype=torch.float64))
+    ref[0][~keep] = 0.0
+    test_decode_shared.check((got, lse), ref)
+
+
+@gpu
+@pytest.mark.parametrize("ctas", [None, 3, 152])
+@pytest.mark.parametrize("d", [64, 128])
+def test_units_of_few_and_many_rows_side_by_side(d, ctas):
+    """Groups whose tiles hold 32 rows, a little more, and several tiles; own keys of one to 33 tokens."""
+    lens_q = [1, 2, 8, 1, 4, 4, 33, 1, 9, 30]
+    lens_k = [200, 1, 130, 0, 127, 129, 40, 1000, 9, 31]
+    x = test_decode_shared.make(lens_q, lens_k, [0, 3, 6, 8, 10], [700, 129, 0, 1500], 8, 2, d, 21)
+    for causal in (False, True):
+        got = test_decode_shared.run(x, 0.1, causal, ctas)
+        fa.fa_device_status()
+        test_decode_shared.check(got, test_decode_shared.reference(x, 0.1, causal))
+
+
+@gpu
+def test_shared_decode_of_one_long_and_many_short_sequences():
+    """Nine single tokens in a group and a sequence of 1100 tokens outside it."""
+    x = test_decode_shared.make([1] * 9 + [1100], [60, 1, 0, 300, 5, 7, 128, 64, 2, 1100], [0, 9], [200], 32, 1, 64, 5)
+    got = test_decode_shared.run(x, 0.1, True)
+    fa.fa_device_status()
+    few = 9
+    part = {n: x[n] for n in ("k", "v", "kp", "vp", "cu_g", "cu_p")}
+    part.update(q=x["q"][:few], cu_q=x["cu_q"][:few + 1], cu_k=x["cu_k"][:few + 1])
+    ref = test_decode_shared.reference(part, 0.1, True)
+    test_decode_shared.check((got[0][:few], got[1][:, :few]), ref)
+    last = x["q"][few:few + 1100]
+    heads = slice(0, 2)
+    tail = dict(q=last[:, heads], k=x["k"][-1100:], v=x["v"][-1100:], kp=x["kp"], vp=x["vp"],
+                cu_q=cu([1100]), cu_k=cu([1100]), cu_g=i32(1, 1), cu_p=i32(0, 200))
+    ref = test_decode_shared.reference(tail, 0.1, True)
+    test_decode_shared.check((got[0][few:, heads], got[1][heads, few:]), ref)
+
+
 # ------------------------------------------------------------------------------ large appends
 
 @gpu
