@@ -3,6 +3,8 @@ of sequences longer than their row of the page table, many key/value heads, call
 make at once, captured work of two streams, tensors that overlap, and what the binding refuses."""
 import ctypes
 import os
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -354,6 +356,83 @@ def test_capture_of_work_that_forks_and_joins():
         for a, b in zip(out, want):
             assert torch.equal(a, b)
     fa.fa_device_status()
+
+
+FIRST_CALLS = """
+import torch, exact_attention_25_gb300 as fa
+i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+q, k = torch.randn(2, 4, 64, device="cuda").bfloat16(), torch.randn(300, 2, 64, device="cuda").bfloat16()
+v, pos, table = torch.randn_like(k), i32(0, 1)[None], fa.rope_table(64, (32,))
+cache, pages = fa.new_cache(10, 64, 2, 64), torch.arange(10, dtype=torch.int32, device="cuda").view(2, 5)
+cu, n, ones, two, p = i32(0, 150, 300), i32(150, 150), i32(0, 1, 2), i32(0, 2), i32(0, 300)
+torch.cuda.synchronize()
+for f in (lambda: fa.rope(q, k[:2].contiguous(), pos, table),
+          lambda: fa.cache_append(cache, k, v, cu, n, pages, 150),
+          lambda: fa.cache_read(cache, cu, pages, 150, 300),
+          lambda: fa.forward_decode_cache(q, cache, ones, n, pages, 1, 150),
+          lambda: fa.forward_decode_shared(q, k, v, k, v, ones, cu, two, p, 1, 150, 2, 300)):
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        r = f()
+    g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(r or (), f() or ()):
+        assert torch.equal(a, b)
+fa.fa_device_status()
+"""
+
+
+@gpu
+def test_first_calls_of_a_process_may_be_captured():
+    """Nothing has run before: the first call of every operator is made inside a capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+# ------------------------------------------------------------------------------ far offsets
+
+@gpu
+def test_pages_more_than_32_bits_into_the_cache():
+    """Sequences whose pages lie at the two ends of a pool of more than 2^32 codes."""
+    Hkv, d, page, H = 8, 128, 64, 16
+    pool = 2 ** 32 // (Hkv * page * d) + 8
+    big = fa.new_cache(pool, page, Hkv, d)
+    assert big.k.numel() > 2 ** 32
+    lens = [150, 200]
+    near = torch.tensor([[0, 1, 2, -1], [3, 4, 5, 6]], dtype=torch.int32)
+    far = torch.tensor([[pool - 1, 0, pool - 2, -1], [pool - 7, pool - 4, 1, pool - 3]], dtype=torch.int32)
+    small = fa.new_cache(7, page, Hkv, d)
+    g = torch.Generator().manual_seed(1)
+    k, v = (torch.randn(350, Hkv, d, generator=g).bfloat16().cuda() for _ in range(2))
+    q = torch.randn(3, H, d, generator=g).bfloat16().cuda()
+    n, got = i32(*lens).cuda(), []
+    for cache, table in ((small, near.cuda()), (big, far.cuda())):
+        fa.cache_append(cache, k, v, cu(lens).cuda(), n, table, 200)
+        back = fa.cache_read(cache, cu(lens).cuda(), table, 200, 350)
+        out = fa.forward_decode_cache(q, cache, i32(0, 1, 3).cuda(), n, table, 2, 200, causal=True)
+        got.append((*back, *out))
+    fa.fa_device_status()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+@gpu
+def test_rope_of_more_than_32_bits_of_elements():
+    """q of more than 2^32 elements, in place: tokens at both ends turn as they do alone."""
+    H, d = 64, 128
+    total = 2 ** 32 // (H * d) + 5
+    q = torch.empty(total, H, d, dtype=torch.bfloat16, device="cuda")
+    ends = torch.tensor([0, 1, total // 2, total - 2, total - 1], device="cuda")
+    part = torch.randn(5, H, d, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    q.zero_()
+    q[ends] = part
+    pos = torch.arange(total, dtype=torch.int32, device="cuda")[None] * 3
+    table = fa.rope_table(d, (64,))
+    fa.fa_rope(q, None, q, None, pos, table)
+    want, _ = fa.rope(part, None, pos[:, ends].contiguous(), table)
+    fa.fa_device_status()
+    assert torch.equal(q[ends], want)
 
 
 # ------------------------------------------------------------------------------ overlap (CPU)
