@@ -1473,8 +1473,8 @@ extern "C" size_t fa_decode_cache_workspace_bytes(int H, int Hkv, int d, int max
         return 0;
     if (num_ctas == 1) return 0;
     const int rc = cache_rows_cta(static_cast<long long>(max_seqlen_q) * (H / Hkv));
-    return cache_part_o_bytes(H, Hkv, d, max_seqlen_q, num_ctas) +
-           align256(static_cast<size_t>(2) * num_ctas * rc * 4) + 256;
+    return cache_part_o_bytes(H, Hkv, d, max_seqlen_q, num_ctas) + align256(static_cast<size_t>(2) * num_ctas * rc * 4) +
+           align256(static_cast<size_t>(num_ctas) * sizeof(int4));
 }
 
 extern "C" int fa_fwd_decode_cache(const void* q, const void* k_cache, const void* v_cache,
@@ -1542,7 +1542,10 @@ extern "C" int fa_fwd_decode_cache(const void* q, const void* k_cache, const voi
     if (need > 0) {
         uint8_t* ws = static_cast<uint8_t*>(workspace);
         p.o_part = reinterpret_cast<float*>(ws);
-        p.lse_part = reinterpret_cast<float*>(ws + cache_part_o_bytes(H, Hkv, d, max_seqlen_q, num_ctas));
+        ws += cache_part_o_bytes(H, Hkv, d, max_seqlen_q, num_ctas);
+        p.lse_part = reinterpret_cast<float*>(ws);
+        const int rows = cache_rows_cta(static_cast<long long>(max_seqlen_q) * (H / Hkv));
+        p.cuts = reinterpret_cast<int4*>(ws + align256(static_cast<size_t>(2) * num_ctas * rows * 4));
     }
     p.ke = static_cast<const uint8_t*>(k_exp);
     p.ve = static_cast<const uint8_t*>(v_exp);

@@ -154,6 +154,14 @@ struct Unit {
 };
 constexpr int kFirst = 1;
 
+// What the merge needs of a unit that is cut, as CacheDecodeParams::cuts holds it: first token, first query
+// row, key/value head, and in one word the query rows (at most 64), whether the first part is its share's
+// second, and the parts (at most 4096).  No rows: the share's end cuts no unit that begins in it.
+__device__ __forceinline__ int4 pack_cut(const Unit& u, int rows, int lead, int parts)
+{
+    return make_int4(u.q0, u.row0, u.hk, rows | lead << 7 | parts << 8);
+}
+
 // Sizes of sequence b: units (row sets times heads) of nblk blocks each.
 __device__ __forceinline__ void sequence_work(const CacheDecodeParams& p, int b, Unit& u)
 {
@@ -260,6 +268,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
         }
         bool ok = true;
         int it = 0, k = 0;                                    // blocks through the ring, units so far
+        bool cut = false;                                     // the share's end cuts a unit that begins here
         while (ok && left > 0) {
             unit_at(p, ui, un);
             const int end = min(un.nblk + kUnitCost, place + left);
@@ -267,6 +276,12 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
             un.jb = max(0, place - kUnitCost);
             un.J = max(0, end - kUnitCost) - un.jb;
             un.flags = k == 0 ? kFirst : 0;
+            if (left == 0 && un.jb == 0 && un.J > 0 && un.J < un.nblk) {
+                const int last = sh.share_of(sh.start(cta + 1) - un.J + un.nblk - 1);
+                if (lane == 0)
+                    p.cuts[cta] = pack_cut(un, min(un.nq * p.G.d - un.row0, p.rows_cta), k == 0 ? 0 : 1, last - cta + 1);
+                cut = true;
+            }
             // page ids base + lane; the first ones are on their way before anything else is done
             int base = (un.jb * kKB) >> p.page_shift, ids = -1;
             auto load_ids = [&]() {
@@ -338,6 +353,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
                 }
             }
         }
+        if (!cut && lane == 0 && p.cuts != nullptr) p.cuts[cta] = make_int4(0, 0, 0, 0);
         // the end of the units
         if (ok && lane == 0) {
             s_unit[k % kUnits].J = 0;
@@ -797,48 +813,29 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
     }
 }
 
-// Merge of the parts of every unit that several shares cut: CTA c takes the unit that the border
-// between shares c and c + 1 cuts, if that is the unit's first cut; a warp takes a query row.  A row
-// that saw no key in any part gets O = 0, lse = -inf.
-// It is always launched behind the attention kernel of its call, whose CTAs let it start only after
-// their own wait: so the lengths, which that wait has made visible, are read before this kernel's.
+// Merge of the parts of every unit that several shares cut: CTA c takes the unit that begins in share c and
+// goes on in the next, if there is one; a warp takes a query row.  A row that saw no key in any part gets
+// O = 0, lse = -inf.  The attention CTAs leave the units' descriptions beside the parts: worked out here again,
+// from the lengths, they would cost every CTA a scan behind its wait (ahead of it nothing may be read).
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) fa_decode_cache_merge_kernel(const CacheDecodeParams p)
 {
     constexpr int EPL = D / 32;
     const int lane = threadIdx.x & 31;
     const int c0 = static_cast<int>(blockIdx.x);
-    Unit u;
-    int at = 0;
-    // the first place of share c0 + 1
-    const Shares sh = find_share(p, c0 + 1, u, at);
-    const int border = sh.start(c0 + 1);
-    const bool cut = border < sh.total;
-    const int ui = cut ? at / (u.nblk + kUnitCost) : 0;
-    const int j = cut ? at - ui * (u.nblk + kUnitCost) : 0;
-    const int start = border - j + kUnitCost;  // the place of the unit's first block
-    // not cut here (no border between two of the unit's blocks), or cut before (share c0 starts
-    // inside them): every CTA waits all the same, so that this grid ends after the attention
-    if (!cut || j <= kUnitCost || sh.start(c0) > start) {
-        dependent_begin();
-        return;
-    }
-    unit_at(p, ui, u);
-    const int c1 = sh.share_of(start + u.nblk - 1);  // the last share in it
-    const int rows = min(u.nq * p.G.d - u.row0, p.rows_cta);
-    const int parts = c1 - c0 + 1;
-    // share c0's part is its last unit, which is also its first if the share starts in its places
-    const int lead = sh.start(c0) >= start - kUnitCost ? 0 : 1;
     dependent_begin();
+    const int4 cut = p.cuts[c0];
+    const int q0 = cut.x, row0 = cut.y, hk = cut.z;
+    const int rows = cut.w & 127, lead = cut.w >> 7 & 1, parts = cut.w >> 8;
     const int r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);
     if (r < rows) {
         float mx, sum, acc[EPL];
         merge_parts<D, 16>(
             parts, [&](int k) { return (2 * (c0 + k) + (k == 0 ? lead : 0)) * p.rows_cta + r; },
             p.o_part, p.lse_part, p.part_ext / D, p.status, mx, sum, acc);
-        const int i = p.G(u.row0 + r), h = u.hk * p.G.d + (u.row0 + r) - i * p.G.d;
-        const long long row = (static_cast<long long>(u.q0 + i) * p.H + h) * D + EPL * lane;
-        const long long stat = static_cast<long long>(h) * p.total_q + u.q0 + i;
+        const int i = p.G(row0 + r), h = hk * p.G.d + (row0 + r) - i * p.G.d;
+        const long long row = (static_cast<long long>(q0 + i) * p.H + h) * D + EPL * lane;
+        const long long stat = static_cast<long long>(h) * p.total_q + q0 + i;
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         if (in_extent(row, EPL, p.q_ext, p.status)) {
             if constexpr (EPL == 4)

@@ -89,13 +89,15 @@ constexpr int kSharedUnitCost = 3;  // shared prefixes (64 over one of 32000: 62
 // every `rows_cta` query rows of a group and every key/value head, kUnitCost places and one place
 // for each 128-key block of the sequence (at least one).  The CTAs take equal shares of that line
 // (to a place), however ragged the lengths are.  A unit whose blocks lie in one share is finished
-// by its CTA; one that several shares cut is written in parts, and merged by the next kernel.
+// by its CTA; one that several shares cut is written in parts, and merged by the next kernel, for
+// which the CTA with the unit's first block describes it (cuts).
 struct CacheDecodeParams {
     const __nv_bfloat16* q;    // [total_q, H, d]
     __nv_bfloat16* o;
     float* lse;                // [H, total_q] (may be null)
     float* o_part;             // workspace: fp32 [2 * ctas, rows_cta, d]; a share's first unit is
     float* lse_part;           // its part 2 c, its last (if another) 2 c + 1; [2 * ctas, rows_cta]
+    int4* cuts;                // workspace [ctas]: the unit that begins in share c and goes on in the next
     const uint8_t* ke;
     const uint8_t* ve;
     const int* cu_q;           // [B + 1]
