@@ -1607,7 +1607,7 @@ extern "C" size_t fa_decode_shared_workspace_bytes(int total_q, int H, int d, in
 {
     if (total_q < 1 || H < 1 || (d != 64 && d != 128) || num_ctas < 1 || num_ctas > kSharedMaxCtas) return 0;
     const size_t rows = shared_rows(total_q, H, num_ctas);
-    return align256(rows * d * 4) + align256(rows * 4);
+    return align256(rows * d * 4) + align256(rows * 4) + align256(static_cast<size_t>(total_q) * 2 * sizeof(int4));
 }
 
 extern "C" int fa_decode_shared_num_ctas(void)
@@ -1680,6 +1680,7 @@ extern "C" int fa_fwd_decode_shared(const void* q, const void* k_prefix, const v
     p.o_part = reinterpret_cast<float*>(ws);
     p.lse_part = reinterpret_cast<float*>(ws + align256(rows * d * 4));
     p.part_row0 = 2LL * total_q * H;
+    p.places = reinterpret_cast<int4*>(ws + align256(rows * d * 4) + align256(rows * 4));
     p.v = static_cast<const __nv_bfloat16*>(v);
     p.cu_q = cu_seqlens_q; p.cu_k = cu_seqlens_k; p.cu_g = cu_groups; p.cu_p = cu_seqlens_p;
     p.B = B; p.groups = num_groups; p.H = H; p.Hkv = Hkv; p.G = fa::FastDiv(G);

@@ -89,21 +89,48 @@ __device__ __forceinline__ int shared_places(const SharedDecodeParams& p, int x)
     return u.in_item * (u.nblk + kSharedUnitCost);
 }
 
-// All lanes of a warp of the merge kernel: the line's length, and the places of the items before x[0] and x[1].
-__device__ __forceinline__ int count_places(const SharedDecodeParams& p, const int* x, int* before)
+// What the merge has to know of tokens [t0, t1), by a warp: for its own keys (the first of two entries) and for
+// its group's prefix, the places of the line before the item, the item's blocks (0: no keys) and the token's
+// index in it (-1: in no sequence); and the line's length.
+__device__ __noinline__ void place_tokens(const SharedDecodeParams& p, int t0, int t1)
 {
-    const int items = p.groups + p.B;
-    int sum = 0, b0 = 0, b1 = 0;
-#pragma unroll 1
-    for (int i = threadIdx.x & 31; i < items; i += 32) {
-        const int w = shared_places(p, i);
-        sum += w;
-        b0 += i < x[0] ? w : 0;
-        b1 += i < x[1] ? w : 0;
+    const int lane = threadIdx.x & 31, items = p.groups + p.B;
+    for (int t = t0 + lane; t < t1; t += 32) {
+        p.places[2ll * t] = make_int4(0, 0, -1, 0);
+        p.places[2ll * t + 1] = make_int4(0, 0, 0, 0);
     }
-    before[0] = __reduce_add_sync(0xffffffffu, b0);
-    before[1] = __reduce_add_sync(0xffffffffu, b1);
-    return __reduce_add_sync(0xffffffffu, sum);
+    __syncwarp();
+    int run = 0;
+#pragma unroll 1
+    for (int x0 = 0; x0 < items; x0 += 32) {
+        SharedUnit u;
+        int w = 0, a = 0, b = 0;
+        u.tok0 = u.nblk = 0;
+        if (x0 + lane < items) {
+            shared_item(p, x0 + lane, u);
+            w = u.in_item * (u.nblk + kSharedUnitCost);
+            a = max(t0, u.tok0);
+            b = min(t1, u.tok0 + u.ntok);
+        }
+        int sum = w;
+#pragma unroll
+        for (int d = 1; d < 32; d *= 2) {
+            const int up = __shfl_up_sync(0xffffffffu, sum, d);
+            if (lane >= d) sum += up;
+        }
+        uint32_t mine = __ballot_sync(0xffffffffu, a < b);  // items with some of the tokens
+        while (mine) {
+            const int src = __ffs(mine) - 1;
+            mine &= mine - 1;
+            const int before = run + __shfl_sync(0xffffffffu, sum - w, src), nblk = __shfl_sync(0xffffffffu, u.nblk, src);
+            const int tok0 = __shfl_sync(0xffffffffu, u.tok0, src), end = __shfl_sync(0xffffffffu, b, src);
+            for (int t = __shfl_sync(0xffffffffu, a, src) + lane; t < end; t += 32)
+                p.places[2ll * t + (x0 + src < p.groups)] = make_int4(before, nblk, t - tok0, 0);
+            __syncwarp();  // (starts that do not rise may give a token to several items: the last one has it)
+        }
+        run += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    for (int t = t0 + lane; t < t1; t += 32) p.places[2ll * t].w = run;
 }
 
 // Two bf16 values, infinities and NaNs replaced by zero.
@@ -458,6 +485,10 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
         const float c2 = p.scale_log2;
         const bool prescale = !(c2 > 0.0f);
         const float cf = prescale ? 1.0f : c2;
+        if (warp == 0) {  // (while the first copies are on their way)
+            const int per = (p.total_q + p.ctas - 1) / p.ctas, t0 = cta * per;
+            if (t0 < p.total_q) place_tokens(p, t0, min(t0 + per, p.total_q));
+        }
         bool ok = true;
         int n = 0;
         for (int k = 0; ok; ++k) {
@@ -701,63 +732,40 @@ __global__ void __launch_bounds__(SharedCfg<D>::THREADS, 1)
 
 // Merge: one warp for each query row (token and head) gathers the row's parts, those of its
 // group's prefix and those of its sequence's keys.  A row that saw no key in any gets O = 0, lse = -inf.
-// It is always launched behind the attention kernel of its call, whose CTAs let it start only after
-// their own wait: so the lengths, which that wait has made visible, are read before this kernel's.
+// The attention CTAs leave beside the parts where each token's lie: ahead of its wait the kernel may read no
+// lengths, and a scan of them behind it would cost every warp several round trips.
 template <int D, int BATCH>
 __global__ void __launch_bounds__(128) fa_decode_shared_merge_kernel(const SharedDecodeParams p)
 {
     constexpr int EPL = D / 32;
     const int lane = threadIdx.x & 31;
     const int w = static_cast<int>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    const int h = w % p.H;
-    const int i = w / p.H % p.max_q, b = w / p.H / p.max_q;
-    SharedUnit u[2];  // its group's prefix, its own keys
-    int count[2] = {0, 0}, c0[2], lead[2];
-    int row[2] = {0, 0};
-    bool here = b < p.B, whole[2] = {false, false};
-    int tok = 0;
-    if (here) {
-        shared_item(p, p.groups + b, u[1]);
-        tok = u[1].tok0 + i;
-        here = i < u[1].ntok;
-    }
-    if (here) {
-        int x = 0;  // the group: groups are runs of sequences
-        u[0].in_item = 0;
-#pragma unroll 1
-        for (int g0 = 0; g0 < p.groups; g0 += 32) {
-            const bool in = g0 + lane < p.groups && p.cu_g[g0 + lane] <= b &&
-                            b < p.cu_g[g0 + lane + 1];
-            const uint32_t some = __ballot_sync(0xffffffffu, in);
-            if (some) {
-                x = g0 + __ffs(some) - 1;
-                shared_item(p, x, u[0]);
-                break;
-            }
-        }
-        const int items[2] = {x, p.groups + b};
-        int before[2];
-        const int all = count_places(p, items, before);
-        const int hk = p.G(h), hg = hk % p.head_groups, hj = hk / p.head_groups;
-        const int nh = (p.Hkv - hg + p.head_groups - 1) / p.head_groups;
-        const Shares sh(all * nh, p.parts);
-#pragma unroll
-        for (int z = 0; z < 2; ++z) {
-            const int ti = tok - u[z].tok0;
-            if (u[z].in_item == 0 || ti < 0 || ti >= u[z].ntok) continue;
-            const int tile = p.tile_tokens(ti);
-            const int start = before[z] * nh + (tile * nh + hj) * (u[z].nblk + kSharedUnitCost) + kSharedUnitCost;
-            const int s0 = sh.share_of(start), s1 = sh.share_of(start + u[z].nblk - 1);
-            c0[z] = s0 * p.head_groups + hg;
-            count[z] = s1 - s0 + 1;
-            whole[z] = s1 == s0;
-            lead[z] = sh.start(s0) >= start - kSharedUnitCost ? 0 : 1;
-            row[z] = whole[z] ? ((z ? p.total_q : 0) + tok) * p.H + h
-                              : static_cast<int>(p.part_row0) + (ti - tile * p.tile_tokens.d) * p.G.d + (h - hk * p.G.d);
-        }
-    }
+    const int tok = w / p.H, h = w - tok * p.H;
+    const int hk = p.G(h), hg = hk % p.head_groups, hj = hk / p.head_groups;
+    const int nh = (p.Hkv - hg + p.head_groups - 1) / p.head_groups;
     dependent_begin();
-    if (!here) return;
+    if (tok >= p.total_q) return;
+    int4 at[2];  // its group's prefix, its own keys
+    at[0] = p.places[2ll * tok + 1];
+    at[1] = p.places[2ll * tok];
+    if (at[1].z < 0) return;
+    const Shares sh(at[1].w * nh, p.parts);
+    int count[2] = {0, 0}, c0[2], lead[2], row[2] = {0, 0};
+    bool whole[2] = {false, false};
+#pragma unroll
+    for (int z = 0; z < 2; ++z) {
+        const int nblk = at[z].y, ti = at[z].z;
+        if (nblk == 0) continue;
+        const int tile = p.tile_tokens(ti);
+        const int start = at[z].x * nh + (tile * nh + hj) * (nblk + kSharedUnitCost) + kSharedUnitCost;
+        const int s0 = sh.share_of(start), s1 = sh.share_of(start + nblk - 1);
+        c0[z] = s0 * p.head_groups + hg;
+        count[z] = s1 - s0 + 1;
+        whole[z] = s1 == s0;
+        lead[z] = sh.start(s0) >= start - kSharedUnitCost ? 0 : 1;
+        row[z] = whole[z] ? ((z ? p.total_q : 0) + tok) * p.H + h
+                          : static_cast<int>(p.part_row0) + (ti - tile * p.tile_tokens.d) * p.G.d + (h - hk * p.G.d);
+    }
     float mx, sum, acc[EPL];
     merge_parts<D, BATCH>(
         count[0] + count[1],
@@ -803,7 +811,7 @@ static cudaError_t launch_decode_shared_impl(const CUtensorMap* maps, const Shar
     // The merge's CTAs start beside the attention's and wait there; with few rows they all fit with 16
     // parts in flight each (8 queries: 12.2 us, 12.7 with 8), with many only with 8 (64 queries: 61.7 us,
     // with 16 a second wave starts late, 65.4).
-    const long long rows = static_cast<long long>(p.B) * p.max_q * p.H;
+    const long long rows = static_cast<long long>(p.total_q) * p.H;
     const dim3 grid(static_cast<unsigned>((rows + 3) / 4));
     return rows <= 8ll * num_sms
                ? launch_dependent(fa_decode_shared_merge_kernel<D, 16>, grid, dim3(128), 0, st, p)

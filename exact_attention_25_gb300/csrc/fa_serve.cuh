@@ -134,6 +134,7 @@ struct SharedDecodeParams {
     float* o_part;
     float* lse_part;
     long long part_row0;
+    int4* places;              // workspace [total_q][2]: where the merge finds a token's parts (place_tokens)
     const __nv_bfloat16* v;    // [total_k, Hkv, d] (read for infinities and NaNs only)
     const int* cu_q;           // [B + 1]
     const int* cu_k;           // [B + 1]

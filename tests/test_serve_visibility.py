@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import exact_attention_25_gb300 as fa
-from tests import test_decode_cache
+from tests import test_decode_cache, test_decode_shared
 from tests.test_cache import cu, table_for
 from tests.test_launch_order import Kernel
 from tests.test_serve_protocol import append, host, rope
@@ -83,7 +83,7 @@ def test_every_serving_kernel_is_looked_at():
         assert len(list(kernels(name))) == n, name
 
 
-@pytest.mark.parametrize("name", ["fa_rope.cu", "fa_cache.cu", "fa_decode_cache.cu"])
+@pytest.mark.parametrize("name", list(SOURCES))
 def test_nothing_is_read_ahead_of_the_wait(name):
     for kernel, body in kernels(name):
         wait = body.index("dependent_begin()")
@@ -133,3 +133,47 @@ def test_cut_units_of_a_growing_cache(d, H, Hkv, nq, graph):
         assert torch.equal(lens, first + (i + 1) * grow)
         ref = test_decode_cache.reference(q.cpu(), codes, exps, table, [nq] * B, lens.tolist(), H, page, 0.1, True)
         test_decode_cache._check((a, b), ref, f"step {i}")
+
+
+@gpu
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("d, H, Hkv, nq", [(128, 8, 2, 1), (64, 12, 3, 5), (128, 64, 1, 4)])
+def test_cut_units_of_growing_prefixes_and_keys(d, H, Hkv, nq, graph):
+    """The same for the decode with shared prefixes: prefixes, own keys and the borders of the groups
+    move from step to step; every step against attention in 64 bits."""
+    B, ctas, steps, total = 5, 17, 5, 4000
+    lens_q = [nq] * B
+    x = test_decode_shared.make(lens_q, [total // B] * B, [0, 2, B], [1500, 1500], H, Hkv, d, d + H)
+    dev = {n: t.cuda() for n, t in x.items() if n != "sizes"}
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32).cuda()  # noqa: E731
+    state = [i32(0, 10, 20, 250, 260, 300), i32(0, 130, 900), i32(0, 1, 5)]     # cu_k, cu_p, cu_g
+    grow = [i32(0, 129, 140, 400, 401, 700), i32(0, 270, 390), i32(0, 1, 0)]
+    first = [t.clone() for t in state]
+    o, lse = torch.empty_like(dev["q"]), torch.empty(H, B * nq, device="cuda")
+    ws = torch.empty(fa.fa_decode_shared_workspace_bytes(B * nq, H, d, ctas), dtype=torch.uint8).cuda()
+
+    def one():
+        for t, by in zip(state, grow):
+            t.add_(by)
+        state[2].remainder_(6)
+        fa.fa_fwd_decode_shared(dev["q"], dev["kp"], dev["vp"], dev["k"], dev["v"], o, lse, dev["cu_q"], state[0],
+                                state[2], state[1], nq, 3000, B * nq, 2000, 0.1, True, ctas, ws)
+
+    one()
+    for t, was in zip(state, first):
+        t.copy_(was)
+    run = one
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            one()
+        run = g.replay
+    got = []
+    for _ in range(steps):
+        run()
+        got.append([t.clone() for t in state + [o, lse]])
+    torch.cuda.synchronize()
+    fa.fa_device_status()
+    for i, (ck, cp, cg, a, b) in enumerate(got):
+        part = dict(x, cu_k=ck.cpu(), cu_p=cp.cpu(), cu_g=cg.cpu())
+        test_decode_shared.check((a, b), test_decode_shared.reference(part, 0.1, True), f"step {i}")
