@@ -496,6 +496,9 @@ class RopeTable:
         self._args = (ctypes.addressof(self._freq), ctypes.addressof(self._axis), self.axes,
                       self.d, self.pairs, self.interleaved)
 
+    def __reduce__(self):  # copies and pickles make arrays, and addresses, of their own
+        return RopeTable, (self.d, self.inv_freq, self.axis, self.interleaved)
+
 
 def rope_table(d: int, sections, base: float = 10000.0, per_axis: bool = False,
                interleaved: bool = False) -> RopeTable:
