@@ -367,6 +367,7 @@ struct DecodeOut {
         o = a.optional();
         lse = a.optional();
         ws = a.optional();
+        if (ws && !ws->is_contiguous()) value_error("the workspace must be contiguous");
     }
     // without o everything is allocated, `bytes` of workspace
     void make(const at::Tensor& q, const Device& dev, size_t bytes)

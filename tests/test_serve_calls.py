@@ -55,3 +55,24 @@ def test_a_copied_module_keeps_its_table():
     del m
     gc.collect()
     assert behind(n.table) == (n.table.inv_freq, n.table.axis)
+
+
+# ------------------------------------------------------------------------------ workspaces that are views
+
+i32 = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
+
+
+@pytest.mark.parametrize("call", ["cache", "shared"])
+def test_a_workspace_with_gaps_is_refused(call):
+    """The kernels write the workspace as one run of bytes: a view with gaps would have what lies in them
+    overwritten."""
+    ws = torch.zeros(64, 2, 1024, dtype=torch.uint8)[:, 0]
+    assert not ws.is_contiguous()
+    q, kv = torch.zeros(2, 4, 64).bfloat16(), torch.zeros(9, 2, 64).bfloat16()
+    with pytest.raises(ValueError, match="workspace"):
+        if call == "cache":
+            fa.fa_fwd_decode_cache(q, fa.new_cache(2, 16, 2, 64, device="cpu"), q.clone(), None, i32(0, 1, 2),
+                                   i32(3, 4), torch.zeros(2, 1, dtype=torch.int32), 1, 9, 0.1, False, 2, ws)
+        else:
+            fa.fa_fwd_decode_shared(q, kv, kv, kv, kv, q.clone(), None, i32(0, 1, 2), i32(0, 4, 9), i32(0, 2),
+                                    i32(0, 9), 1, 5, 2, 9, 0.1, False, 2, ws)
