@@ -691,7 +691,8 @@ def fa_fwd_decode_shared(q, k_prefix, v_prefix, k, v, o, lse, cu_seqlens_q, cu_s
                          num_ctas: int, workspace, stream=None) -> None:
     """C ``fa_fwd_decode_shared``: q, o [total_q, H, d]; k_prefix, v_prefix [total_p, Hkv, d];
     k, v [total_k, Hkv, d] (bf16); lse [H, total_q] fp32 or None; cu_seqlens_q, cu_seqlens_k
-    int32 [B + 1]; cu_groups (first sequence of each group), cu_seqlens_p int32 [groups + 1]."""
+    int32 [B + 1]; cu_groups (first sequence of each group), cu_seqlens_p int32 [groups + 1].  A batch
+    without own keys, or without prefixes, has tensors of no rows there."""
     if o is None:
         raise ValueError("o must be given")
     if num_ctas < 1:

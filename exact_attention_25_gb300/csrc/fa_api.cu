@@ -1627,6 +1627,17 @@ extern "C" int fa_fwd_decode_shared(const void* q, const void* k_prefix, const v
                                     int num_ctas, void* workspace, size_t workspace_bytes,
                                     void* stream)
 {
+    // Batches without own keys or without prefixes: no unit reads these tensors, so any row will do for
+    // the tensor maps, and the kernels find no keys in totals of zero.
+    const bool no_own = total_k == 0 && max_seqlen_k == 0, no_prefix = total_p == 0 && max_seqlen_p == 0;
+    if (no_own) {
+        k = v = q;
+        total_k = max_seqlen_k = 1;
+    }
+    if (no_prefix) {
+        k_prefix = v_prefix = q;
+        total_p = max_seqlen_p = 1;
+    }
     if (int rc = check_varlen(cu_seqlens_q, cu_seqlens_k, B, &max_seqlen_q, &max_seqlen_k, total_q,
                               total_k, H, Hkv, d, scale, causal))
         return rc;
@@ -1661,7 +1672,7 @@ extern "C" int fa_fwd_decode_shared(const void* q, const void* k_prefix, const v
         return fail(FA_ERR_WORKSPACE, "workspace must hold " + std::to_string(need) + " bytes");
     if (!aligned16(workspace)) return fail(FA_ERR_MISALIGNED, "workspace must be 16-byte aligned");
     {
-        const size_t row = static_cast<size_t>(Hkv) * d * 2;
+        const size_t row = static_cast<size_t>(Hkv) * d * 2;  // (where q stands in, its first row is part of it)
         const Span out[3] = {{o, static_cast<size_t>(total_q) * H * d * 2},
                              {lse, lse ? static_cast<size_t>(total_q) * H * 4 : 0}, {workspace, need}};
         const Span in[9] = {{q, out[0].n}, {k_prefix, total_p * row}, {v_prefix, total_p * row}, {k, total_k * row},
@@ -1685,7 +1696,7 @@ extern "C" int fa_fwd_decode_shared(const void* q, const void* k_prefix, const v
     p.cu_q = cu_seqlens_q; p.cu_k = cu_seqlens_k; p.cu_g = cu_groups; p.cu_p = cu_seqlens_p;
     p.B = B; p.groups = num_groups; p.H = H; p.Hkv = Hkv; p.G = fa::FastDiv(G);
     p.max_q = max_seqlen_q; p.max_k = max_seqlen_k; p.max_group_q = max_group_q; p.max_p = max_seqlen_p;
-    p.total_q = total_q; p.total_k = total_k; p.total_p = total_p;
+    p.total_q = total_q; p.total_k = no_own ? 0 : total_k; p.total_p = no_prefix ? 0 : total_p;
     p.tile_tokens = fa::FastDiv(tok);
     p.ctas = num_ctas;
     p.head_groups = shared_head_groups(Hkv, num_ctas);

@@ -441,7 +441,10 @@ PyObject* decode_shared(Args a)
     DecodeOut out;
     out.read(a);
     const at::Tensor &cq = a.tensor(), &ck = a.tensor(), &cg = a.tensor(), &cp = a.tensor();
-    const int mq = a.int32(), mk = a.int32(), mg = a.int32(), mp = a.int32();
+    const int mq = a.int32();
+    int mk = a.int32();
+    const int mg = a.int32();
+    int mp = a.int32();
     const float scale = static_cast<float>(a.real());
     const int causal = a.truth();
     int ctas = a.int32();
@@ -464,6 +467,10 @@ PyObject* decode_shared(Args a)
     int32s(cp, "cu_seqlens_p", cg.size(0));
     for (const at::Tensor* t : {&cq, &ck, &cg, &cp}) dev.same(*t);
     const int H = size32(q.size(1)), total_q = size32(q.size(0));
+    // no rows, or none that count: the call takes both numbers as 0
+    int total_k = size32(k.size(0)), total_p = size32(kp.size(0));
+    if (total_k == 0 || mk == 0) total_k = mk = 0;
+    if (total_p == 0 || mp == 0) total_p = mp = 0;
     const c10::cuda::CUDAGuard guard(dev.cuda());
     if (ctas == 0) ctas = ctas_fn();
     if (ctas < 0) return PyLong_FromLong(ctas);
@@ -471,8 +478,8 @@ PyObject* decode_shared(Args a)
     const int rc = fn(q.data_ptr(), kp.data_ptr(), vp.data_ptr(), k.data_ptr(), v.data_ptr(), out.o->data_ptr(),
                       static_cast<float*>(at_(out.lse)), cq.data_ptr<int>(), ck.data_ptr<int>(),
                       cg.data_ptr<int>(), cp.data_ptr<int>(), size32(cq.size(0)) - 1, size32(cg.size(0)) - 1, mq,
-                      mk, mg, mp, total_q, size32(k.size(0)), size32(kp.size(0)), H, size32(Hkv), size32(d),
-                      scale, causal, ctas, at_(out.ws), out.ws_bytes(), raw_stream(dev));
+                      mk, mg, mp, total_q, total_k, total_p, H, size32(Hkv), size32(d), scale, causal, ctas,
+                      at_(out.ws), out.ws_bytes(), raw_stream(dev));
     if (rc) return PyLong_FromLong(rc);
     return two(*out.o, out.lse);
 }

@@ -454,10 +454,12 @@ int fa_decode_cache_ctas_for(int B, int H, int Hkv, int max_seqlen_q, int max_se
  * every query sees the whole prefix of its group and, under one softmax, its sequence's own keys
  * (those bottom-right causal among themselves when causal = 1).
  *   - k, v [total_k, Hkv, d]: the sequences' own keys, cu_seqlens_q / cu_seqlens_k as
- *     fa_fwd_varlen; sequences may have none.
+ *     fa_fwd_varlen; sequences may have none.  Where none has any, total_k and max_seqlen_k may both be
+ *     0, and k and v NULL.
  *   - k_prefix, v_prefix [total_p, Hkv, d]: the prefixes back to back, cu_seqlens_p (device int32
  *     [num_groups + 1]); group g has the sequences [cu_groups[g], cu_groups[g + 1]) (device int32
- *     [num_groups + 1], rising).  A sequence in no group sees only its own keys.
+ *     [num_groups + 1], rising).  A sequence in no group sees only its own keys.  Where every prefix is
+ *     empty, total_p and max_seqlen_p may both be 0, and k_prefix and v_prefix NULL.
  *   - max_group_q: the most queries of a group; max_seqlen_p: the longest prefix.
  * A prefix is read once for every 128 / (H / Hkv) tokens of its group, instead of once a sequence.
  * The batch's blocks of 128 keys are shared out evenly over num_ctas thread blocks (in [1, 1024];

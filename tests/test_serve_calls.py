@@ -76,3 +76,51 @@ def test_a_workspace_with_gaps_is_refused(call):
         else:
             fa.fa_fwd_decode_shared(q, kv, kv, kv, kv, q.clone(), None, i32(0, 1, 2), i32(0, 4, 9), i32(0, 2),
                                     i32(0, 9), 1, 5, 2, 9, 0.1, False, 2, ws)
+
+
+# ------------------------------------------------------------------------------ no own keys, no prefixes
+
+@pytest.fixture(scope="module")
+def lib():
+    from exact_attention_25_gb300 import _lib, build
+
+    build.build()
+    return _lib.load(_lib.LIB_PATH)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="calls with dummy pointers that pass every check")
+@pytest.mark.parametrize("kw", [dict(tk=0, mk=0, k=0, v=0), dict(tp=0, mp=0, kp=0, vp=0), dict(tk=0, mk=0, k=0x60008),
+                                dict(tk=0, mk=0, tp=0, mp=0, k=0, v=0, kp=0, vp=0)])
+def test_shared_decode_takes_no_own_keys_or_no_prefixes(lib, kw):
+    a = dict(q=0x10000, kp=0x20000, vp=0x30000, k=0x40000, v=0x50000, o=0x60000, lse=0x70000, mk=10, mp=100, tk=20,
+             tp=100)
+    a.update(kw)
+    vp = ctypes.c_void_p
+    rc = lib.fa_fwd_decode_shared(
+        *(vp(a[n]) for n in ("q", "kp", "vp", "k", "v", "o", "lse")), vp(0x90000), vp(0x91000), vp(0x92000),
+        vp(0x93000), 2, 1, 1, a["mk"], 2, a["mp"], 2, a["tk"], a["tp"], 4, 2, 64, ctypes.c_float(0.1), 0, 2,
+        vp(0xA0000), 1 << 30, None)
+    assert rc == -5, lib.fa_last_error()  # every check passed: only the device is missing
+
+
+@gpu
+@pytest.mark.parametrize("most", [0, 7])
+@pytest.mark.parametrize("d, H, Hkv", [(64, 4, 1), (128, 16, 8)])
+@pytest.mark.parametrize("none", ["own", "prefix", "either"])
+def test_shared_decode_of_empty_tensors(none, d, H, Hkv, most):
+    """Own keys, prefixes or both are tensors of no rows (`most`: the longest, as the caller has it); or
+    tensors with rows of which the longest sequence takes none."""
+    from tests import test_decode_shared as t
+
+    lens_q, own, prefix = [1, 3, 2], [5, 130, 40], [300, 17]
+    own = [0] * 3 if none != "prefix" else own
+    prefix = [0] * 2 if none != "own" else prefix
+    x = t.make(lens_q, own, [0, 2, 3], prefix, H, Hkv, d, d, behind=float("nan"))
+    if most:
+        x.update({n: x[n][:-40] for n in ("k", "v", "kp", "vp")})  # as the sequences have them: perhaps no rows
+    mq, mk, mg, mp = x["sizes"]
+    x["sizes"] = (mq, mk if any(own) else most, mg, mp if any(prefix) else most)
+    for causal in (False, True):
+        got = t.run(x, 0.1, causal)
+        fa.fa_device_status()
+        t.check(got, t.reference(x, 0.1, causal))
