@@ -433,7 +433,9 @@ def forward_decode(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int, max_s
 # Made once for every token and layer of a decode, so their host side is native (the _serve module,
 # csrc/serve_binding.cpp): it checks the tensors, allocates what is to be returned, and makes the C
 # call on the tensors' device and its current stream.  A call on another stream makes that the
-# current one first, so torch's allocator ties outputs and workspaces to it.
+# current one first, so torch's allocator ties outputs and workspaces to it.  A step in which no sequence has
+# a row (a total, or the longest sequence's number, of 0) does nothing and returns what it was given, or
+# tensors that nothing is written to.
 
 @functools.lru_cache(maxsize=None)
 def _native():

@@ -2,7 +2,8 @@
 // over shared prefixes).  They are made once per token and layer, where a kernel takes a few
 // microseconds, so their host side is compiled: argument checks, output allocation by torch's
 // allocator and the C call of include/fa.h take about a third of what the same steps cost in Python.
-// Nothing is computed here.  Every function takes the address of its C entry point first (the caller
+// Nothing is computed here.  A call without rows, or whose longest sequence has none, returns without
+// launching anything (the C entry points take sizes from 1 on).  Every function takes the address of its C entry point first (the caller
 // chooses the library) and returns the outputs, or the int code of a refused call.
 #include <Python.h>
 
@@ -274,6 +275,7 @@ PyObject* rope(Args a)
         value_error("outputs must have their inputs' shape and dtype");
     dev.same(*qo);
     if (ko) dev.same(*ko);
+    if (total == 0) return two(*qo, ko);
     Strides st;
     for (const at::Tensor* t : {&q, k, qo, ko}) st.add(t);
     const int rc = fn(q.data_ptr(), at_(k), qo->data_ptr(), at_(ko), pos.data_ptr<int>(), freq, axis,
@@ -310,6 +312,7 @@ PyObject* cache_append(Args a)
     st.add(&k);
     st.add(&v);
     const c10::cuda::CUDAGuard guard(dev.cuda());
+    if (k.size(0) == 0 || most == 0) return none();
     const int rc = fn(k.data_ptr(), v.data_ptr(), st.get(), c.k->data_ptr(), c.v->data_ptr(), c.ke->data_ptr(),
                       c.ve->data_ptr(), cu.data_ptr<int>(), n.data_ptr<int>(), table.data_ptr<int>(), c.B,
                       most, size32(k.size(0)), c.max_pages, c.pages, c.page, c.Hkv, c.d, dt, raw_stream(dev));
@@ -348,6 +351,7 @@ PyObject* cache_read(Args a)
     dev.same(*k);
     dev.same(*v);
     const int dt = dtype_of(*k);
+    if (k->size(0) == 0 || most == 0) return two(*k, v);
     Strides st;
     st.add(k);
     st.add(v);
@@ -388,6 +392,12 @@ struct DecodeOut {
         if (ws) dev.same(*ws);
     }
     size_t ws_bytes() const { return ws ? ws->nbytes() : 0; }
+    // the result of a call without queries
+    PyObject* nothing(const at::Tensor& q, const Device& dev)
+    {
+        make(q, dev, 0);
+        return two(*o, lse);
+    }
 };
 
 // decode_cache(fn, ctas_fn, bytes_fn, q, k_cache, v_cache, k_exp, v_exp, o|None, lse|None, ws|None,
@@ -417,6 +427,7 @@ PyObject* decode_cache(Args a)
     dev.same(n);
     const int H = size32(q.size(1));
     const c10::cuda::CUDAGuard guard(dev.cuda());
+    if (q.size(0) == 0 || mq == 0) return out.nothing(q, dev);
     if (ctas == 0) ctas = ctas_fn(c.B, H, c.Hkv, mq, mk);
     if (ctas < 0) return PyLong_FromLong(ctas);
     out.make(q, dev, out.o ? 0 : bytes_fn(H, c.Hkv, c.d, mq, ctas));
@@ -472,6 +483,7 @@ PyObject* decode_shared(Args a)
     if (total_k == 0 || mk == 0) total_k = mk = 0;
     if (total_p == 0 || mp == 0) total_p = mp = 0;
     const c10::cuda::CUDAGuard guard(dev.cuda());
+    if (total_q == 0 || mq == 0) return out.nothing(q, dev);
     if (ctas == 0) ctas = ctas_fn();
     if (ctas < 0) return PyLong_FromLong(ctas);
     out.make(q, dev, out.o ? 0 : bytes_fn(total_q, H, size32(d), ctas));

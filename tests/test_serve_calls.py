@@ -124,3 +124,57 @@ def test_shared_decode_of_empty_tensors(none, d, H, Hkv, most):
         got = t.run(x, 0.1, causal)
         fa.fa_device_status()
         t.check(got, t.reference(x, 0.1, causal))
+
+
+# ------------------------------------------------------------------------------ empty steps
+
+@gpu
+@pytest.mark.parametrize("rows", [0, 3])
+def test_a_step_without_rows_does_nothing(rows):
+    """No sequence has a token this step: tensors of no rows, or (rows = 3) padded ones with a longest
+    sequence of 0.  Every call returns, writes nothing and reports nothing."""
+    H, Hkv, d, page = 4, 2, 64, 16
+    rnd = lambda h: torch.randn(rows, h, d).bfloat16().cuda()  # noqa: E731
+    q, k, v = rnd(H), rnd(Hkv), rnd(Hkv)
+    none, lens = i32(0, 0, 0).cuda(), i32(5, 0).cuda()
+    cache = fa.new_cache(4, page, Hkv, d)
+    before = [t.view(torch.uint8).clone() for t in cache]
+    tab = i32(0, 1).view(2, 1).cuda()
+    if rows == 0:
+        pos, table = torch.zeros(1, 0, dtype=torch.int32).cuda(), fa.rope_table(d, (32,))
+        for f in (fa.rope, fa.rope_backward):
+            a, b = f(q, k, pos, table)
+            assert a.shape == q.shape and b.shape == k.shape
+        assert fa.rope(q, None, pos, table)[1] is None
+        fa.fa_rope(q, k, q, k, pos, table)
+    fa.cache_append(cache, k, v, none, lens, tab, 0)
+    kr, vr = (t.fill_(3.0) for t in fa.cache_read(cache, none, tab, 0, rows))
+    assert kr.shape == vr.shape == (rows, Hkv, d)
+    fa.fa_cache_read(cache, kr, vr, none, tab, 0)
+    o, lse = torch.full_like(q, 3.0), torch.full((H, rows), 4.0, device="cuda")
+    out = fa.forward_decode_cache(q, cache, none, lens, tab, 0, 5)
+    assert out[0].shape == q.shape and out[1].shape == (H, rows)
+    fa.fa_fwd_decode_cache(q, cache, o, lse, none, lens, tab, 0, 5, 0.1, True, 2, None)
+    own = torch.randn(5, Hkv, d).bfloat16().cuda()
+    a = (own, own, own, own)
+    starts = (none, i32(0, 5, 5).cuda(), i32(0, 2).cuda(), i32(0, 5).cuda(), 0, 5, 0, 5)
+    out = fa.forward_decode_shared(q, *a, *starts)
+    assert out[0].shape == q.shape and out[1].shape == (H, rows)
+    fa.fa_fwd_decode_shared(q, *a, o, lse, *starts, 0.1, True, 2, None)
+    fa.fa_device_status()
+    assert (kr == 3).all() and (vr == 3).all() and (o == 3).all() and (lse == 4).all()
+    assert all(torch.equal(t.view(torch.uint8), b) for t, b in zip(cache, before))
+
+
+@gpu
+def test_an_empty_step_is_checked_like_any_other():
+    q = torch.zeros(0, 4, 64).bfloat16().cuda()
+    cache, ones, tab = fa.new_cache(4, 16, 2, 64), i32(0, 0).cuda(), i32(0).view(1, 1).cuda()
+    with pytest.raises(TypeError):
+        fa.forward_decode_cache(q.float(), cache, ones, i32(5).cuda(), tab, 0, 5)
+    with pytest.raises(ValueError):
+        fa.forward_decode_cache(q, cache, ones, i32(5, 5).cuda(), tab, 0, 5)
+    with pytest.raises(ValueError):
+        fa.rope(q, None, torch.zeros(1, 1, dtype=torch.int32).cuda(), fa.rope_table(64, (32,)))
+    with pytest.raises(ValueError):
+        fa.cache_append(cache, q, q, ones, i32(5).cuda(), tab, 0)  # 4 heads for a cache of 2
