@@ -1663,10 +1663,9 @@ extern "C" int fa_fwd_decode_shared(const void* q, const void* k_prefix, const v
     // (tokens are divided by the tile's: FastDiv)
     if ((std::max(max_group_q, max_seqlen_q) + 128LL) * tok >= (1LL << 32))
         return fail(FA_ERR_TOO_LARGE, "max_seqlen_q and max_group_q must be < 2^25");
-    if (places >= (1LL << 31) || static_cast<long long>(B) * H * max_seqlen_q >= (1LL << 31) ||
-        static_cast<long long>(B) + num_groups > 16384)
-        return fail(FA_ERR_TOO_LARGE, "the batch must have fewer than 2^31 blocks of 128 keys, B*H*max_seqlen_q < 2^31 "
-                                      "and at most 16384 sequences and groups");
+    if (places >= (1LL << 31) || static_cast<long long>(B) + num_groups > 16384)
+        return fail(FA_ERR_TOO_LARGE, "the batch must have fewer than 2^31 blocks of 128 keys and at most 16384 "
+                                      "sequences and groups");
     const size_t need = fa_decode_shared_workspace_bytes(total_q, H, d, num_ctas);
     if (!workspace || workspace_bytes < need)
         return fail(FA_ERR_WORKSPACE, "workspace must hold " + std::to_string(need) + " bytes");

@@ -178,3 +178,38 @@ def test_an_empty_step_is_checked_like_any_other():
         fa.rope(q, None, torch.zeros(1, 1, dtype=torch.int32).cuda(), fa.rope_table(64, (32,)))
     with pytest.raises(ValueError):
         fa.cache_append(cache, q, q, ones, i32(5).cuda(), tab, 0)  # 4 heads for a cache of 2
+
+
+# ------------------------------------------------------------------------------ one long sequence, many short ones
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="calls with dummy pointers that pass every check")
+def test_shared_decode_takes_one_long_and_very_many_short_sequences(lib):
+    """The limits go by the queries that there are, not by what every sequence might have."""
+    vp = ctypes.c_void_p
+    at = [vp((i + 1) << 40) for i in range(11)]
+    rc = lib.fa_fwd_decode_shared(*at, 16000, 1, 5000, 5000, 21000, 100, 21000, 21000, 100, 32, 1, 64,
+                                  ctypes.c_float(0.1), 0, 152, vp(12 << 40), 1 << 39, None)
+    assert rc == -5, lib.fa_last_error()  # only the device is missing
+
+
+@gpu
+def test_shared_decode_of_one_long_and_very_many_short_sequences():
+    from tests import test_decode_shared as t
+
+    few, long, H, Hkv, d = 3000, 3000, 256, 2, 64
+    g = torch.Generator().manual_seed(3)
+    rnd = lambda n, h: torch.randn(n, h, d, generator=g).bfloat16()  # noqa: E731
+    q, k, v, kp, vp = rnd(few + long, H), rnd(few + long, Hkv), rnd(few + long, Hkv), rnd(90, Hkv), rnd(90, Hkv)
+    starts = torch.cat([torch.arange(few + 1), torch.tensor([few + long])]).to(torch.int32)
+    assert (few + 1) * H * long > 2 ** 31
+    x = dict(q=q, k=k, v=v, kp=kp, vp=vp, cu_q=starts, cu_k=starts, cu_g=i32(0, few), cu_p=i32(0, 90))
+    x["sizes"] = (long, long, few, 90)
+    o, lse = t.run(x, 0.1, True)
+    fa.fa_device_status()
+    heads, rows = [5, 200], list(range(0, few, 7)) + [few - 1]
+    part = dict(q=q[rows][:, heads], k=k[rows], v=v[rows], kp=kp, vp=vp, cu_g=i32(0, len(rows)), cu_p=i32(0, 90),
+                cu_q=torch.arange(len(rows) + 1, dtype=torch.int32), cu_k=torch.arange(len(rows) + 1, dtype=torch.int32))
+    t.check((o[rows][:, heads], lse[heads][:, rows]), t.reference(part, 0.1, True))
+    tail = dict(q=q[few:, heads], k=k[few:], v=v[few:], kp=kp, vp=vp, cu_g=i32(1, 1), cu_p=i32(0, 90),
+                cu_q=i32(0, long), cu_k=i32(0, long))
+    t.check((o[few:, heads], lse[heads, few:]), t.reference(tail, 0.1, True))
