@@ -444,9 +444,9 @@ def _native():
     try:
         from . import _serve
     except ImportError as e:
-        raise ImportError("the native binding is missing: build it with "
-                          "exact_attention_25_gb300.build.build_all() (there is no fallback "
-                          "implementation)") from e
+        raise ImportError(f"the native binding is missing or was built for another torch or Python ({e}): "
+                          "build it with exact_attention_25_gb300.build.build_all() (there is no "
+                          "fallback implementation)") from e
     return _serve
 
 

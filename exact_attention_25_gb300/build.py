@@ -69,7 +69,8 @@ def build(force: bool = False, verbose_ptxas: bool = False, checked: bool = Fals
     os.makedirs(bdir, exist_ok=True)
     if force:
         for f in os.listdir(bdir):
-            os.remove(os.path.join(bdir, f))
+            if not f.endswith(".txt"):  # (the binding's, which is built beside this)
+                os.remove(os.path.join(bdir, f))
     srcs = sources()
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas, checked), srcs))
@@ -86,14 +87,17 @@ def build(force: bool = False, verbose_ptxas: bool = False, checked: bool = Fals
 
 def build_binding(force: bool = False) -> str:
     """Compile the native binding of the serving calls (``_serve.so``, a Python extension that
-    allocates through torch and calls the C entry points by address); returns its path."""
+    allocates through torch and calls the C entry points by address) unless the one that is there was
+    built from these sources with this torch and Python; returns its path."""
     import sysconfig
 
     import torch
 
     src = os.path.join(CSRC, "serve_binding.cpp")
     header = os.path.join(ROOT, "include", "fa.h")
-    if (not force and os.path.exists(BINDING)
+    made_for = f"torch {torch.__version__} python {sys.version}"
+    note = os.path.join(BUILD, "serve_binding.txt")  # what the binding was built for
+    if (not force and os.path.exists(BINDING) and _content(note) == made_for
             and os.path.getmtime(BINDING) > max(os.path.getmtime(src), os.path.getmtime(header))):
         return BINDING
     tdir = os.path.dirname(torch.__file__)
@@ -111,7 +115,17 @@ def build_binding(force: bool = False) -> str:
     if res.returncode != 0:
         raise RuntimeError(f"g++ failed for {src}:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, BINDING)
+    os.makedirs(BUILD, exist_ok=True)
+    with open(note, "w") as f:
+        f.write(made_for)
     return BINDING
+
+
+def _content(path: str) -> str | None:
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
 
 
 def build_all(force: bool = False) -> list[str]:

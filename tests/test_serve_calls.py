@@ -213,3 +213,56 @@ def test_shared_decode_of_one_long_and_very_many_short_sequences():
     tail = dict(q=q[few:, heads], k=k[few:], v=v[few:], kp=kp, vp=vp, cu_g=i32(1, 1), cu_p=i32(0, 90),
                 cu_q=i32(0, long), cu_k=i32(0, long))
     t.check((o[few:, heads], lse[heads, few:]), t.reference(tail, 0.1, True))
+
+
+# ------------------------------------------------------------------------------ stale native bindings
+
+class _Compiler:
+    """subprocess.run that writes the output file and counts."""
+    def __init__(self):
+        self.calls = 0
+
+    def __call__(self, cmd, **kw):
+        self.calls += 1
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("compiled")
+        return type("Done", (), dict(returncode=0, stdout="", stderr=""))()
+
+
+def test_a_binding_of_another_torch_is_built_again(monkeypatch, tmp_path):
+    from exact_attention_25_gb300 import build
+
+    run = _Compiler()
+    monkeypatch.setattr(build.subprocess, "run", run)
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / "_serve.so"))
+    monkeypatch.setattr(build, "BUILD", str(tmp_path / "objects"))
+    build.build_binding()
+    build.build_binding()
+    assert run.calls == 1
+    monkeypatch.setattr(torch, "__version__", "9.9.9+other")
+    build.build_binding()
+    build.build_binding()
+    assert run.calls == 2
+    monkeypatch.setattr(build.sys, "version", "4.0 (other)")
+    build.build_binding()
+    assert run.calls == 3
+    build.build_binding(force=True)
+    assert run.calls == 4
+
+
+def test_a_binding_that_does_not_load_says_so(monkeypatch):
+    import builtins
+
+    real = builtins.__import__
+
+    def broken(name, globals=None, locals=None, fromlist=(), level=0):
+        if level and "_serve" in (fromlist or ()):
+            raise ImportError("undefined symbol: of_another_torch")
+        return real(name, globals, locals, fromlist, level)
+
+    fa._native.cache_clear()
+    with monkeypatch.context() as m:
+        m.setattr(builtins, "__import__", broken)
+        with pytest.raises(ImportError, match="of_another_torch.*build_all"):
+            fa._native()
+    assert fa._native().rope
