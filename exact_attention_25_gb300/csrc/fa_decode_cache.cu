@@ -44,7 +44,8 @@
 // to 2^-38 of the row's largest keep a value).  Two running maxima are kept.  m, of the
 // logits x (base 2), frames the sum l.  M, of x + (V's exponent), frames the weights
 // w = 2^(x + ev - M + 11) that multiply V's codes, so a V row of any size keeps its weight's
-// 11 bits and w <= 2^15 (maxima move when they are exceeded by more than 4, so most steps need no
+// 11 bits (rows of zeros, kept under scale 1 whatever the others' size, stay out of M: they would push the weights of
+// small rows below f16's smallest step) and w <= 2^15 (maxima move when they are exceeded by more than 4, so most steps need no
 // reduction over the keys' lanes, only a vote); f16's smallest step puts a floor of 2^-36 of the
 // largest weight under what a single key can still add.
 #include "fa_serve.cuh"
@@ -504,6 +505,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
             }
             // ---- logits x, and x plus V's exponent
             float x[U][NR][4], tv[U][NR][4];
+            bool unit = false;  // a row under scale 1: perhaps a row of zeros
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -511,6 +513,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
                     const int key = (gi + u * gap) * 16 + hf * 8 + kp;
                     const float ks = exp_byte_scale(ex[key]);
                     const float ev = exp_byte_log2(ex[kKB + key]);
+                    unit = unit || ev == 0.0f;
 #pragma unroll
                     for (int n = 0; n < NR; ++n)
 #pragma unroll
@@ -522,6 +525,26 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
                             tv[u][n][2 * hf + e] = w;
                         }
                 }
+            if (__any_sync(0xffffffffu, unit)) {
+                // of a key's row each of the thread's three neighbours reads a quarter too (-0 is zero as well)
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        const int row = (gi + u * gap) * 16 + hf * 8 + kp;
+                        const uint4* w = reinterpret_cast<const uint4*>(vt + row * D + D / 4 * t);
+                        uint32_t some = 0;
+#pragma unroll
+                        for (int i = 0; i < D / 64; ++i) some |= w[i].x | w[i].y | w[i].z | w[i].w;
+                        some &= 0x7f7f7f7fu;
+                        some |= __shfl_xor_sync(0xffffffffu, some, 1);
+                        some |= __shfl_xor_sync(0xffffffffu, some, 2);
+                        if (some == 0 && ex[kKB + row] == 127) {
+#pragma unroll
+                            for (int n = 0; n < NR; ++n) tv[u][n][2 * hf] = tv[u][n][2 * hf + 1] = -INFINITY;
+                        }
+                    }
+            }
             bool need = false;
             float xm[NR][2], tm[NR][2];
 #pragma unroll
