@@ -1335,11 +1335,14 @@ int cache_rows_params(const void* k, const void* v, const long long* strides, vo
         const size_t rows = strides ? 0 : static_cast<size_t>(total) * Hkv * d * (dtype == FA_F32 ? 4 : 2);
         const Span cache[4] = {{kc, codes * d}, {vc, codes * d}, {ke, codes}, {ve, codes}};
         // (strided views may interleave: not checked)
-        const Span out[2] = {{strides ? nullptr : k, rows}, {strides ? nullptr : v, rows}};
+        const Span kv[2] = {{strides ? nullptr : k, rows}, {strides ? nullptr : v, rows}};
+        const Span ints[3] = {{cu, (B + 1ull) * 4}, {table, static_cast<size_t>(B) * max_pages * 4},
+                              {seqlens, seqlens ? B * 4ull : 0}};
         // append writes the cache, read writes k and v: either way they lie apart
-        if (outputs_overlap(cache, 4, out, 2) || (!seqlens && outputs_overlap(out, 2, cache, 0)))
-            return fail(FA_ERR_INVALID_ARG, "the cache's tensors must not overlap one another, k or v (nor k and v "
-                                            "one another where they are written)");
+        if (outputs_overlap(cache, 4, kv, 2) || (seqlens ? outputs_overlap(cache, 4, ints, 3)
+                                                         : outputs_overlap(kv, 2, ints, 2)))
+            return fail(FA_ERR_INVALID_ARG, "what is written (the cache, or k and v) must not overlap itself, the other "
+                                            "side or the integers, nor the cache's tensors one another");
     }
     const int heads[2] = {Hkv, Hkv};
     long long rs[2], hs[2];

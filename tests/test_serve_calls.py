@@ -266,3 +266,23 @@ def test_a_binding_that_does_not_load_says_so(monkeypatch):
         with pytest.raises(ImportError, match="of_another_torch.*build_all"):
             fa._native()
     assert fa._native().rope
+
+
+# ------------------------------------------------------------------------------ integers inside the outputs
+
+@pytest.mark.parametrize("name", ["cu", "n", "table"])
+@pytest.mark.parametrize("at", [0x30000, 0x41000, 0x50000, 0x60020])
+def test_append_refuses_integers_inside_the_cache(lib, name, at):
+    from tests import test_cache
+
+    assert test_cache.append(lib, {**test_cache.BASE, name: at}) == -1
+    assert b"overlap" in lib.fa_last_error()
+
+
+@pytest.mark.parametrize("name", ["cu", "table"])
+@pytest.mark.parametrize("at", [0x10000, 0x20100])
+def test_read_refuses_integers_inside_its_outputs(lib, name, at):
+    from tests import test_cache
+
+    assert test_cache.read(lib, {**test_cache.BASE, name: at}) == -1
+    assert b"overlap" in lib.fa_last_error()
