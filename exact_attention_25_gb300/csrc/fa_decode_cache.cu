@@ -505,25 +505,14 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
             }
             // ---- logits x, and x plus V's exponent
             float x[U][NR][4], tv[U][NR][4];
+            float ev[U][2];
             bool unit = false;  // a row under scale 1: perhaps a row of zeros
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    const int key = (gi + u * gap) * 16 + hf * 8 + kp;
-                    const float ks = exp_byte_scale(ex[key]);
-                    const float ev = exp_byte_log2(ex[kKB + key]);
-                    unit = unit || ev == 0.0f;
-#pragma unroll
-                    for (int n = 0; n < NR; ++n)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            float v = sc[u][n][2 * hf + e] * (cx[n][e] * ks);
-                            float w = v + ev;
-                            if (MASKED && block * kKB + key > lim[n][e]) v = w = -INFINITY;
-                            x[u][n][2 * hf + e] = v;
-                            tv[u][n][2 * hf + e] = w;
-                        }
+                    ev[u][hf] = exp_byte_log2(ex[kKB + (gi + u * gap) * 16 + hf * 8 + kp]);
+                    unit = unit || ev[u][hf] == 0.0f;
                 }
             if (__any_sync(0xffffffffu, unit)) {
                 // of a key's row each of the thread's three neighbours reads a quarter too (-0 is zero as well)
@@ -539,12 +528,26 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
                         some &= 0x7f7f7f7fu;
                         some |= __shfl_xor_sync(0xffffffffu, some, 1);
                         some |= __shfl_xor_sync(0xffffffffu, some, 2);
-                        if (some == 0 && ex[kKB + row] == 127) {
-#pragma unroll
-                            for (int n = 0; n < NR; ++n) tv[u][n][2 * hf] = tv[u][n][2 * hf + 1] = -INFINITY;
-                        }
+                        if (some == 0 && ev[u][hf] == 0.0f) ev[u][hf] = -INFINITY;
                     }
             }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int key = (gi + u * gap) * 16 + hf * 8 + kp;
+                    const float ks = exp_byte_scale(ex[key]);
+#pragma unroll
+                    for (int n = 0; n < NR; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float v = sc[u][n][2 * hf + e] * (cx[n][e] * ks);
+                            float w = v + ev[u][hf];
+                            if (MASKED && block * kKB + key > lim[n][e]) v = w = -INFINITY;
+                            x[u][n][2 * hf + e] = v;
+                            tv[u][n][2 * hf + e] = w;
+                        }
+                }
             bool need = false;
             float xm[NR][2], tm[NR][2];
 #pragma unroll
