@@ -1455,8 +1455,8 @@ extern "C" int fa_decode_cache_ctas_for(int B, int H, int Hkv, int max_seqlen_q,
     if (B < 1 || H < 1 || Hkv < 1 || H % Hkv || max_seqlen_q < 1 || max_seqlen_k < 1 || num_sms < 1)
         return fail(FA_ERR_INVALID_ARG, "sizes must be >= 1 and H a multiple of Hkv");
     const long long most = cache_blocks(B, H, Hkv, max_seqlen_q, max_seqlen_k);
-    // two blocks at least, so that a CTA's fixed latency is spread (one sequence of 4 K keys and 8
-    // heads: 9.8 us with 128 CTAs of two blocks, 10.4 with 228)
+    // two blocks at least: beyond that there is little to gain (one sequence of 4 K keys and 8 heads: 10.7 us with
+    // 128 CTAs of two blocks, 10.6 with 228, 10.1 with 304), and the places left over serve other streams
     return static_cast<int>(std::min<long long>((most + 1) / 2, std::min(2 * num_sms, kCacheMaxCtas)));
 }
 

@@ -4,11 +4,12 @@
 // to fp32 accumulation and the f16 rounding of the softmax weights.
 //
 // What bounds it: the codes, read once (2 * Nk * Hkv * d bytes a sequence): 8 sequences of up to 32 K
-// keys, 8 heads of 128: 61 us, 89 % of the copy rate; 64 of up to 4 K: 50 us, 80 %.  With 16 query rows a
-// head at d = 128 (8 sequences of 16 K: 88 us, 45 %) a step's chain of products, exponentials and products,
+// keys, 8 heads of 128: 62 us, 87 % of the copy rate; 64 of up to 4 K: 51 us, 78 %.  With 16 query rows a
+// head at d = 128 (8 sequences of 16 K: 86 us, 46 %) a step's chain of products, exponentials and products,
 // of which the registers hold only one at a time.  Calls of one or two blocks a CTA are a chain of
-// latencies: one sequence of 4 K keys 9.7 us, of which lengths 0.9, page ids 1.1, copies and products 2-3,
-// the warps' merge 1, the parts' stores 0.5, and the merge kernel 2.3.
+// latencies: one sequence of 4 K keys 10.6 us, of which lengths 0.9, page ids 1.1, copies and products 2-3,
+// the warps' merge 1, the parts' stores 0.5, and the merge kernel about 3 (two round trips: what the parts are
+// of, then the parts).
 // At the copy rate an SM receives about 23 bytes a clock, so tcgen05 has no place here although a decode
 // tile of bf16 keys uses it: the codes would have to become 16-bit operands in shared memory, and one
 // write by the copy, a read and a double-width write by the conversion and a double-width read
@@ -703,7 +704,7 @@ __global__ void __launch_bounds__(CacheCfg<D>::THREADS, 2)
             // Steps in the clear go U at a time, so that one's products hide the other's latencies.  (16
             // rows at d = 64: 16 sequences of up to 5000 keys, 32 rows: 18.0 us, one at a time 19.5.  At
             // d = 128 their registers do not hold two: 8 sequences of 16 K keys, 16 rows: 95 us, one at a
-            // time 87.)
+            // time 86.)
             constexpr int U = NR == 1 || D == 64 ? 2 : 1;
             if (most >= 0)  // (else there is no query row in this warp's tile)
 #pragma unroll 1

@@ -8,8 +8,8 @@
 //
 // What bounds it: reading prefix and own keys once (HBM), and for large groups the exponentials of
 // tokens x heads x prefix scores.  64 sequences with up to 1024 keys of their own over 32000 tokens, 32
-// heads over 8 of 128: 62 us, 253 MB from HBM (4.1 TB/s) and 421 MB from L2 (the prefix is copied for each of
-// its two tiles); 53 us without the softmax, 57 without its products.  8 sequences over 4 K tokens: 12.2 us,
+// heads over 8 of 128: 64 us, 253 MB from HBM (4.0 TB/s) and 421 MB from L2 (the prefix is copied for each of
+// its two tiles); 9 us less without the softmax, 5 less without its products.  8 sequences over 4 K tokens: 13.4 us,
 // a chain of latencies.
 //
 // Both kinds of work are units of one line (units, below) shared out evenly over the SMs, so memory-bound
@@ -809,8 +809,8 @@ static cudaError_t launch_decode_shared_impl(const CUtensorMap* maps, const Shar
                                      st, maps[0], maps[1], maps[2], maps[3], maps[4], p);
     if (e != cudaSuccess) return e;
     // The merge's CTAs start beside the attention's and wait there; with few rows they all fit with 16
-    // parts in flight each (8 queries: 12.2 us, 12.7 with 8), with many only with 8 (64 queries: 61.7 us,
-    // with 16 a second wave starts late, 65.4).
+    // parts in flight each (8 queries: 13.3 us, 13.8 with 8), with many only with 8 (64 queries: 63.9 us,
+    // with 16 a second wave starts late, 68.2).
     const long long rows = static_cast<long long>(p.total_q) * p.H;
     const dim3 grid(static_cast<unsigned>((rows + 3) / 4));
     return rows <= 8ll * num_sms

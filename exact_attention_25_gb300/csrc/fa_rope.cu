@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kRopeThreads) fa_rope_kernel(const __grid_cons
     const int lane = threadIdx.x & 31;
     const int c = lane % C, hs = lane / C;
     // The lane's pairs of the table.  Read through a generic address: as constants, with another index in
-    // every lane, they took a third of a small call (8 tokens: 3.0 us instead of 2.1).
+    // every lane, they took a third of a small call (8 tokens: 3.0 us instead of 1.8).
     const unsigned long long* turns = p.turn;
     const unsigned char* axes = p.axis;
     asm volatile("" : "+l"(turns), "+l"(axes));

@@ -82,8 +82,12 @@ struct CacheParams {
 constexpr int kCacheBlock = 128;  // keys of a block of the cache decode
 
 // What a unit (below) costs besides its blocks (queries, merge of the warps, output), in blocks.
-constexpr int kUnitCost = 2;        // cache decode (64 sequences of up to 4 K keys: 51 us; 1: 55, 3: 51, 4: 51)
-constexpr int kSharedUnitCost = 3;  // shared prefixes (64 over one of 32000: 62 us; 4: 64, 2: 63, 1: 66)
+// Cache decode with 1, 2, 3 and 4: 64 sequences of up to 4 K keys 56.6, 51.7, 51.8, 52.4 us; 16 of up to 5000, 32 rows
+// at d = 64: 17.4, 16.8, 16.8, 17.0; 8 of up to 32 K: 62.3-62.6.  Shared prefixes: 64 sequences over 32000 tokens at
+// d = 128: 67.5, 64.6, 63.9, 67.0 us, at d = 64: 63.4, 60.4, 61.6, 64.8; 8 over 4 K: 14.5, 13.3, 13.4, 13.9; 24 with 4
+// queries each over three prefixes of up to 8 K: 40.6, 38.3, 38.9, 39.8.
+constexpr int kUnitCost = 2;
+constexpr int kSharedUnitCost = 3;
 
 // Split-KV decode over the paged cache.  The work is a line of units: for every sequence, for
 // every `rows_cta` query rows of a group and every key/value head, kUnitCost places and one place
@@ -209,8 +213,8 @@ __device__ __forceinline__ Shares find_share(int items, int ctas, int c, F place
 // The merge of a query row's parts, by a warp: O = sum_s e^{lse_s} O_s / sum_s e^{lse_s} and lse = log
 // sum_s e^{lse_s}, whose numerators are left in acc (elements D / 32 * lane on), denominator in sum and
 // frame in mx (sum = 0: no part saw a key).  Part k is row row_of(k) of the workspace.  The rows of a batch
-// are loaded along with their lse, in one round trip (one sequence of 4 K keys, 16 parts: 9.8 us; four at a
-// time, after their lse, 11.0); those of parts that saw no key hold anything and are not used.
+// are loaded along with their lse, in one round trip (one sequence of 4 K keys, 16 parts: 1.2 us less than four
+// at a time, after their lse); those of parts that saw no key hold anything and are not used.
 template <int D, int BATCH, class F>
 __device__ __forceinline__ void merge_parts(int parts, F row_of, const float* o_part, const float* lse_part,
                                             long long rows, int* status, float& mx, float& sum, float* acc)
