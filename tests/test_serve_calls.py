@@ -286,3 +286,43 @@ def test_read_refuses_integers_inside_its_outputs(lib, name, at):
 
     assert test_cache.read(lib, {**test_cache.BASE, name: at}) == -1
     assert b"overlap" in lib.fa_last_error()
+
+
+# ------------------------------------------------------------------------------ calls without lse, long pages
+
+@gpu
+@pytest.mark.parametrize("ctas", [1, 7])
+def test_decodes_without_lse_give_the_same_outputs(ctas):
+    from tests import test_decode_cache as c
+    from tests import test_decode_shared as t
+    from tests.test_cache import cu, table_for
+
+    H, Hkv, d, page, lens_q, lens_k = 8, 2, 128, 64, [1, 2], [700, 90]
+    table, pool = table_for(lens_k, page, 1, 3)
+    cache = c.to_cache(*c.random_cache(pool, Hkv, page, d, 3))
+    q = torch.randn(3, H, d, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    a = (cu(lens_q).cuda(), i32(*lens_k).cuda(), table.cuda(), 2, 700, 0.1, True, ctas)
+    want = fa.forward_decode_cache(q, cache, *a)
+    o = torch.empty_like(q)
+    ws = torch.empty(max(fa.fa_decode_cache_workspace_bytes(H, Hkv, d, 2, ctas), 16), dtype=torch.uint8).cuda()
+    fa.fa_fwd_decode_cache(q, cache, o, None, *a, ws)
+    assert torch.equal(o, want[0])
+    x = t.make([1, 2, 1], [30, 200, 5], [0, 3], [900], H, Hkv, d, 2)
+    dev = {n: v.cuda() for n, v in x.items() if n != "sizes"}
+    want = t.run(x, 0.1, True, ctas)
+    o = torch.empty_like(dev["q"])
+    ws = torch.empty(fa.fa_decode_shared_workspace_bytes(4, H, d, ctas), dtype=torch.uint8).cuda()
+    fa.fa_fwd_decode_shared(*(dev[n] for n in ("q", "kp", "vp", "k", "v")), o, None,
+                            *(dev[n] for n in ("cu_q", "cu_k", "cu_g", "cu_p")), *x["sizes"], 0.1, True, ctas, ws)
+    assert torch.equal(o, want[0])
+    fa.fa_device_status()
+
+
+@gpu
+@pytest.mark.parametrize("ctas", [None, 5])
+@pytest.mark.parametrize("page", [256, 512, 1024])
+def test_cache_decode_over_long_pages(page, ctas):
+    from tests import test_decode_cache as c
+
+    c.run_case([1, 4, 2], [2500, 1024, 7], 8, 2, 64, page, True, ctas, seed=page)
+    c.run_case([1, 1], [1025, 513], 4, 4, 128, page, False, ctas, seed=page + 1)
