@@ -1095,7 +1095,7 @@ __global__ void __launch_bounds__(kMergeThreads) fa_decode_tree_merge_kernel(con
     const int r = blockIdx.y * (kMergeThreads / 32) + (threadIdx.x >> 5);
     if (r < rows) {
         float mx, sum, acc[EPL];
-        merge_parts<D, 16>(
+        merge_parts<D, 16, true>(
             parts, [&](int k) { return (2 * (c0 + k) + (k == 0 ? lead : 0)) * p.part_rows + r; }, p.o_part,
             p.lse_part, p.part_ext / D, p.status, mx, sum, acc);
         const int i = p.G(row0 + r), h = hk * p.G.d + (row0 + r) - i * p.G.d;

@@ -314,8 +314,10 @@ __device__ __forceinline__ Shares find_share(int items, int ctas, int c, F place
 // sum_s e^{lse_s}, whose numerators are left in acc (elements D / 32 * lane on), denominator in sum and
 // frame in mx (sum = 0: no part saw a key).  Part k is row row_of(k) of the workspace.  The rows of a batch
 // are loaded along with their lse, in one round trip (one sequence of 4 K keys, 16 parts: 1.2 us less than four
-// at a time, after their lse); those of parts that saw no key hold anything and are not used.
-template <int D, int BATCH, class F>
+// at a time, after their lse); those of parts that saw no key hold anything and are not used.  HALVES: weights are applied as
+// their square root twice, so that one below fp32's smallest still counts where its part's O is large (down to 2^-250 of
+// the largest; values span 2^-110 to 2^128).
+template <int D, int BATCH, bool HALVES = false, class F>
 __device__ __forceinline__ void merge_parts(int parts, F row_of, const float* o_part, const float* lse_part,
                                             long long rows, int* status, float& mx, float& sum, float* acc)
 {
@@ -352,19 +354,20 @@ __device__ __forceinline__ void merge_parts(int parts, F row_of, const float* o_
         float nm = fmaxf(mx, ls);
 #pragma unroll
         for (int d = 16; d; d >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, d));
-        const float keep = mx == -INFINITY ? 0.0f : expf(mx - nm);
-        sum *= keep;
+        const float part = HALVES ? 0.5f : 1.0f;
+        const float keep = mx == -INFINITY ? 0.0f : expf(part * (mx - nm));
+        sum *= HALVES ? keep * keep : keep;
 #pragma unroll
-        for (int e = 0; e < EPL; ++e) acc[e] *= keep;
+        for (int e = 0; e < EPL; ++e) acc[e] = HALVES ? acc[e] * keep * keep : acc[e] * keep;
         mx = nm;
-        const float wt = ls == -INFINITY ? 0.0f : expf(ls - nm);
+        const float wt = ls == -INFINITY ? 0.0f : expf(part * (ls - nm));
 #pragma unroll
         for (int k = 0; k < BATCH; ++k) {
             const float w = __shfl_sync(0xffffffffu, wt, k);
             if (!(live >> k & 1)) continue;
-            sum += w;
+            sum += HALVES ? w * w : w;
 #pragma unroll
-            for (int e = 0; e < EPL; ++e) acc[e] = fmaf(w, v[k][e], acc[e]);
+            for (int e = 0; e < EPL; ++e) acc[e] = fmaf(w, HALVES ? w * v[k][e] : v[k][e], acc[e]);
         }
     }
 }
