@@ -18,9 +18,11 @@
 //
 // What bounds it: the chain of a step, some 1400 clocks of 64 keys, in which every part (copy, exponents, conversion, product,
 // softmax, product) takes a warp 500 to 1400; the schedulers issue half the time and the tensor cores run a third of it.  On 8
-// sequences of up to 32 K keys, H = 32 / Hkv = 8, d = 128: trees of up to 24 tokens 108 us (2.9 TB/s of codes), of 64
-// tokens 212 us (0.74 PFLOP/s).  Registers decide how the softmax's loop is written: 20 warps have 96 each, and a few of its
-// values in local memory cost a quarter (O rescaled 64 columns at a time, scores read once and kept: 140 to 147 us).
+// sequences of up to 32 K keys, H = 32 / Hkv = 8, d = 128: trees of up to 24 tokens 110 us (2.85 TB/s of codes), of 64
+// tokens 217 us (0.72 PFLOP/s).  Registers decide how the softmax's loop is written: 20 warps have 96 each, and a few of its
+// values in local memory cost a quarter (O rescaled 64 columns at a time, scores read once and kept: 140 to 147 us).  The sum's
+// own frame costs 2 and 5 us; its part of a step added after the weights are handed on the same, one vote for both maxima
+// 111 and 220.
 //
 // Roles of a CTA (20 warps):
 //  - warp 16 copies pages of codes and exponents to a ring of raw tiles, 16.1 KB a step at d = 128, a lane each of a
@@ -36,13 +38,15 @@
 //
 // Number ranges.  The converted codes of a step hold their rows' powers of two relative to the step's largest
 // (exactly: both spread over few binades), so x = S c with one factor a row and step, and V's tile stands for V 2^-E,
-// E the step's largest exponent.  One running maximum M of x + E frames both sums: w = 2^(x + E - M + 7), f16,
-// multiplies V's tile, and p = 2^(x - M - 4) = w 2^-(E + 11) adds up to l.  Weights keep 11 bits
-// down to 2^-21 of the largest (M moves when it is exceeded by more than 8, so w <= 2^15), and f16's smallest step puts a
-// floor of 2^-32 of the largest under what a single key can still add, whatever the values' size in
-// other steps; x - M lies between -120 and 118, so p stays within fp32's range.  Steps whose rows' sizes lie further
-// apart go key by key: K's scale multiplies the score, V's exponent E becomes the row's own, and the tiles hold
-// the plain codes.
+// E the step's largest exponent.  Two running maxima are kept, as in the cache decode.  M, of x + E, frames the weights:
+// w = 2^(x + E - M + 7), f16, multiplies V's tile.  Weights keep 11 bits down to 2^-21 of the largest (a maximum moves when
+// it is exceeded by more than 8, so w <= 2^15), and f16's smallest step puts a floor of 2^-32 of the largest under what
+// a single key can still add.  m, of x, frames the sum l of 2^(x - m), which has nothing to do with V.  A step's part of it is
+// the sum of its w in fp32 times 2^(M - E - 7 - m): one exponential a row.  Where w is too small for that although the
+// keys count in l (a step whose V rows are far smaller than another's), the step's 2^(x - m) are computed for
+// themselves.  M - m is V's size, up to 2^+-126, so the result's power of two is applied in halves.  Steps whose rows' sizes
+// lie further apart go key by key: K's scale multiplies the score, V's exponent E becomes the row's own, and the tiles
+// hold the plain codes.
 #include "fa_serve.cuh"
 #include "tc_ptx.cuh"
 
@@ -58,13 +62,17 @@ constexpr int kTreeUnits = 32;     // units described ahead
 constexpr int kRing = 16;          // steps that something is known of (SLOTS + 6 at least: see the scout)
 constexpr int kTile = 128;         // query rows of a tile
 constexpr int kMergeThreads = 128;
-constexpr float kGrow = 8.0f;      // M moves when it is exceeded by more than this (in a warp of 32 rows one grows at most steps:
+constexpr float kGrow = 8.0f;      // a maximum moves when it is exceeded by more than this (in a warp of 32 rows one grows at most steps:
                                    // with 4, two of three steps rescaled O; 64 tokens 215 us in place of 212)
+// A step's largest weight below 2^(kFrame - kDeep) leaves its lesser ones no room above fp32's smallest, 2^-126 (2^-43 of
+// it is left); keys below 2^-kSmall of a row's largest add nothing to l that it could hold (2^31 of them 2^-33).
+constexpr float kDeep = 90.0f, kSmall = 64.0f;
 constexpr float kFrame = 7.0f;     // log2 of the largest weight right after that
 // A step's codes take their rows' scales along into f16, relative to the largest of the step, if K's spread
 // over at most kSpreadK binades and V's over at most kSpreadV, and none lies beyond 2^+-100 (as bytes: kLow to
-// kHigh).  Rows of zeros, kept under scale 1 whatever the others' size, count as kLow where the step is not so.
-constexpr int kSpreadK = 14, kSpreadV = 10, kLow = 27, kHigh = 227;
+// kHigh).  V rows of zeros, kept under scale 1 whatever the others' size, count as kZero, below every row that is not
+// (2^-110 is the smallest scale that is written).
+constexpr int kSpreadK = 14, kSpreadV = 10, kLow = 27, kHigh = 227, kZero = 1;
 
 template <int D>
 struct TreeCfg {
@@ -388,10 +396,10 @@ struct StepKeys {
     }
 };
 
-// The largest x + E of a row.
-__device__ __noinline__ float step_max(uint32_t ts, StepKeys k, const float* ks, const float* ev, float down)
+// The largest x and the largest x + E of a row.
+__device__ __noinline__ float2 step_max(uint32_t ts, StepKeys k, const float* ks, const float* ev, float down)
 {
-    float mt = -INFINITY;
+    float mx = -INFINITY, mt = -INFINITY;
     uint32_t vis = 0;
 #pragma unroll 1
     for (int c = 0; c < 2 * k.chunks(); ++c, ts += 16, ks += 16, ev += 16) {
@@ -402,16 +410,19 @@ __device__ __noinline__ float step_max(uint32_t ts, StepKeys k, const float* ks,
         reg_fence16(v);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const float t = fmaf(__uint_as_float(v[i]), ks[i] * down, ev[i]);
-            if (vis >> i & 1) mt = fmaxf(mt, t);
+            const float x = __uint_as_float(v[i]) * (ks[i] * down);
+            if (!(vis >> i & 1)) continue;
+            mx = fmaxf(mx, x);
+            mt = fmaxf(mt, x + ev[i]);
         }
     }
-    return mt;
+    return make_float2(mx, mt);
 }
 
-// The weights of a row, over its scores (P of 16 keys goes where S of keys up to those was); nm: -M.
-// Returns the sum of p.
-__device__ __noinline__ float step_weights(uint32_t ts, StepKeys k, const float* ks, const float* ev, float down, float nm)
+// The weights of a row, over its scores (P of 16 keys goes where S of keys up to those was); nm: -M, nl: -m.
+// Returns the sum of 2^(x - m).
+__device__ __noinline__ float step_weights(uint32_t ts, StepKeys k, const float* ks, const float* ev, float down, float nm,
+                                           float nl)
 {
     float l = 0.0f;
     uint32_t vis = 0, tp = ts;
@@ -428,13 +439,29 @@ __device__ __noinline__ float step_weights(uint32_t ts, StepKeys k, const float*
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const bool see = vis >> (i + e) & 1;
-                const float x = fmaf(__uint_as_float(v[i + e]), ks[i + e] * down, nm);
-                l += see ? ex2(x - 4.0f) : 0.0f;
-                w[e] = see ? ex2(x + (ev[i + e] + kFrame)) : 0.0f;
+                const float x = __uint_as_float(v[i + e]) * (ks[i + e] * down);
+                l += see ? ex2(x + nl) : 0.0f;
+                w[e] = see ? ex2(x + (nm + (ev[i + e] + kFrame))) : 0.0f;
             }
             v[i / 2] = pack_f16x2(w[0], w[1]);
         }
         tmem_st8(tp, v);
+    }
+    return l;
+}
+
+// The sum of 2^(x - m) of a row that sees all keys of a step whose scales are in the tiles (x = S cf); nl: -m.
+__device__ __noinline__ float step_sum(uint32_t ts, float cf, float nl)
+{
+    float l = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c < kHalf; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(ts + c, v);
+        tmem_wait_ld();
+        reg_fence16(v);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) l += ex2(fmaf(__uint_as_float(v[i]), cf, nl));
     }
     return l;
 }
@@ -459,7 +486,8 @@ __device__ __noinline__ void note_nan(StepKeys k, bool valid, const uint16_t* na
 
 // What a unit's row came to.
 struct RowResult {
-    float f0, f1, inv;      // factors of the two accumulators, and of both
+    float f0, f1;           // factors of the two accumulators (below 0: what it holds is not used) ...
+    float inv, half;        // ... and of both: inv, and half twice
     const uint32_t *nan0, *nan1;  // columns that are NaN, or null
 };
 
@@ -468,7 +496,7 @@ struct RowResult {
 template <int D>
 __device__ __noinline__ void write_row(uint32_t to, int c0, RowResult r, __nv_bfloat16* o, float* part, bool in)
 {
-    const float g0 = r.f0 * 0x1p-11f, g1 = r.f1 * 0x1p-11f;
+    const float both = r.inv * r.half;
 #pragma unroll 1
     for (int c = c0; c < c0 + D / 2; c += 16) {
         uint32_t x[16], y[16];
@@ -478,13 +506,12 @@ __device__ __noinline__ void write_row(uint32_t to, int c0, RowResult r, __nv_bf
         reg_fence16(x);
         reg_fence16(y);
         const uint32_t nan = ((r.nan0 ? r.nan0[c / 32] : 0u) | (r.nan1 ? r.nan1[c / 32] : 0u)) >> (c & 16);
-        // (the power in two steps: 2^-11 / l may be too small where O is not.  A row that saw no key in a stream has a
-        // factor of 0 there, and what the accumulator holds is not used.)
+        // (a factor of 0, of a stream whose values are small beside the other's, still hands on a NaN)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            float v = r.f0 == 0.0f ? 0.0f : __uint_as_float(x[i]) * g0 * r.inv;
-            if (r.f1 != 0.0f) v += __uint_as_float(y[i]) * g1 * r.inv;
-            x[i] = __float_as_uint(nan >> i & 1 ? NAN : v);
+            float v = r.f0 < 0.0f ? 0.0f : __uint_as_float(x[i]) * r.f0;
+            if (!(r.f1 < 0.0f)) v = fmaf(__uint_as_float(y[i]), r.f1, v);
+            x[i] = __float_as_uint(nan >> i & 1 ? NAN : v * both * r.half);
         }
         if (!in) continue;
         if (o != nullptr) {
@@ -551,7 +578,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1) fa_decode_tree_kernel(
     __shared__ uint16_t s_nan[2][kHalf][D / 16];  // NaN codes that were taken out of V's tile
     __shared__ uint32_t s_any_nan[2][2];          // by converting warp
     __shared__ uint32_t s_row_nan[2][kTile][D / 32];  // by stream: the row's columns that are NaN
-    __shared__ float2 s_post[2][kTile];           // by stream: M and l
+    __shared__ float4 s_post[2][kTile];           // by stream: M, m and l
     __shared__ uint8_t s_post_odd[2][kTile];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
@@ -861,7 +888,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1) fa_decode_tree_kernel(
                 const bool far = (kany && (ktop > kHigh || klow < kLow || ktop - klow > kSpreadK)) ||
                                  (vany && (vtop > kHigh || vlow < kLow || vtop - vlow > kSpreadV));
                 if (!kany) ktop = 127;
-                if (!vany) vtop = kLow;
+                if (!vany) vtop = kZero;
                 if (far || !whole) {
 #pragma unroll 1
                     for (int j = 0; j < 4; ++j) {
@@ -869,7 +896,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1) fa_decode_tree_kernel(
                         const bool zero = !(vin >> (8 * j) & 1);
                         s_ks[nr][4 * l4 + j] = p.scale_log2 * exp_byte_scale(far ? kb : static_cast<uint32_t>(ktop));
                         s_ev[nr][4 * l4 + j] = !far ? static_cast<float>(vtop - 127)
-                                                    : zero ? static_cast<float>(kLow - 127) : exp_byte_log2(vb);
+                                                    : zero ? static_cast<float>(kZero - 127) : exp_byte_log2(vb);
                     }
                 }
                 if (lane == 0) s_info[nr] = BlockInfo(valid, far, ktop, vtop).v;
@@ -903,7 +930,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1) fa_decode_tree_kernel(
             const bool valid = r < un.rows;
             const bool any_valid = __any_sync(0xffffffffu, valid);
             // (rows that are none need no rescaling: their scores are 0)
-            float M = valid ? -INFINITY : 1000.0f, l = 0.0f, down = 0.0f;
+            float M = valid ? -INFINITY : 1000.0f, m = M, l = 0.0f, down = 0.0f;
             bool odd = false;
 #pragma unroll 1
             for (int hh = first; hh < nh; hh += 2) {
@@ -920,12 +947,16 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1) fa_decode_tree_kernel(
                     const BlockInfo info(s_info[n4]);
                     const int groups = info.groups();
                     const bool whole = hh < clear && groups == 0xf;
-                    auto move_max = [&](float mt) {
+                    // (both are -infinity until there is a logit that is not)
+                    auto move_max = [&](float xm, float mt) {
+                        if (xm > m + kGrow) {
+                            l *= ex2(m - xm);
+                            m = xm;
+                        }
                         need = mt > M + kGrow;
                         if (need) {
                             alpha = ex2(M - mt);
                             M = mt;
-                            l *= alpha;
                         }
                         return M == -INFINITY ? 0.0f : -M;
                     };
@@ -943,7 +974,12 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1) fa_decode_tree_kernel(
                                 asm volatile("" : "+f"(mx[c2]));
                             }
                         }
-                        const float nm = move_max(fmaf(fmaxf(mx[0], mx[1]), cf, ev)) + (ev + kFrame);
+                        const float xm = fmaxf(mx[0], mx[1]) * cf;
+                        const float nm = move_max(xm, xm + ev) + (ev + kFrame);
+                        const float nl = m == -INFINITY ? 0.0f : -m;
+                        float sum = -1.0f;
+                        if (__any_sync(0xffffffffu, valid && xm + nm < kFrame - kDeep && xm + nl > -kSmall))
+                            sum = step_sum(tS, cf, nl);
                         // (the loads find the maximum: 64 tokens 220 us in replays, with the registers' own 225.)
                         // S is read again, 32 columns at a time in a rolled loop: with eight kinds of warps the instruction
                         // cache, not their arithmetic, was what they waited for
@@ -973,15 +1009,17 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1) fa_decode_tree_kernel(
                         }
                         float a0, a1;
                         f2_split(f2_add(la, lb), a0, a1);
-                        // (w is 2^(ev + 11) p)
-                        l = fmaf(a0 + a1, __uint_as_float(static_cast<uint32_t>(243 - info.ev()) << 23), l);
+                        // (2^91 suffices where w is large enough: 2^(8 + 90 - 7); rows of lesser keys may ask for more)
+                        if (sum < 0.0f) sum = (a0 + a1) * ex2(fminf(nl - nm, 100.0f));
+                        l += sum;
                     } else {
                         // key by key
                         const int tok = valid ? un.q0 + p.G(un.row0 + r) : un.q0;
                         const StepKeys keys{p.mask + static_cast<long long>(tok) * p.words, p.words, un.ts, un.nk, step * kHalf, groups,
                                             whole, in_extent(static_cast<long long>(tok) * p.words, p.words, p.mask_ext, p.status)};
-                        const float nm = move_max(step_max(tS, keys, s_ks[n4], s_ev[n4], down));
-                        l += step_weights(tS, keys, s_ks[n4], s_ev[n4], down, nm);
+                        const float2 top = step_max(tS, keys, s_ks[n4], s_ev[n4], down);
+                        const float nm = move_max(top.x, top.y);
+                        l += step_weights(tS, keys, s_ks[n4], s_ev[n4], down, nm, m == -INFINITY ? 0.0f : -m);
                         if (!whole) {
                             // NaN codes that were taken out of V: the columns of rows that see them
                             ok = tree_wait(&bar_full[1][n & 1], (n >> 1) & 1, wd, kSiteTreeV);
@@ -1032,7 +1070,7 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1) fa_decode_tree_kernel(
             // Both streams know both streams' sums then, and write half of the columns each.
             if (posted) ok = tree_wait(&bar_joined, (k - 1) & 1, wd, kSiteTreeMerge);
             if (!ok) break;
-            s_post[s][r] = make_float2(M, l);
+            s_post[s][r] = make_float4(M, m, l, 0.0f);
             s_post_odd[s][r] = odd;
             __syncwarp();
             if (lane == 0) mbar_arrive(&bar_post[s]);
@@ -1040,24 +1078,28 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1) fa_decode_tree_kernel(
             if (!ok) break;
             tc_fence_after();
             // (a row that saw no key in a stream has l = 0 there, and what O holds is not used)
-            const float2 x = s_post[0][r], y = s_post[1][r];
-            const float m2 = fmaxf(x.y == 0.0f ? -INFINITY : x.x, y.y == 0.0f ? -INFINITY : y.x);
-            const float f0 = x.y == 0.0f ? 0.0f : m2 == -INFINITY ? 1.0f : ex2(x.x - m2);
-            const float f1 = y.y == 0.0f ? 0.0f : m2 == -INFINITY ? 1.0f : ex2(y.x - m2);
-            l = x.y * f0 + y.y * f1;
+            const float4 x = s_post[0][r], y = s_post[1][r];
+            const bool no0 = x.z == 0.0f, no1 = y.z == 0.0f;
+            // (a maximum that is infinite or missing frames nothing)
+            auto factor = [](float a, float top) { return a == top || top == -INFINITY ? 1.0f : ex2(a - top); };
+            const float M2 = fmaxf(no0 ? -INFINITY : x.x, no1 ? -INFINITY : y.x);
+            const float m2 = fmaxf(no0 ? -INFINITY : x.y, no1 ? -INFINITY : y.y);
+            const float f0 = no0 ? -1.0f : factor(x.x, M2), f1 = no1 ? -1.0f : factor(y.x, M2);
+            l = (no0 ? 0.0f : x.z * factor(x.y, m2)) + (no1 ? 0.0f : y.z * factor(y.y, m2));
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            const float half = M2 == -INFINITY || m2 == -INFINITY ? 1.0f : ex2(0.5f * (M2 - kFrame - m2));
             const int i = p.G(un.row0 + r), h = un.hk * p.G.d + un.row0 + r - i * p.G.d;
             const bool whole = un.J == un.nblk;
             const long long at = whole ? static_cast<long long>(un.q0 + i) * p.H + h
                                        : static_cast<long long>(2 * cta + (un.first ? 0 : 1)) * p.part_rows + r;
             const bool in = valid && in_extent(at * D, D, whole ? p.q_ext : p.part_ext, p.status);
             if (any_valid) {
-                const RowResult res{f0, f1, inv, s_post_odd[0][r] ? s_row_nan[0][r] : nullptr,
+                const RowResult res{f0, f1, inv, half, s_post_odd[0][r] ? s_row_nan[0][r] : nullptr,
                                     s_post_odd[1][r] ? s_row_nan[1][r] : nullptr};
                 write_row<D>(tO0, s * (D / 2), res, whole ? p.o + at * D : nullptr, whole ? nullptr : p.o_part + at * D, in);
             }
             if (in && s == 0) {
-                const float lse = l == 0.0f ? -INFINITY : (m2 + 4.0f + log2f(l)) * kLn2;
+                const float lse = l == 0.0f ? -INFINITY : (m2 + log2f(l)) * kLn2;
                 if (!whole) {
                     p.lse_part[at] = lse;
                 } else if (p.lse != nullptr) {
