@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kCopyThreads) fa_cache_copy_kernel(const PageC
     const int n = static_cast<int>(rest / p.Hkv), hk = static_cast<int>(rest - static_cast<long long>(n) * p.Hkv);
     if (n >= p.n) return;
     const int src = p.copies[3ll * n], dst = p.copies[3ll * n + 1];
-    const int rows = min(p.copies[3ll * n + 2] - 16 * part, 16);  // of this warp
+    const int rows = min(max(p.copies[3ll * n + 2], 0) - 16 * part, 16);  // of this warp
     if (rows <= 0 || src < 0 || src >= p.src_pages || dst < 0 || dst >= p.dst_pages) return;
     const long long from = ((static_cast<long long>(src) * p.Hkv + hk) << p.page_shift) + 16 * part;
     const long long to = ((static_cast<long long>(dst) * p.Hkv + hk) << p.page_shift) + 16 * part;
