@@ -804,7 +804,7 @@ def pages_update(refs, page_table, seqlens, source, kept, new_lens, page_size: i
     of slot source[b] (itself, another that it forks, -1 for none) with room for new_lens[b] rows.
     refs (entries that name each page, 0: free) and page_table are updated in place.  Returns copies
     (int32 [slots, 3], for ``cache_copy_pages`` on every layer's cache) and counts (int32 [2]: pages
-    missing, in which case nothing was changed, and pages free)."""
+    missing, in which case nothing was changed, and pages free).  Without slots only the free pages are counted."""
     if stream is not None:
         with _on(stream, refs):
             return pages_update(refs, page_table, seqlens, source, kept, new_lens, page_size)

@@ -608,7 +608,7 @@ PyObject* pages_update(Args a)
         counts_new = empty({2}, at::kInt, dev);
         counts = &counts_new;
     }
-    if (!ws) {
+    if (!ws && slots > 0) {
         ws_new = empty({static_cast<int64_t>(bytes_fn(S, M, P))}, at::kByte, dev);
         ws = &ws_new;
     }
@@ -616,8 +616,20 @@ PyObject* pages_update(Args a)
         !copies->is_contiguous())
         value_error("copies must be contiguous int32 [slots, 3]");
     int32s(*counts, "counts", 2);
-    if (!ws->is_contiguous()) value_error("the workspace must be contiguous");
-    for (const at::Tensor* t : {copies, counts, ws}) dev.same(*t);
+    if (ws && !ws->is_contiguous()) value_error("the workspace must be contiguous");
+    for (const at::Tensor* t : {copies, counts}) dev.same(*t);
+    if (ws) dev.same(*ws);
+    if (slots == 0) {
+        // only the free pages to count: the step of one slot that has none and wants none
+        const at::Tensor zero = at::zeros({1}, refs.options()), nobody = at::full({1}, -1, refs.options());
+        const at::Tensor row = empty({1}, at::kInt, dev), copy = empty({1, 3}, at::kInt, dev);
+        const at::Tensor own = empty({static_cast<int64_t>(bytes_fn(1, 1, P))}, at::kByte, dev);
+        const int rc = fn(refs.data_ptr<int>(), row.data_ptr<int>(), zero.data_ptr<int>(), nobody.data_ptr<int>(),
+                          zero.data_ptr<int>(), zero.data_ptr<int>(), copy.data_ptr<int>(), counts->data_ptr<int>(), 1, 1,
+                          P, page, own.data_ptr(), own.nbytes(), raw_stream(dev));
+        if (rc) return PyLong_FromLong(rc);
+        return two(*copies, counts);
+    }
     const int rc = fn(refs.data_ptr<int>(), table.data_ptr<int>(), len.data_ptr<int>(), source.data_ptr<int>(),
                       kept.data_ptr<int>(), next.data_ptr<int>(), copies->data_ptr<int>(), counts->data_ptr<int>(), S,
                       M, P, page, ws->data_ptr(), ws->nbytes(), raw_stream(dev));

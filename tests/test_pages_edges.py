@@ -21,3 +21,19 @@ def test_counts_of_rows_that_are_none(page):
     fa.fa_device_status()
     guard()
     same(cache, want)
+
+
+@gpu
+@pytest.mark.parametrize("room", [0, 5])
+def test_a_step_without_slots(room):
+    """No slots: nothing to copy, and the free pages are counted."""
+    refs = ints([0, 2, 0, 0, 1, 0, 0]).cuda()
+    table, none = torch.zeros(0, room, dtype=torch.int32).cuda(), torch.zeros(0, dtype=torch.int32).cuda()
+    copies, counts = fa.pages_update(refs, table, none, none, none, none, 16)
+    assert copies.shape == (0, 3) and counts.tolist() == [0, 5]
+    out = torch.zeros(0, 3, dtype=torch.int32).cuda(), torch.full((2,), 9, dtype=torch.int32).cuda()
+    fa.fa_pages_update(refs, table, none, none, none, none, 16, *out, torch.zeros(0, dtype=torch.uint8).cuda())
+    fa.fa_device_status()
+    assert out[1].tolist() == [0, 5] and refs.tolist() == [0, 2, 0, 0, 1, 0, 0]
+    with pytest.raises(fa.FaError):
+        fa.pages_update(refs, table, none, none, none, none, 24)
