@@ -1713,6 +1713,9 @@ extern "C" int fa_pages_update(int* refs, int* page_table, const int* seqlens, c
     ws += align256(static_cast<size_t>(num_pages) * 4);
     p.offset = reinterpret_cast<int*>(ws);
     p.shared_last = reinterpret_cast<int*>(ws + align256(n4));
+    const int cut = (g_debug_flags & fa::kDebugShrinkExtents) ? 1 : 0;
+    p.refs_ext = num_pages - cut; p.table_ext = static_cast<long long>(slots - cut) * max_pages; p.slot_ext = slots - cut;
+    p.status = di->status;
     cudaError_t e = fa::launch_pages_update(p, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail(e, "pages update launch");
     return FA_OK;

@@ -255,6 +255,28 @@ __device__ __forceinline__ Slot slot_at(const PagesParams& p, int b)
 
 __device__ __forceinline__ bool is_page(const PagesParams& p, int id) { return id >= 0 && id < p.num_pages; }
 
+// Element i of a tensor of `extent` ints (checked builds; -1 past it).
+__device__ __forceinline__ int int_at(const PagesParams& p, const int* t, long long i, long long extent)
+{
+    return in_extent(i, 1, extent, p.status) ? t[i] : -1;
+}
+__device__ __forceinline__ void put_int(const PagesParams& p, int* t, long long i, long long extent, int v)
+{
+    if (in_extent(i, 1, extent, p.status)) t[i] = v;
+}
+// A page's count and v.
+__device__ __forceinline__ void add_ref(const PagesParams& p, int id, int v)
+{
+    if (is_page(p, id) && in_extent(id, 1, p.refs_ext, p.status)) atomicAdd(p.refs + id, v);
+}
+__device__ __forceinline__ void put_copy(const PagesParams& p, int b, int from, int to, int rows)
+{
+    if (!in_extent(b, 1, p.slot_ext, p.status)) return;
+    p.copies[3ll * b] = from;
+    p.copies[3ll * b + 1] = to;
+    p.copies[3ll * b + 2] = rows;
+}
+
 // The block's sum of v, in all threads; s_part: 32 words, free again after the next __syncthreads.
 __device__ __forceinline__ unsigned block_sum(unsigned v, unsigned* s_part)
 {
@@ -311,7 +333,7 @@ __global__ void __launch_bounds__(kPagesThreads) fa_pages_update_kernel(const Pa
     };
     // its last kept page, if the slot writes on in it (the table stands until step 4)
     auto last_of = [&](const Slot& s) {
-        return s.part ? p.table[static_cast<long long>(s.source) * M + s.p_kept - 1] : -1;
+        return s.part ? int_at(p, p.table, static_cast<long long>(s.source) * M + s.p_kept - 1, p.table_ext) : -1;
     };
     const int first_last = last_of(first);
     // All threads over all of the batch's `all` entries, four at once; find(e, k): the slot (of the batch) that has
@@ -355,17 +377,17 @@ __global__ void __launch_bounds__(kPagesThreads) fa_pages_update_kernel(const Pa
                     const long long row = static_cast<long long>(c0 + i) * M;
                     if (k < static_cast<unsigned>(w.y)) {
                         delta[u] = -sign;
-                        id[u] = p.table[row + w.x + k];
+                        id[u] = int_at(p, p.table, row + w.x + k, p.table_ext);
                     } else {
                         delta[u] = sign;
-                        id[u] = p.table[static_cast<long long>(w.z) * M + (k - w.y)];
-                        stage[u] = p.stage + row + (k - w.y);
+                        id[u] = int_at(p, p.table, static_cast<long long>(w.z) * M + (k - w.y), p.table_ext);
+                        if (in_extent(row + (k - w.y), 1, p.table_ext, p.status)) stage[u] = p.stage + row + (k - w.y);
                     }
                 }
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
                     if (stage[u] != nullptr) *stage[u] = id[u];
-                    if (is_page(p, id[u])) atomicAdd(p.refs + id[u], delta[u]);
+                    add_ref(p, id[u], delta[u]);
                 }
             }
             __syncthreads();
@@ -408,15 +430,15 @@ __global__ void __launch_bounds__(kPagesThreads) fa_pages_update_kernel(const Pa
         int need = s.p_new - s.p_kept, last = -1;
         if (s.part) {
             last = c0 == b0 ? first_last : last_of(s);
-            if (!is_page(p, last) || __ldcg(p.refs + last) < 2) last = -1;
+            if (!is_page(p, last) || !in_extent(last, 1, p.refs_ext, p.status) || __ldcg(p.refs + last) < 2) last = -1;
             need += last >= 0;
         }
         // places of the fresh pages among this CTA's
         unsigned all;
         const unsigned before = block_before(need, s_part, all);
         if (tid < batch && b < b1) {
-            p.offset[b] = need_all + before;
-            p.shared_last[b] = last;
+            put_int(p, p.offset, b, p.slot_ext, need_all + before);
+            put_int(p, p.shared_last, b, p.slot_ext, last);
         }
         need_all += all;
         __syncthreads();
@@ -446,10 +468,7 @@ __global__ void __launch_bounds__(kPagesThreads) fa_pages_update_kernel(const Pa
     }
     if (need_total > free_total) {
         count_entries(-1);
-        for (int b = b0 + tid; b < b1; b += kPagesThreads) {
-            p.copies[3ll * b] = p.copies[3ll * b + 1] = -1;
-            p.copies[3ll * b + 2] = 0;
-        }
+        for (int b = b0 + tid; b < b1; b += kPagesThreads) put_copy(p, b, -1, -1, 0);
         cluster_sync();
         const int left = count_free();
         const int f = block_sum(lane == 0 ? left : 0, s_part);
@@ -479,8 +498,8 @@ __global__ void __launch_bounds__(kPagesThreads) fa_pages_update_kernel(const Pa
                 const unsigned here = __ballot_sync(0xffffffffu, r[u] == 0);
                 const int to = at + __popc(here & ((1u << lane) - 1));
                 if (r[u] == 0 && to < need_total) {
-                    p.fresh[to] = i0 + 32 * u;
-                    p.refs[i0 + 32 * u] = 1;
+                    put_int(p, p.fresh, to, p.refs_ext, i0 + 32 * u);
+                    put_int(p, p.refs, i0 + 32 * u, p.refs_ext, 1);
                 }
                 at += __popc(here);
             }
@@ -500,13 +519,11 @@ __global__ void __launch_bounds__(kPagesThreads) fa_pages_update_kernel(const Pa
         int last = -1, fresh = 0, from = 0;
         unsigned n = 0;
         if (tid < batch && b < b1) {
-            last = p.shared_last[b];
-            fresh = need_before + p.offset[b];
-            const int page = last >= 0 ? __ldcg(p.fresh + fresh) : -1;
-            if (last >= 0) atomicAdd(p.refs + last, -1);
-            p.copies[3ll * b] = last;
-            p.copies[3ll * b + 1] = page;
-            p.copies[3ll * b + 2] = last >= 0 ? s.part : 0;
+            last = int_at(p, p.shared_last, b, p.slot_ext);
+            fresh = need_before + int_at(p, p.offset, b, p.slot_ext);
+            const int page = last >= 0 && in_extent(fresh, 1, p.refs_ext, p.status) ? __ldcg(p.fresh + fresh) : -1;
+            if (last >= 0) add_ref(p, last, -1);
+            put_copy(p, b, last, page, last >= 0 ? s.part : 0);
             from = s.own ? s.p_kept - (last >= 0) : 0;
             n = max(max(s.p_new, s.p_old) - from, 0);
         }
@@ -531,10 +548,11 @@ __global__ void __launch_bounds__(kPagesThreads) fa_pages_update_kernel(const Pa
                 const int4 w = s_slot[i];
                 const int at = w.x + static_cast<int>(k);
                 const long long row = static_cast<long long>(c0 + i) * M + at;
+                if (!in_extent(row, 1, p.table_ext, p.status)) continue;
                 to[u] = p.table + row;
                 if (at < w.y)
                     id[u] = p.stage[row];
-                else if (at < w.z)
+                else if (at < w.z && in_extent(w.w + static_cast<long long>(at - w.y), 1, p.refs_ext, p.status))
                     id[u] = __ldcg(p.fresh + w.w + (at - w.y));
             }
 #pragma unroll

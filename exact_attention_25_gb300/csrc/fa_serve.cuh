@@ -222,6 +222,8 @@ struct PagesParams {
     int* shared_last;          // workspace [slots]: the page that its last one is a copy of, or -1
     int slots, max_pages, num_pages, page_shift;
     int cluster;
+    long long refs_ext, table_ext, slot_ext;  // checked builds: of refs and fresh, of table and stage, of what goes by slot
+    int* status;
 };
 
 // Decode with shared prefixes: the same kind of line, over the groups' prefixes and then the

@@ -4,7 +4,9 @@ import pytest
 import torch
 
 import exact_attention_25_gb300 as fa
+from exact_attention_25_gb300 import _lib
 from tests.test_pages import copied, host, ints, random_pages, same
+from tests.test_serve_edges import checked  # noqa: F401 (a fixture)
 
 gpu = pytest.mark.gpu
 
@@ -37,3 +39,49 @@ def test_a_step_without_slots(room):
     assert out[1].tolist() == [0, 5] and refs.tolist() == [0, 2, 0, 0, 1, 0, 0]
     with pytest.raises(fa.FaError):
         fa.pages_update(refs, table, none, none, none, none, 24)
+
+
+# ------------------------------------------------------------------------------ checked library
+
+def pages_steps(slots=70, num_pages=600, most=12, page=16):
+    """Steps in which sequences begin, fork, write on in shared pages, are trimmed and end, the last one with too few pages;
+    what each leaves."""
+    refs = torch.zeros(num_pages, dtype=torch.int32).cuda()
+    table = torch.full((slots, most), -1, dtype=torch.int32).cuda()
+    r, lens, out = np.random.RandomState(1), np.zeros(slots, np.int64), []
+    for step in range(4):
+        source = np.where(r.rand(slots) < 0.4, r.randint(-1, slots, slots), np.arange(slots))
+        kept = np.where(source < 0, 0, np.maximum(lens[source] - r.randint(0, 9, slots), 0))
+        new = np.minimum(kept + r.randint(0, 60, slots), most * page) if step < 3 else np.full(slots, most * page)
+        copies, counts = fa.pages_update(refs, table, *(ints(x).cuda() for x in (lens, source, kept, new)), page)
+        out += [copies, counts, refs.clone(), table.clone()]
+        if step < 3:
+            lens = new
+    return out
+
+
+@gpu
+def test_checked_library_gives_the_same_pages(checked):  # noqa: F811
+    with _lib.library(_lib.LIB_PATH):
+        want = pages_steps()
+        fa.fa_device_status()
+    assert [c[0].item() > 0 for c in want[1::4]] == [False, False, False, True]
+    with _lib.library(checked):
+        got = pages_steps()
+        fa.fa_device_status()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@gpu
+def test_checked_library_catches_shrunk_extents_of_pages(checked):  # noqa: F811
+    with _lib.library(checked) as lib:
+        lib.fa_debug_set_flags(2)  # every extent one row short
+        try:
+            pages_steps()
+            with pytest.raises(fa.FaError) as e:
+                fa.fa_device_status()
+            assert e.value.code == -9
+        finally:
+            lib.fa_debug_set_flags(0)
+        pages_steps()
+        fa.fa_device_status()
