@@ -40,7 +40,7 @@ cudaError_t launch_decode_cache(int d, const CUtensorMap& tk, const CUtensorMap&
                                 const CacheDecodeParams& p, cudaStream_t st);
 cudaError_t launch_cache_copy(int d, const PageCopyParams& p, cudaStream_t st);
 cudaError_t launch_cache_compact(int d, const CompactParams& p, cudaStream_t st, int num_sms);
-cudaError_t launch_pages_update(PagesParams p, cudaStream_t st);
+cudaError_t launch_pages_update(PagesParams p, cudaStream_t st, int debug_flags);
 cudaError_t launch_tree_mask(const TreeMaskParams& p, cudaStream_t st);
 cudaError_t launch_decode_tree(int d, const TreeDecodeParams& p, cudaStream_t st);
 cudaError_t launch_decode_shared(int d, const CUtensorMap* maps, const SharedDecodeParams& p,
@@ -1716,7 +1716,7 @@ extern "C" int fa_pages_update(int* refs, int* page_table, const int* seqlens, c
     const int cut = (g_debug_flags & fa::kDebugShrinkExtents) ? 1 : 0;
     p.refs_ext = num_pages - cut; p.table_ext = static_cast<long long>(slots - cut) * max_pages; p.slot_ext = slots - cut;
     p.status = di->status;
-    cudaError_t e = fa::launch_pages_update(p, static_cast<cudaStream_t>(stream));
+    cudaError_t e = fa::launch_pages_update(p, static_cast<cudaStream_t>(stream), g_debug_flags);
     if (e != cudaSuccess) return cuda_fail(e, "pages update launch");
     return FA_OK;
 }

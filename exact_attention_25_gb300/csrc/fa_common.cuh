@@ -42,6 +42,8 @@ constexpr int kDebugDropFirstLoad = 1;
 // Test hook of checked builds: the host passes every buffer extent one row short, so the
 // bounds checks must catch (and skip) the last row's accesses.
 constexpr int kDebugShrinkExtents = 2;
+// Test hook (fa_debug_set_flags): the bookkeeping of pages as on a device that holds no clusters beyond the portable 8.
+constexpr int kDebugPortableClusters = 4;
 
 // Status word value of a failed bounds check (checked builds); wait sites are below 64.
 constexpr int kStatusOutOfBounds = 0x0B0B;

@@ -608,21 +608,38 @@ cudaError_t launch_cache_compact(int d, const CompactParams& p, cudaStream_t st,
     return d == 64 ? launch_compact<64>(p, st, num_sms) : launch_compact<128>(p, st, num_sms);
 }
 
-cudaError_t launch_pages_update(PagesParams p, cudaStream_t st)
+cudaError_t launch_pages_update(PagesParams p, cudaStream_t st, int debug_flags)
 {
-    // one CTA for every 8 K pages or 16 slots, up to the 16 of the largest cluster (256 beams: 18.5 us in replays; with a CTA for
+    // the largest cluster that the device holds (0: not asked yet): 16 CTAs need as many SMs of one GPC, 8 are always there
+    static int largest[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    int most = dev < 64 ? largest[dev] : 0;
+    if (most == 0) {
+        cudaError_t e = cudaFuncSetAttribute(fa_pages_update_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 16;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.gridDim = dim3(16);
+        cfg.blockDim = dim3(kPagesThreads);
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        e = cudaOccupancyMaxActiveClusters(&n, fa_pages_update_kernel, &cfg);
+        if (e != cudaSuccess) cudaGetLastError();  // (as if there were none)
+        most = e == cudaSuccess && n > 0 ? 16 : 8;
+        if (dev < 64) largest[dev] = most;
+    }
+    if (debug_flags & kDebugPortableClusters) most = 8;
+    // one CTA for every 8 K pages or 16 slots, up to the largest cluster (256 beams: 18.5 us in replays; with a CTA for
     // every 64 slots 22.6, for every 8 the same, but 64 slots 12.3 in place of 10.4.
     // 16 slots of a pool of 60 K pages: 10.4 us, a CTA for every 2 K or 32 K pages 12.4)
     p.cluster = 1;
-    while (p.cluster < 16 && (p.num_pages > p.cluster * 8192 || p.slots > p.cluster * 16)) p.cluster *= 2;
-    static bool attr_set[64] = {};
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 64 && !attr_set[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(fa_pages_update_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-        attr_set[dev] = true;
-    }
+    while (p.cluster < most && (p.num_pages > p.cluster * 8192 || p.slots > p.cluster * 16)) p.cluster *= 2;
     return launch_cluster(fa_pages_update_kernel, p.cluster, dim3(p.cluster), dim3(kPagesThreads), 0, st, p);
 }
 

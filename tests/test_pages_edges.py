@@ -85,3 +85,19 @@ def test_checked_library_catches_shrunk_extents_of_pages(checked):  # noqa: F811
             lib.fa_debug_set_flags(0)
         pages_steps()
         fa.fa_device_status()
+
+
+# ------------------------------------------------------------------------------ devices, sizes
+
+@gpu
+def test_clusters_of_eight_give_the_same_pages():
+    """A device that holds no 16 CTAs in a cluster (a test hook) takes 8 for the same result."""
+    lib = fa.load()
+    want = pages_steps(500, 70000, 40)
+    lib.fa_debug_set_flags(4)
+    try:
+        got = pages_steps(500, 70000, 40)
+    finally:
+        lib.fa_debug_set_flags(0)
+    fa.fa_device_status()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
