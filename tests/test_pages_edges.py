@@ -5,7 +5,7 @@ import torch
 
 import exact_attention_25_gb300 as fa
 from exact_attention_25_gb300 import _lib
-from tests.test_pages import copied, host, ints, random_pages, same
+from tests.test_pages import Pool, copied, host, ints, lists_of, pages, random_pages, run_compact, same, updated
 from tests.test_serve_edges import checked  # noqa: F401 (a fixture)
 
 gpu = pytest.mark.gpu
@@ -101,3 +101,59 @@ def test_clusters_of_eight_give_the_same_pages():
         lib.fa_debug_set_flags(0)
     fa.fa_device_status()
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@gpu
+@pytest.mark.parametrize("share", [0.3, 0.9])
+@pytest.mark.parametrize("B, rows, Hkv", [(1, 9000, 1), (2, 5000, 2), (1, 1300, 8), (40, 600, 8)])
+def test_long_lists_of_short_rows(B, rows, Hkv, share):
+    """Rows of 64: several steps to a sequence, with one thread block each and with several that wait for one another."""
+    n = [rows - 7 * b for b in range(B)]
+    run_compact(n, lists_of(n, share, B), [3 * b for b in range(B)], Hkv, 64, 64, 5)
+
+
+@gpu
+def test_more_slots_than_a_cluster_takes_at_once():
+    """20000 slots, 1250 to a thread block, which takes 1024 at once."""
+    slots, page, most = 20000, 16, 80
+    r = np.random.RandomState(3)
+    pool = Pool(60000, slots, pages(most, page), page)
+    for step in range(4):
+        source = np.arange(slots)
+        move = r.rand(slots)
+        source[move < 0.3] = r.randint(0, slots, (move < 0.3).sum())
+        source[move < 0.1] = -1
+        kept = [0 if s < 0 else max(pool.lens[s] - int(r.choice([0, 0, 1, 3, 20])), 0) for s in source]
+        grow = most if step == 2 else 25
+        new = [min(k + int(r.choice([0, 1, 5, grow])), most) for k in kept]
+        if step == 2:
+            new = [most] * slots  # 100000 pages
+        counts, copies = pool.step(source.tolist(), kept, new)
+        assert (counts[0] > 0) == (step == 2)
+        assert step != 1 or (copies[:, 0] >= 0).sum() > 1000
+
+
+@gpu
+@pytest.mark.parametrize("short", [False, True])
+def test_rows_of_a_table_wider_than_a_batch(short):
+    """12 slots of 2^27 entries, of which 8 are taken at once; entries beyond 2^31 bytes; the far ones stay as they are."""
+    slots, M, page, num = 12, 2 ** 27, 16, 400
+    table = torch.full((slots, M), -1, dtype=torch.int32, device="cuda")
+    table[:, 64:] = -7
+    refs = torch.zeros(num, dtype=torch.int32).cuda()
+    r = np.random.RandomState(2)
+    lens, t, c = [0] * slots, np.full((slots, 64), -1), np.zeros(num, np.int64)
+    for step in range(3):
+        source = np.where(r.rand(slots) < 0.5, r.randint(-1, slots, slots), np.arange(slots)).tolist()
+        kept = [0 if s < 0 else max(lens[s] - int(r.randint(0, 20)), 0) for s in source]
+        new = [k + int(r.randint(0, 150)) for k in kept]
+        if short and step == 2:
+            new = [900] * slots
+        got = fa.pages_update(refs, table, *(ints(x).cuda() for x in (lens, source, kept, new)), page)
+        fa.fa_device_status()
+        c, t, copies, counts = updated(c, t, lens, source, kept, new, page)
+        assert got[1].tolist() == counts and (got[0].cpu().numpy() == copies).all()
+        assert (table[:, :64].cpu().numpy() == t).all() and (refs.cpu().numpy() == c).all()
+        assert (counts[0] > 0) == (short and step == 2)
+        lens = lens if counts[0] else new
+    assert (table[:, 64:] == -7).all()
