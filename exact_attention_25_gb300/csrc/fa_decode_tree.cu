@@ -885,8 +885,10 @@ __global__ void __launch_bounds__(TreeCfg<D>::THREADS, 1) fa_decode_tree_kernel(
                 const int klow = static_cast<int>(__reduce_min_sync(0xffffffffu, min_byte(kw | ~in)));
                 const int vlow = static_cast<int>(__reduce_min_sync(0xffffffffu, min_byte(vw | ~vin)));
                 const bool kany = __any_sync(0xffffffffu, in != 0), vany = __any_sync(0xffffffffu, vin != 0);
+                // (some rows of zeros: with the others' exponent their weights could outgrow the others')
+                const bool some_zero = __any_sync(0xffffffffu, vin != in);
                 const bool far = (kany && (ktop > kHigh || klow < kLow || ktop - klow > kSpreadK)) ||
-                                 (vany && (vtop > kHigh || vlow < kLow || vtop - vlow > kSpreadV));
+                                 (vany && (vtop > kHigh || vlow < kLow || vtop - vlow > kSpreadV || some_zero));
                 if (!kany) ktop = 127;
                 if (!vany) vtop = kZero;
                 if (far || !whole) {

@@ -158,3 +158,22 @@ def test_the_sum_does_not_depend_on_the_values(d):
         want = fa.forward_decode_cache(q.cuda(), to_cache(codes, exps), cu([nq]).cuda(), ints([nk]).cuda(), table.cuda(),
                                        nq, nk, 0.1, True)[1]
         assert (got - want).abs().max() < 2e-5, pattern
+
+
+@gpu
+@pytest.mark.parametrize("ctas", [1, 3])
+@pytest.mark.parametrize("e", [-90, 0, 86])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rows_of_zeros_that_weigh_the_most(d, e, ctas):
+    """Keys 2^50 times the others' weight whose value rows are zeros lie among the others: those keep their bits."""
+    nk, nq, page = 500, 4, 32
+    table, pool = table_for([nk], page, 0, 1)
+    codes, exps = random_cache(pool, 1, page, d, 1)
+    codes[1] &= 0xBF
+    exps[0], exps[1] = 121, 127 + e
+    zero = np.random.RandomState(2).rand(*exps[1].shape) < 0.2
+    codes[0][zero], exps[0][zero], codes[1][zero], exps[1][zero] = 0x38, 127, 0, 127
+    plain = exps.copy()
+    plain[1][zero] = 1
+    q, mask = torch.ones(nq, 2, d).bfloat16(), words_of(ancestors([-1, 0, 0, 1]), 1)
+    check((q, codes, exps, mask, nq, nk, table), (codes, plain, page), ctas, 50 * float(np.log(2.0)) / d)
