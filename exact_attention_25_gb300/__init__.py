@@ -688,7 +688,8 @@ def fa_tree_mask(parents, mask, cu_seqlens_q, max_seqlen_q: int, stream=None) ->
 
 def tree_mask(parents, cu_seqlens_q, max_seqlen_q: int, stream=None):
     """Allocate and return the mask rows of trees given by their tokens' parents: bit j of a
-    token's row is set for the token itself and its ancestors."""
+    token's row is set for the token itself and its ancestors.  Rows that belong to no sequence are
+    not written and hold anything, as in the decodes' outputs."""
     if stream is not None:
         with _on(stream, parents):
             return tree_mask(parents, cu_seqlens_q, max_seqlen_q)

@@ -1,9 +1,9 @@
 // Attention of trees of drafted tokens over the paged e4m3 cache: O = softmax(scale Q K^T + mask) V
 // for the bf16 queries of a sequence's drafted tokens, where every token sees the sequence's history
 // and, of the drafted keys, those that its row of mask bits names (its ancestors and itself).  K and V
-// are the cache's codes times their rows' powers of two.  Nothing is rounded on the way in: the
-// result is exact attention on the cached values up to fp32 accumulation and the f16 rounding of the
-// softmax weights.
+// are the cache's codes times their rows' powers of two, which are not rounded on the way in.  Q becomes f16
+// under a power of two a row, exactly down to 2^-31 of the row's largest (down to 2^-38 something is left).  The result
+// is exact attention on those up to fp32 accumulation and the f16 rounding of the softmax weights.
 //
 // A tree has tens of tokens, so a key/value head has 32 to 256 query rows and more: too many for the
 // cache decode's products in registers (64 rows read every code four times from shared memory), but
@@ -12,7 +12,7 @@
 //
 // Work is cut as in the cache decode: a line of units (sequence, up to 128 query rows r = i * G + g, i
 // the token and g the head of the G that share the K/V head), shared out evenly over one CTA an SM, the
-// parts of a unit that several shares cut merged by a second kernel.  (Units of two tiles of 128 rows, which converted
+// parts of a unit that several shares cut merged by a second kernel.  (Before the steps below were made faster: units of two tiles of 128 rows, which converted
 // the codes once for both, were slower: 64 tokens in 249 us where these took 240.  With P over S, for want of room in
 // TMEM, a stream's next scores waited for its product.)
 //
@@ -1160,7 +1160,8 @@ __global__ void __launch_bounds__(kMergeThreads) fa_decode_tree_merge_kernel(con
 
 // Rows of ancestors' bits from parents: a warp for each token, lane w holding word w of its row, walks up
 // the tree.  A walk has at most as many steps as the sequence has tokens, so a circle of parents ends it too.
-// (8 trees of 24 tokens 3 us, nearly all of it launch and reads.)
+// (In replays 8 trees of 24 tokens 1.9 us, nearly all of it launch and reads, chains of 64 tokens 2.7.  A chain of 1024 is
+// as many dependent reads of shared memory: 28 us, eight of them 76.)
 constexpr int kMaskWarps = 8;
 constexpr int kMaskTokens = 1024;  // the longest tree
 

@@ -107,8 +107,9 @@ __global__ void __launch_bounds__(kCopyThreads) fa_cache_copy_kernel(const PageC
 // Every thread copies its own 16 bytes of its rows in and out again, so that memory needs no barrier of its own.
 //
 // Bound by HBM (each moved row read and written once): 8 sequences that keep 24 K of 32 K rows and less, 8 heads,
-// d = 128, 102 us, 5.4 TB/s.  What that takes is many rows under way: with the rows in registers and one step ahead 247 us,
-// with the ring but the table's entries looked up when needed 113.  A CTA's step of 64 rows by 128 threads, three stages, seven
+// d = 128, 109 us, 5.1 TB/s (102 on the same rows again and again, as the figures that follow).  What that takes is many rows
+// under way: with the rows in registers and one step ahead 247 us, with the ring but the table's entries looked up when
+// needed 113.  A CTA's step of 64 rows by 128 threads, three stages, seven
 // CTAs an SM; four stages 106 us, five 122; 128 rows by 256 threads 104 (and 40 rows 8.4 us, here 6.2); writes a step later
 // than the barrier's arrival, so that nobody waits there, the same.
 template <int D, int THREADS, int U, int S>
@@ -216,7 +217,8 @@ __global__ void __launch_bounds__(THREADS) fa_cache_compact_kernel(const Compact
 //
 // A few microseconds of latencies: a scan of refs, a table entry for each page that changes hands, and the
 // order of the steps below, each of which needs all of the one before.  So one cluster does it,
-// with a hardware barrier (some 0.3 us) between the steps, where a grid would need a launch each.  A CTA's threads
+// with a hardware barrier (some 0.3 us) between the steps, where a grid would need a launch each, 1 to 2 us.  (For pools of a
+// million pages that would pay; it was not built.)  A CTA's threads
 // share out all entries of its slots, found by a search in the slots' sums: with a warp to a slot the longest
 // ones of 1024 slots (10 of 100 replaced, pages of 16 of up to 32 K tokens, 1.1 M pages) kept the others waiting, 85 us in
 // place of 44; now 35, of which 11 for the fresh pages (9 K sectors of counts written by each SM), 9 and 7 for the
@@ -595,8 +597,8 @@ static cudaError_t launch_compact(const CompactParams& p, cudaStream_t st, int n
     // large steps 8.4; up to 225 rows 6.3, in the small steps 18.5)
     constexpr int kFew = 128 / (D / 16), kMany = 4 * 128 / (D / 16);
     if (p.max_keep <= kFew) return launch_compact_as<D, 128, 1, 2>(p, st, 1);
-    // as many CTAs to a cluster as the SMs hold at once, and have rows (8 sequences of up to 24 K rows kept: 102 us;
-    // one CTA each 238)
+    // as many CTAs to a cluster as the SMs hold at once, and have rows (8 sequences of up to 24 K rows kept, the
+    // same ones again and again: 102 us; one CTA each 238)
     const long long units = 2ll * p.B * p.Hkv;
     int cluster = 1;
     while (cluster < 8 && 2 * units * cluster <= 8 * num_sms && p.max_keep > cluster * kMany) cluster *= 2;

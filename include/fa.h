@@ -497,10 +497,10 @@ int fa_cache_copy_pages(const void* src_k, const void* src_v, const void* src_k_
 /* Keeps some rows of each sequence and moves them together, in place: position start[b] + i becomes what
  * position start[b] + keep[cu_keep[b] + i] was (the path accepted of a drafted tree; a history without
  * the rows that are dropped).  keep: device int32 [total_keep], the lists of the sequences back to back
- * (cu_keep, device int32 [B + 1]; what lies behind the last is not read), each rising, from 0 on, none longer
- * than max_keep; start: device int32 [B].  Rows behind the last kept one stay as they are; positions whose
+ * (cu_keep, device int32 [B + 1]; what lies behind the last is not read), each rising (every entry above the one
+ * before), from 0 on, none longer than max_keep; start: device int32 [B].  Rows behind the last kept one stay as they are; positions whose
  * page is missing are left out.  Every page that is written belongs to one sequence.  A list that does not rise
- * gives rows of the sequence in no particular order. */
+ * leaves the sequence's rows from start[b] on undefined, and others as they are. */
 int fa_cache_compact(void* k_cache, void* v_cache, void* k_exp, void* v_exp, const int* keep,
                      const int* cu_keep, const int* start, const int* page_table, int B,
                      int max_keep, int total_keep, int max_pages, int num_pages, int page_size,
